@@ -2,7 +2,10 @@
 
 ``libptored.so`` (HIP, gfx950) computes dst = src_0 (+) ... (+) src_{N-1}
 over a valid rectangle of N equally shaped buffers; ``binding`` exposes its
-C ABI to Python and ``workloads`` draws seeded synthetic inputs.
+C ABI to Python and ``workloads`` draws seeded synthetic inputs.  ``block``
+holds what follows the reduction in a tensor-parallel model: the block
+boundary's norms, gate and residual with their gradients, and activations
+kept in 8 bits.
 """
 
 from .binding import (  # noqa: F401
@@ -26,4 +29,22 @@ from .binding import (  # noqa: F401
     ring_bounds,
     treduce,
     tuning,
+)
+from .block import (  # noqa: F401
+    Checkpoint,
+    block_norm,
+    block_norm_backward,
+    block_norm_backward_workspace,
+    checkpoint_empty,
+    checkpoint_pack,
+    checkpoint_unpack,
+    checkpoint_wgrad,
+    checkpoint_wgrad_workspace,
+    ptored_block_norm,
+    ptored_block_norm_backward,
+    ptored_block_norm_backward_workspace,
+    ptored_checkpoint_pack,
+    ptored_checkpoint_unpack,
+    ptored_checkpoint_wgrad,
+    ptored_checkpoint_wgrad_workspace,
 )

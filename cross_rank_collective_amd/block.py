@@ -1,0 +1,472 @@
+"""The block boundary after a cross-rank reduction, and 8-bit activation
+checkpoints: ctypes binding and tensor-level calls (``include/ptored_block.h``).
+
+A tensor-parallel block ends with N ranks' partial outputs.  ``block_norm``
+folds them, normalises, gates and scales the fold, adds it to the residual
+stream and normalises the result for the next block, in one pass over the
+data; ``block_norm_backward`` takes its gradients.  ``checkpoint_pack`` keeps
+an activation in 8 bits (32 elements of a row share a power of two),
+``checkpoint_unpack`` reads it back, and the backward pass and
+``checkpoint_wgrad`` (a projection's weight gradient) take it as it is.
+
+As in ``binding``, every step runs in the library's HIP kernels: these
+functions check tensors, hand over pointers and raise on errors.  Outputs are
+the caller's tensors; nothing is allocated but, where none is given, the
+workspace of a backward pass (from torch's allocator, on the call's stream).
+Calls are asynchronous on ``stream`` (default: torch's current stream).  A
+caller that uses tensors on another stream than the one they were allocated on
+keeps them alive until that stream is done, as with every torch call.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+from . import binding as B
+
+PTORED_BLOCK_MAX_COLS = 16384
+PTORED_CHECKPOINT_BLOCK = 32
+
+_vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class ptored_rows(ctypes.Structure):
+    _fields_ = [("data", _vp), ("ld", _i64)]
+
+
+class ptored_checkpoint(ctypes.Structure):
+    _fields_ = [("q", _vp), ("q_ld", _i64), ("scales", _vp), ("scales_ld", _i64)]
+
+
+class ptored_block_params(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("post_weight", _vp), ("pre_weight", _vp),
+                ("gate", ptored_rows), ("gate_rows", _i64), ("weight_offset", _f32),
+                ("branch_scale", _f32), ("residual_scale", _f32), ("eps", _f32),
+                ("dtype", _i32), ("weight_dtype", _i32)]
+
+
+class ptored_block_io(ctypes.Structure):
+    _fields_ = [("x", ptored_rows), ("x_out", ptored_rows), ("z", ptored_rows),
+                ("h", ptored_rows), ("post_rstd", _vp), ("pre_rstd", _vp),
+                ("h_kept", ptored_checkpoint), ("x_kept", ptored_checkpoint),
+                ("z_kept", ptored_checkpoint)]
+
+
+class ptored_block_grad_io(ctypes.Structure):
+    _fields_ = [("dz", ptored_rows), ("dx_out", ptored_rows), ("x_out", ptored_rows),
+                ("h", ptored_rows), ("x_kept", ptored_checkpoint),
+                ("h_kept", ptored_checkpoint), ("post_rstd", _vp), ("pre_rstd", _vp),
+                ("dx", ptored_rows), ("dh", ptored_rows), ("dgate", ptored_rows),
+                ("dpost_weight", _vp), ("dpre_weight", _vp), ("workspace", _vp),
+                ("workspace_bytes", _i64)]
+
+
+class Checkpoint(NamedTuple):
+    """A T x D activation in 8 bits: ``q`` int8 [T, D] and ``scales`` uint8
+    [T, ceil(D / 32)].  Any pair of such tensors serves as one."""
+
+    q: "torch.Tensor"  # noqa: F821
+    scales: "torch.Tensor"  # noqa: F821
+
+
+_lib = None
+
+
+def _load() -> ctypes.CDLL:
+    global _lib
+    if _lib is None:
+        lib = B.load()
+        P = ctypes.POINTER
+        lib.ptored_block_norm.argtypes = [P(_vp), ctypes.c_int, _i64, P(ptored_block_params),
+                                          P(ptored_block_io), _vp]
+        lib.ptored_block_norm_backward.argtypes = [P(ptored_block_params),
+                                                   P(ptored_block_grad_io), _vp]
+        lib.ptored_block_norm_backward_workspace.argtypes = [_i64, _i64, _i64, P(_i64)]
+        lib.ptored_checkpoint_pack.argtypes = [ptored_rows, _i64, _i64, ctypes.c_int,
+                                               ptored_checkpoint, _vp]
+        lib.ptored_checkpoint_unpack.argtypes = [ptored_checkpoint, _i64, _i64, ctypes.c_int,
+                                                 ptored_rows, _vp]
+        lib.ptored_checkpoint_wgrad.argtypes = [ptored_rows, ptored_checkpoint, _i64, _i64, _i64,
+                                                ctypes.c_int, ptored_rows, ctypes.c_int,
+                                                ctypes.c_int, _vp, _i64, _vp]
+        lib.ptored_checkpoint_wgrad_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, P(_i64)]
+        for name in ("ptored_block_norm", "ptored_block_norm_backward",
+                     "ptored_block_norm_backward_workspace", "ptored_checkpoint_pack",
+                     "ptored_checkpoint_unpack", "ptored_checkpoint_wgrad",
+                     "ptored_checkpoint_wgrad_workspace"):
+            getattr(lib, name).restype = ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+# ---------------------------------------------------------------- raw calls
+
+def ptored_block_norm(parts, nranks: int, part_ld: int, params: ptored_block_params,
+                      io: ptored_block_io, stream: int) -> int:
+    """Raw call: ``parts`` are device pointers as ints; returns the status code."""
+    return _load().ptored_block_norm(B._ptrs(parts), nranks, part_ld, params, io, stream)
+
+
+def ptored_block_norm_backward(params: ptored_block_params, io: ptored_block_grad_io,
+                               stream: int) -> int:
+    return _load().ptored_block_norm_backward(params, io, stream)
+
+
+def ptored_block_norm_backward_workspace(rows: int, cols: int, gate_rows: int):
+    out = _i64()
+    st = _load().ptored_block_norm_backward_workspace(rows, cols, gate_rows, out)
+    return st, out.value
+
+
+def ptored_checkpoint_pack(x: ptored_rows, rows: int, cols: int, dtype: int,
+                           kept: ptored_checkpoint, stream: int) -> int:
+    return _load().ptored_checkpoint_pack(x, rows, cols, dtype, kept, stream)
+
+
+def ptored_checkpoint_unpack(kept: ptored_checkpoint, rows: int, cols: int, dtype: int,
+                             out: ptored_rows, stream: int) -> int:
+    return _load().ptored_checkpoint_unpack(kept, rows, cols, dtype, out, stream)
+
+
+def ptored_checkpoint_wgrad(dy: ptored_rows, x: ptored_checkpoint, rows: int, outs: int, cols: int,
+                            dtype: int, dw: ptored_rows, dw_dtype: int, accumulate: int,
+                            workspace: int, workspace_bytes: int, stream: int) -> int:
+    return _load().ptored_checkpoint_wgrad(dy, x, rows, outs, cols, dtype, dw, dw_dtype,
+                                           accumulate, workspace, workspace_bytes, stream)
+
+
+def ptored_checkpoint_wgrad_workspace(rows: int, outs: int, cols: int, dtype: int):
+    out = _i64()
+    st = _load().ptored_checkpoint_wgrad_workspace(rows, outs, cols, dtype, out)
+    return st, out.value
+
+
+# ---------------------------------------------------------------- tensors
+
+def _is_kept(v) -> bool:
+    return isinstance(v, (tuple, list))
+
+
+_NO_ROWS = ptored_rows()
+_NO_KEPT = ptored_checkpoint()
+_FLOATS = {}  # torch dtype -> C ABI code, filled on first use
+
+
+def _float_code(dtype, what: str) -> int:
+    if not _FLOATS:
+        import torch
+
+        _FLOATS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32, bfloat16 or float16, not {dtype}")
+    return code
+
+
+def _pitch(t, rows: int, cols: int, what: str) -> int:
+    """Row pitch of a 2-D row-major tensor with unit column stride."""
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{what} must be row-major with unit column stride")
+    if rows <= 1:
+        return s0 if s0 > cols else cols  # a single row has no pitch of its own
+    if s0 < cols:
+        raise ValueError(f"{what}: rows overlap (a broadcast tensor? pass it unexpanded)")
+    return s0
+
+
+class _Group:
+    """The shape, type and device that a call's tensors have to share."""
+
+    __slots__ = ("rows", "cols", "dtype", "device", "code")
+
+    def __init__(self, t, what: str):
+        if t.dim() != 2:
+            raise ValueError(f"{what} must be 2-D (rows x columns)")
+        self.rows, self.cols = t.shape
+        self.dtype, self.device = t.dtype, t.device
+        self.code = _float_code(t.dtype, what)
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be on a GPU")
+
+    def _same(self, t, dtype, shape, what):
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{what} must be {dtype} of shape {shape}, not {t.dtype} of "
+                             f"{tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{what} must be on {self.device}")
+
+    def mat(self, t, what: str, rows: Optional[int] = None, cols: Optional[int] = None,
+            dtype=None) -> ptored_rows:
+        if t is None:
+            return _NO_ROWS
+        rows = self.rows if rows is None else rows
+        cols = self.cols if cols is None else cols
+        self._same(t, self.dtype if dtype is None else dtype, (rows, cols), what)
+        return ptored_rows(t.data_ptr(), _pitch(t, rows, cols, what))
+
+    def kept(self, k, what: str) -> ptored_checkpoint:
+        if k is None:
+            return _NO_KEPT
+        import torch
+
+        q, s = k
+        blocks = (self.cols + PTORED_CHECKPOINT_BLOCK - 1) // PTORED_CHECKPOINT_BLOCK
+        self._same(q, torch.int8, (self.rows, self.cols), what + "'s values")
+        self._same(s, torch.uint8, (self.rows, blocks), what + "'s scales")
+        return ptored_checkpoint(q.data_ptr(), _pitch(q, self.rows, self.cols, what + "'s values"),
+                                 s.data_ptr(), _pitch(s, self.rows, blocks, what + "'s scales"))
+
+    def vec(self, t, n: int, dtype, what: str) -> Optional[int]:
+        if t is None:
+            return None
+        self._same(t, dtype, (n,), what)
+        if n > 1 and t.stride(0) != 1:
+            raise ValueError(f"{what} must be contiguous")
+        return t.data_ptr()
+
+    def params(self, post_weight, pre_weight, gate, eps, weight_offset, branch_scale,
+               residual_scale) -> ptored_block_params:
+        w = pre_weight if post_weight is None else post_weight
+        wt = self.dtype if w is None else w.dtype
+        code = self.code if wt == self.dtype else _float_code(wt, "weights")
+        if code not in (0, self.code):
+            raise TypeError("weights must be float32 or of the activations' type")
+        gate_rows, g = 0, _NO_ROWS
+        if gate is not None:
+            if gate.dim() == 1:
+                gate = gate.unsqueeze(0)
+            gate_rows = gate.shape[0]
+            if gate.dim() != 2 or gate_rows == 0 or self.rows % gate_rows:
+                raise ValueError("gate must be [D] or [G, D] with G a divisor of the rows")
+            g = self.mat(gate, "gate", gate_rows)
+        return ptored_block_params(
+            self.rows, self.cols, self.vec(post_weight, self.cols, wt, "post_weight"),
+            self.vec(pre_weight, self.cols, wt, "pre_weight"), g, gate_rows, weight_offset,
+            branch_scale, residual_scale, eps, self.code, code)
+
+
+def _call(device, stream, call) -> None:
+    """``call(stream handle)`` with the tensors' GPU current, raising on errors."""
+    import torch
+
+    handle = B._stream_handle(stream, device)
+    if torch.cuda.current_device() == device.index:
+        B._raise_on(call(handle))
+        return
+    with torch.cuda.device(device):
+        B._raise_on(call(handle))
+
+
+def _torch_stream(stream, device):
+    """torch's object for the stream of a call."""
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _zero(tensors, device, stream) -> None:
+    """Sums over no rows, on the call's stream."""
+    import torch
+
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        for t in tensors:
+            if t is not None:
+                t.zero_()
+
+
+def _workspace(nbytes: int, given, device, stream):
+    """(tensor to keep until the call is made, pointer, bytes)."""
+    import torch
+
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the call's GPU")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if nbytes == 0:
+        return None, None, 0
+    if stream is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:  # belongs to the stream that uses it, so that it is not reused too early
+        with torch.cuda.stream(_torch_stream(stream, device)):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), nbytes
+
+
+def block_norm(parts, x, x_out=None, z=None, *, post_weight=None, gate=None, pre_weight=None,
+               eps: float = 1e-6, weight_offset: float = 0.0, branch_scale: float = 1.0,
+               residual_scale: float = 1.0, h=None, post_rstd=None, pre_rstd=None, h_kept=None,
+               x_kept=None, z_kept=None, stream=None) -> None:
+    """The block boundary, forward, into the outputs that are given:
+
+        h     = parts[0] + ... + parts[N-1]
+        p     = h r1 (post_weight + weight_offset), r1 = 1/sqrt(mean(h^2) + eps)
+        x_out = residual_scale x + branch_scale gate p
+        z     = x_out r2 (pre_weight + weight_offset), r2 = 1/sqrt(mean(x_out^2) + eps)
+
+    ``parts`` (0 to 64 ranks' partial outputs), ``x``, ``x_out``, ``z`` and
+    ``h`` are [T, D] of one floating type; without ``post_weight`` p = h,
+    without ``pre_weight`` there is no z.  ``gate`` is [D] or [G, D], each row
+    for T / G consecutive rows.  Weights are float32 or of the activations'
+    type.  For the backward pass: ``h`` (with one rank, parts[0] is h),
+    ``post_rstd`` and ``pre_rstd`` (float32 [T]), and ``h_kept``, ``x_kept``,
+    ``z_kept``, the 8-bit forms of h, x_out and z.  ``x_out`` may be ``x``.
+    """
+    g = _Group(x, "x")
+    import torch
+
+    parts = list(parts)
+    part_ld = g.cols
+    if parts:
+        part_ld = g.mat(parts[0], "parts[0]").ld
+        for t in parts[1:]:
+            if t.stride() != parts[0].stride():
+                raise ValueError("every part must have the same strides")
+            g._same(t, g.dtype, (g.rows, g.cols), "every part")
+    params = g.params(post_weight, pre_weight, gate, eps, weight_offset, branch_scale,
+                      residual_scale)
+    io = ptored_block_io(g.mat(x, "x"), g.mat(x_out, "x_out"), g.mat(z, "z"), g.mat(h, "h"),
+                         g.vec(post_rstd, g.rows, torch.float32, "post_rstd"),
+                         g.vec(pre_rstd, g.rows, torch.float32, "pre_rstd"),
+                         g.kept(h_kept, "h_kept"), g.kept(x_kept, "x_kept"),
+                         g.kept(z_kept, "z_kept"))
+    if g.rows == 0 or g.cols == 0:
+        return  # empty tensors have no storage
+    ptrs = [t.data_ptr() for t in parts]
+    _call(g.device, stream,
+          lambda s: ptored_block_norm(ptrs, len(ptrs), part_ld, params, io, s))
+
+
+def block_norm_backward_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
+    """Bytes of workspace of ``block_norm_backward``; ``gate_rows`` 0 where no
+    gate gradient is asked for."""
+    st, n = ptored_block_norm_backward_workspace(rows, cols, gate_rows)
+    B._raise_on(st)
+    return n
+
+
+def block_norm_backward(dz, dx_out, x_out, pre_rstd, dx=None, dh=None, *, h=None, post_rstd=None,
+                        post_weight=None, gate=None, pre_weight=None, dpost_weight=None,
+                        dgate=None, dpre_weight=None, weight_offset: float = 0.0,
+                        branch_scale: float = 1.0, residual_scale: float = 1.0, workspace=None,
+                        stream=None) -> None:
+    """Gradients of ``block_norm``, into the outputs that are given.
+
+    ``dz`` is z's gradient (None without ``pre_weight``), ``dx_out`` the one
+    that reaches x_out from further on (or None).  ``x_out`` and ``h`` are the
+    forward pass's activations, both as tensors or both as 8-bit checkpoints;
+    ``post_rstd`` and ``pre_rstd`` are its reciprocal norms.  ``dx`` is the
+    residual stream's gradient, ``dh`` that of the fold and so of every rank's
+    partial output; ``dgate``, ``dpost_weight`` and ``dpre_weight`` have the
+    shapes and types of what they are gradients of.  ``dx`` and ``dh`` may be
+    any of the [T, D] inputs.
+    """
+    ref = dz if dz is not None else dx_out
+    if ref is None:
+        raise ValueError("block_norm_backward needs dz, dx_out or both")
+    g = _Group(ref, "dz" if dz is not None else "dx_out")
+    import torch
+
+    params = g.params(post_weight, pre_weight, gate, 0.0, weight_offset, branch_scale,
+                      residual_scale)
+    packed = _is_kept(x_out) or _is_kept(h)
+    if packed and not all(v is None or _is_kept(v) for v in (x_out, h)):
+        raise ValueError("x_out and h must both be tensors or both be checkpoints")
+    wt = torch.float32 if params.weight_dtype == 0 else g.dtype
+    if dgate is not None and dgate.dim() == 1:
+        dgate = dgate.unsqueeze(0)
+    nbytes = 0
+    if g.cols <= PTORED_BLOCK_MAX_COLS:
+        nbytes = block_norm_backward_workspace(g.rows, g.cols,
+                                               0 if dgate is None else params.gate_rows)
+    wanted = dgate is not None or dpost_weight is not None or dpre_weight is not None
+    io = ptored_block_grad_io(
+        g.mat(dz, "dz"), g.mat(dx_out, "dx_out"),
+        _NO_ROWS if packed else g.mat(x_out, "x_out"), _NO_ROWS if packed else g.mat(h, "h"),
+        g.kept(x_out, "x_out") if packed else _NO_KEPT,
+        g.kept(h, "h") if packed else _NO_KEPT,
+        g.vec(post_rstd, g.rows, torch.float32, "post_rstd"),
+        g.vec(pre_rstd, g.rows, torch.float32, "pre_rstd"), g.mat(dx, "dx"), g.mat(dh, "dh"),
+        g.mat(dgate, "dgate", params.gate_rows),
+        g.vec(dpost_weight, g.cols, wt, "dpost_weight"),
+        g.vec(dpre_weight, g.cols, wt, "dpre_weight"), None, 0)
+    if g.cols == 0:
+        return
+    if g.rows == 0:  # nothing to read; the sums over no rows are zero
+        _zero((dgate, dpost_weight, dpre_weight), g.device, stream)
+        return
+    keep, io.workspace, io.workspace_bytes = _workspace(nbytes if wanted else 0, workspace,
+                                                        g.device, stream)
+    _call(g.device, stream, lambda s: ptored_block_norm_backward(params, io, s))
+
+
+def checkpoint_empty(rows: int, cols: int, device="cuda") -> Checkpoint:
+    """Room for a rows x cols activation in 8 bits."""
+    import torch
+
+    blocks = (cols + PTORED_CHECKPOINT_BLOCK - 1) // PTORED_CHECKPOINT_BLOCK
+    return Checkpoint(torch.empty(rows, cols, dtype=torch.int8, device=device),
+                      torch.empty(rows, blocks, dtype=torch.uint8, device=device))
+
+
+def checkpoint_pack(x, kept, stream=None) -> None:
+    """``kept`` = the 8-bit form of ``x`` ([T, D] of a floating type): each
+    value to within half a step, a step being 1/64 of the power of two below
+    the largest magnitude of its block of 32 (or 1/32 where that magnitude
+    comes within 1/256 of the next power).  A block with an infinity or a NaN
+    stands for NaN."""
+    g = _Group(x, "x")
+    xm, k = g.mat(x, "x"), g.kept(kept, "kept")
+    if g.rows and g.cols:
+        _call(g.device, stream,
+              lambda s: ptored_checkpoint_pack(xm, g.rows, g.cols, g.code, k, s))
+
+
+def checkpoint_unpack(kept, out, stream=None) -> None:
+    """``out`` = the values kept (exact in float32 and bfloat16)."""
+    g = _Group(out, "out")
+    om, k = g.mat(out, "out"), g.kept(kept, "kept")
+    if g.rows and g.cols:
+        _call(g.device, stream,
+              lambda s: ptored_checkpoint_unpack(k, g.rows, g.cols, g.code, om, s))
+
+
+def checkpoint_wgrad_workspace(rows: int, outs: int, cols: int, dtype) -> int:
+    """Bytes of workspace of ``checkpoint_wgrad``; ``dtype`` is dy's."""
+    st, n = ptored_checkpoint_wgrad_workspace(rows, outs, cols, B._dtype_code(dtype))
+    B._raise_on(st)
+    return n
+
+
+def checkpoint_wgrad(dy, kept, dw, accumulate: bool = False, workspace=None, stream=None) -> None:
+    """dw = dy^T x (or dw += dy^T x): the weight gradient of y = x W^T from
+    ``dy`` [T, O] and the kept input x [T, I], into ``dw`` [O, I], float32 or
+    of dy's type.  Products are exact and sums in float32."""
+    g = _Group(dy, "dy")
+    if dw.dim() != 2 or dw.shape[0] != g.cols:
+        raise ValueError("dw must be [dy's columns, x's columns]")
+    if kept[0].dim() != 2 or kept[0].shape[0] != g.rows:
+        raise ValueError("dy and the kept input must have the same rows")
+    code = _float_code(dw.dtype, "dw")
+    if code not in (0, g.code):
+        raise TypeError("dw must be float32 or of dy's type")
+    dym = g.mat(dy, "dy")
+    outs, cols = dw.shape
+    dwm = g.mat(dw, "dw", outs, cols, dw.dtype)
+    g.cols = cols
+    k = g.kept(kept, "kept")
+    if outs == 0 or cols == 0 or (g.rows == 0 and accumulate):
+        return
+    if g.rows == 0:  # the sum over no rows
+        _zero((dw,), g.device, stream)
+        return
+    nbytes = checkpoint_wgrad_workspace(g.rows, outs, cols, dy.dtype)
+    keep, ptr, given = _workspace(nbytes, workspace, g.device, stream)
+    _call(g.device, stream,
+          lambda s: ptored_checkpoint_wgrad(dym, k, g.rows, outs, cols, g.code, dwm, code,
+                                            1 if accumulate else 0, ptr, given, s))

@@ -3,7 +3,9 @@
 Every translation unit under csrc/ is compiled with hipcc in parallel and
 linked into ``cross_rank_collective_amd/libptored.so``: the host code, one
 unit per element type (copy and push-with-add kernels) and ``treduce_op.hip``
-once per (element type, operator) pair (reduction and ring kernels).  Run as
+once per (element type, operator) pair (reduction and ring kernels); and from
+csrc/block/ the block-boundary operators' kernels, once per floating type,
+with their host code.  Run as
 ``python -m cross_rank_collective_amd.build`` or through
 ``__graft_entry__.build()``.
 """
@@ -32,6 +34,11 @@ UNITS = [("treduce_op.hip", f"treduce_op_{dt.lower()}_{op.lower()}",
          for dt in ("BF16", "F16", "F32", "I32") for op in OPS]
 UNITS += [(f"treduce_{dt.lower()}.hip", f"treduce_{dt.lower()}", ()) for dt in DTYPES]
 UNITS += [("treduce_host.cpp", "treduce_host", ())]
+# The block-boundary operators: one unit per floating type, and their host code.
+UNITS += [("block/block_ops.hip", f"block_ops_{dt.lower()}",
+           (f"-DPTORED_INST_DT=PTORED_{dt}", f"-DPTORED_INST_NAME={dt.lower()}"))
+          for dt in ("BF16", "F16", "F32")]
+UNITS += [("block/block_host.cpp", "block_host", ())]
 
 ARCH = "gfx950"
 CFLAGS = [

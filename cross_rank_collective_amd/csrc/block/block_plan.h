@@ -1,0 +1,109 @@
+// block_plan.h -- what the host code hands to the kernels of the
+// block-boundary operators, and the launch functions (one per element type,
+// each in a unit of its own, block_ops.hip).
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+#include "ptored_block.h"
+
+namespace ptored {
+namespace block {
+
+// A matrix as the kernels address it: a null base means "not there".
+struct Mat {
+    char* p;
+    int64_t ld;  // bytes from one row to the next
+};
+
+// A packed matrix; q null means "not there".
+struct Kept {
+    int8_t* q;
+    int64_t q_ld;
+    uint8_t* s;
+    int64_t s_ld;
+};
+
+struct NormArgs {
+    const char* part[PTORED_MAX_RANKS];
+    int64_t part_ld;  // bytes
+    int64_t rows;
+    Mat x, x_out, z, h, gate;
+    Kept kh, kx, kz;
+    const char *w1, *w2;
+    float *r1, *r2;
+    int64_t rows_per_gate;
+    int32_t nranks, cols, w_f32;
+    float offset, alpha, beta, eps, inv_cols;
+};
+
+struct GradArgs {
+    int64_t rows;
+    Mat dz, dxo, x, h, dx, dh, gate, dgate;
+    Kept kx, kh;
+    const char *w1, *w2;
+    const float *r1, *r2;
+    float* ws;              // partial sums: [chunk][which][cols], see grad_split()
+    char *dw1, *dw2;
+    int64_t unit_rows;      // rows are cut into units of this many ...
+    int64_t chunks_per_unit;  // ... and each unit into this many chunks ...
+    int64_t chunk_rows;       // ... of this many rows (the unit's last may have fewer)
+    int64_t chunks;
+    int64_t gate_rows;
+    int64_t rows_per_gate;
+    int32_t gate_direct;  // 1: whole gate rows lie inside chunks, which write them at once
+    int32_t ws_slots;     // partial rows per chunk: dw1, dw2 and, without gate_direct, dgate
+    int32_t slot_w2, slot_gate;  // position of dw2's and dgate's (dw1's is 0); -1: none
+    int32_t slot_w1;
+    int32_t cols, w_f32;
+    float offset, alpha, beta, inv_cols;
+};
+
+// How the backward pass cuts its rows: a chunk is what one workgroup walks,
+// keeping the column sums in registers.  With a gate the chunks never
+// straddle two gate rows unless they hold whole ones.
+struct GradSplit {
+    int64_t unit_rows, chunks_per_unit, chunk_rows, chunks;
+    int32_t gate_direct;
+};
+
+struct PackArgs {
+    Mat x;
+    Kept k;
+    int64_t rows;
+    int32_t cols;
+};
+
+struct WgradArgs {
+    const char* dy;
+    int64_t dy_ld;  // bytes
+    Kept x;
+    char* dw;
+    int64_t dw_ld;  // bytes
+    float* ws;      // [split][outs][cols] partial sums when splits > 1
+    int64_t rows;
+    int64_t rows_per_split;  // a multiple of the kernel's step
+    int32_t outs, cols;
+    int32_t splits;
+    int32_t dw_f32, accumulate;
+    int32_t tiles_m, tiles_n;
+};
+
+enum : int { kOk = 0, kFailed = 1 };
+
+// T = f32, bf16, f16
+#define PTORED_BLOCK_LAUNCHES(T)                            \
+    int norm_##T(const NormArgs&, hipStream_t);             \
+    int grad_##T(const GradArgs&, hipStream_t);             \
+    int pack_##T(const PackArgs&, hipStream_t);             \
+    int unpack_##T(const PackArgs&, hipStream_t);           \
+    int wgrad_##T(const WgradArgs&, hipStream_t);
+PTORED_BLOCK_LAUNCHES(f32)
+PTORED_BLOCK_LAUNCHES(bf16)
+PTORED_BLOCK_LAUNCHES(f16)
+#undef PTORED_BLOCK_LAUNCHES
+
+}  // namespace block
+}  // namespace ptored

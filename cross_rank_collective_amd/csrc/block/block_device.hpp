@@ -2,11 +2,12 @@
 // a row in registers, wave and workgroup sums, the 8-bit form.
 //
 // A slot is 16 bytes of activations: V consecutive elements of one row (8 of
-// 16 bits, 4 of 32), held as V floats.  Lane l of a workgroup of B threads
-// holds slots l, l + B, ...: every wave instruction covers 1 KiB of a row.
-// Rows may start at any element and end inside a slot (TAIL): full slots are
-// one unaligned 16-byte access, which the hardware serves, the last partial
-// one goes element by element.  Nothing past a row's columns is touched.
+// 16 bits, 4 of 32), held as V floats.  Thread l of a workgroup of B holds
+// slots l, l + B, ..., S of them: every wave instruction covers 1 KiB of a
+// row.  Rows are accessed through buffer resources that end with the row, so
+// slots past it read as zeros and are not stored without a branch.  Rows may
+// start at any element (the hardware serves unaligned accesses) and end
+// inside a slot (EDGE).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -23,6 +24,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // the same with an element's alignment, for rows that start anywhere
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
@@ -106,54 +108,204 @@ struct Elem<PTORED_F16> {
     }
 };
 
-// The slot of V elements at column `col` of a row of `cols` elements starting
-// at `row`; elements past the row are 0.
-template <int DT, bool TAIL>
-__device__ __forceinline__ void load_slot(const char* row, int col, int cols, float* v) {
-    using E = Elem<DT>;
-    const char* p = row + (int64_t)col * E::kBytes;
-    if (!TAIL ? col < cols : col + E::V <= cols) {
-        E::widen(*reinterpret_cast<const u32x4_any*>(p), v);
-        return;
-    }
+// ---------------------------------------------------------------- rows
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr int kPolicyStream = 2;  // nt: read or written once
+constexpr int kPolicyKeep = 0;    // weights, which every row reads
+
+__device__ __forceinline__ rsrc_t row_rsrc(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
+}
+
+// The 16 bytes of `v` without the first `n` (0 to 15), zeros behind.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int n) {
+    const bool two = n & 8, one = n & 4;
+    v = (u32x4){two ? v[2] : v[0], two ? v[3] : v[1], two ? 0u : v[2], two ? 0u : v[3]};
+    v = (u32x4){one ? v[1] : v[0], one ? v[2] : v[1], one ? v[3] : v[2], one ? 0u : v[3]};
+    const uint32_t b = (uint32_t)n & 3u;
+    return (u32x4){__builtin_amdgcn_alignbyte(v[1], v[0], b),
+                   __builtin_amdgcn_alignbyte(v[2], v[1], b),
+                   __builtin_amdgcn_alignbyte(v[3], v[2], b),
+                   __builtin_amdgcn_alignbyte(0u, v[3], b)};
+}
+
+// The same for 8 words and whole words.
+__device__ __forceinline__ void shift_words(uint32_t* w, int n) {
 #pragma unroll
-    for (int i = 0; i < E::V; ++i) v[i] = 0.0f;
-    if constexpr (TAIL) {
+    for (int b = 4; b >= 1; b /= 2) {
 #pragma unroll
-        for (int i = 0; i < E::V - 1; ++i)
-            if (col + i < cols) v[i] = E::load1(p + i * E::kBytes);
+        for (int i = 0; i < 8; ++i) w[i] = n & b ? (i + b < 8 ? w[i + b] : 0u) : w[i];
     }
 }
 
-template <int DT, bool TAIL>
-__device__ __forceinline__ void store_slot(char* row, int col, int cols, const float* v) {
-    using E = Elem<DT>;
-    char* p = row + (int64_t)col * E::kBytes;
-    if (!TAIL ? col < cols : col + E::V <= cols) {
-        *reinterpret_cast<u32x4_any*>(p) = E::narrow(v);
-        return;
-    }
-    if constexpr (TAIL) {
-#pragma unroll
-        for (int i = 0; i < E::V - 1; ++i)
-            if (col + i < cols) E::store1(p + i * E::kBytes, v[i]);
-    }
-}
-
-// V elements of a norm weight (32 bits, or the activations' type) at `col`,
-// plus the offset.
-template <int DT, bool TAIL>
-__device__ __forceinline__ void load_weight(const char* w, int w_f32, float offset, int col,
-                                            int cols, float* v) {
+// Rows that end inside a slot.
+enum : int {
+    kWhole = 0,  // they do not
+    kPart = 1,   // the last slot is loaded so that it ends with the row, and moved
+    kTiny = 2,   // rows shorter than a slot: element by element
+};
+template <int DT>
+inline int edge_of(int cols) {
     constexpr int V = Elem<DT>::V;
-    if (w_f32) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) load_slot<PTORED_F32, TAIL>(w, col + i, cols, v + i);
-    } else {
-        load_slot<DT, TAIL>(w, col, cols, v);
+    return cols % V == 0 ? kWhole : cols > V ? kPart : kTiny;
+}
+
+// A packed slot as loaded: V values and their block's scale byte.
+struct KeptRaw {
+    u32x2 q;
+    uint32_t scale;
+};
+
+// Where this thread's S slots lie in a row of `cols` elements.  The launch
+// has S - 1 slots of every thread inside the row: only the last can lie past
+// it or be cut by its end.
+template <int DT, int S, int EDGE>
+struct Slots {
+    using E = Elem<DT>;
+    static constexpr int V = E::V, ES = E::kBytes;
+    int cols, stride;  // elements
+    int col0, last;    // column of the first slot, and of the last as loaded
+    int lost;          // elements of the last, as loaded, that belong to the one before
+    bool part;
+
+    __device__ __forceinline__ explicit Slots(int n) {
+        cols = n;
+        stride = (int)blockDim.x * V;
+        col0 = (int)threadIdx.x * V;
+        last = col(S - 1);
+        part = EDGE != kWhole && last < cols && last + V > cols;
+        lost = 0;
+        if (EDGE == kPart && part) {
+            lost = last + V - cols;
+            last = cols - V;
+        }
     }
+    __device__ __forceinline__ int col(int s) const { return col0 + s * stride; }
+    __device__ __forceinline__ int at(int s) const { return s == S - 1 ? last : col(s); }
+    __device__ __forceinline__ rsrc_t row(const char* p) const { return row_rsrc(p, cols * ES); }
+
+    // The slot as loaded, to be passed to take() when it is used.
+    __device__ __forceinline__ u32x4 load(rsrc_t r, int s) const {
+        if constexpr (EDGE == kTiny) {
+            uint32_t w[4] = {};
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += offset;
+            for (int i = 0; i < V - 1; ++i) {
+                if constexpr (ES == 4)
+                    w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (col0 + i) * ES, 0, 0);
+                else
+                    w[i / 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                    r, (col0 + i) * ES, 0, 0)
+                                << (16 * (i % 2));
+            }
+            return (u32x4){w[0], w[1], w[2], w[3]};
+        } else {
+            return __builtin_amdgcn_raw_buffer_load_b128(r, at(s) * ES, 0, kPolicyStream);
+        }
+    }
+    __device__ __forceinline__ void take(u32x4 w, int s, float* v) const {
+        if (EDGE == kPart && s == S - 1) w = shift_down(w, lost * ES);
+        E::widen(w, v);
+    }
+    __device__ __forceinline__ void store(rsrc_t r, int s, const float* v) const {
+        const u32x4 w = E::narrow(v);
+        if (EDGE == kWhole || s < S - 1 || (EDGE == kPart && !part)) {
+            __builtin_amdgcn_raw_buffer_store_b128(w, r, col(s) * ES, 0, kPolicyStream);
+            return;
+        }
+        if (EDGE == kTiny && !part) return;
+#pragma unroll
+        for (int i = 0; i < V - 1; ++i) {
+            if constexpr (ES == 4)
+                __builtin_amdgcn_raw_buffer_store_b32(w[i], r, (col(s) + i) * ES, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(w[i / 2] >> (16 * (i % 2))),
+                                                      r, (col(s) + i) * ES, 0, 0);
+        }
+    }
+
+    // V values of a norm weight (32 bits, or the activations' type).
+    struct Weight {
+        u32x4 w[V == 8 ? 2 : 1];
+    };
+    __device__ __forceinline__ Weight load_weight(const char* p, int f32, int s) const {
+        Weight k;
+        if (V == 4 || !f32) {
+            const rsrc_t r = row(p);
+            if constexpr (EDGE == kTiny)
+                k.w[0] = load(r, s);
+            else
+                k.w[0] = __builtin_amdgcn_raw_buffer_load_b128(r, at(s) * ES, 0, kPolicyKeep);
+        } else {
+            const rsrc_t r = row_rsrc(p, cols * 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (EDGE == kTiny) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        k.w[h % (V / 4)][i] = __builtin_amdgcn_raw_buffer_load_b32(
+                            r, (col0 + 4 * h + i) * 4, 0, 0);
+                } else {
+                    k.w[h % (V / 4)] = __builtin_amdgcn_raw_buffer_load_b128(
+                        r, at(s) * 4 + 16 * h, 0, kPolicyKeep);
+                }
+            }
+        }
+        return k;
+    }
+    __device__ __forceinline__ void take_weight(const Weight& k, int f32, float offset, int s,
+                                                float* v) const {
+        if (V == 4 || !f32) {
+            take(k.w[0], s, v);
+        } else {
+            uint32_t u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = k.w[i / 4 % (V / 4)][i % 4];
+            if (EDGE == kPart && s == S - 1) shift_words(u, lost);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = as_f(u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += offset;
+    }
+
+    // A packed row: its values and its scale bytes.
+    struct KeptRow {
+        rsrc_t q, s;
+    };
+    __device__ __forceinline__ KeptRow kept_row(const Kept& k, int64_t row) const {
+        return {row_rsrc(k.q + row * k.q_ld, cols),
+                row_rsrc(k.s + row * k.s_ld,
+                         (cols + PTORED_CHECKPOINT_BLOCK - 1) / PTORED_CHECKPOINT_BLOCK)};
+    }
+    __device__ __forceinline__ KeptRaw load_kept(const KeptRow& k, int s) const {
+        KeptRaw w;
+        w.q = (u32x2){0u, 0u};
+        if constexpr (EDGE == kTiny) {
+#pragma unroll
+            for (int i = 0; i < V - 1; ++i)
+                w.q[i / 4] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(k.q, col0 + i, 0, 0)
+                              << (8 * (i % 4));
+        } else if constexpr (V == 8) {
+            w.q = __builtin_amdgcn_raw_buffer_load_b64(k.q, at(s), 0, kPolicyStream);
+        } else {
+            w.q[0] = __builtin_amdgcn_raw_buffer_load_b32(k.q, at(s), 0, kPolicyStream);
+        }
+        w.scale = __builtin_amdgcn_raw_buffer_load_b8(k.s, col(s) / PTORED_CHECKPOINT_BLOCK, 0, 0);
+        return w;
+    }
+    // The values kept times `by`; exact products aside, the same as taking them first.
+    __device__ __forceinline__ void take_kept(const KeptRaw& w, int s, float by, float* v) const;
+    __device__ __forceinline__ void store_kept(const KeptRow& k, int s, const float* v) const;
+};
+
+// Threads of a launch as Slots counts on it, with `per` slots each or, where
+// a thread's first per - 1 would not all lie inside the row, fewer.
+inline int slot_threads(int slots, int& per) {
+    for (;; per /= 2) {
+        const int threads = ((slots + per - 1) / per + 63) / 64 * 64;
+        if (per == 1 || (per - 1) * threads < slots) return threads;
+    }
 }
 
 // ---------------------------------------------------------------- sums
@@ -188,23 +340,39 @@ constexpr int kMaxWaves = 16;  // waves of the largest workgroup
 // caller's buffers; the caller alternates between two, so that one barrier
 // per sum is enough: a wave writes a buffer again only after the barrier of
 // the sum in between, which every wave reaches after it has read this one.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <int K>
-__device__ __forceinline__ void block_sum(float (*red)[kMaxWaves], float* v) {
+__device__ __forceinline__ void block_sum(f32x4 (*red)[kMaxWaves / 4], float* v) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
-    const int waves = (int)blockDim.x >> 6;
+    const int waves = (int)blockDim.x >> 6, wave = (int)threadIdx.x >> 6;
     if (waves == 1) return;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) red[k][threadIdx.x >> 6] = v[k];
+        for (int k = 0; k < K; ++k) red[k][wave / 4][wave % 4] = v[k];
+        // the last wave fills its group of four
+        for (int w = waves; w % 4 != 0 && wave == waves - 1; ++w)
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[k][w / 4][w % 4] = 0.0f;
     }
     __syncthreads();
+    f32x4 s[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float s = 0.0f;
-        for (int w = 0; w < waves; ++w) s += red[k][w];
-        v[k] = s;
+    for (int k = 0; k < K; ++k) s[k] = red[k][0];
+    if (waves > 4) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[k] += red[k][1];
     }
+    if (waves > 8) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[k] += red[k][2];
+    }
+    if (waves > 12) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[k] += red[k][3];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = (s[k][0] + s[k][1]) + (s[k][2] + s[k][3]);
 }
 
 // ---------------------------------------------------------------- 8 bits
@@ -226,46 +394,34 @@ __device__ __forceinline__ uint32_t block_amax(const float* v) {
     return m;
 }
 
-// Packs the slot at `col` of a row; every lane of the wave takes part (slots
-// past the row hold zeros and store nothing).  Zeros past a row's end do not
-// change its last block's largest magnitude.
-template <int V, bool TAIL>
-__device__ __forceinline__ void pack_slot(const Kept& k, int64_t row, int col, int cols,
-                                          const float* v) {
+// A slot's packed form: V bytes and the block's scale byte.  Every lane of the
+// wave takes part (slots past the row hold zeros, which do not change its last
+// block's largest magnitude).
+template <int V>
+__device__ __forceinline__ KeptRaw quantise(const float* v) {
     const uint32_t top = block_amax<V>(v);
     const bool finite = top < 0x7F800000u;
     // E: the exponent of amax, one more where amax 2^(6-E) would round to 128
     // (127.5 = 64 * 1.1111111b does, ties to even)
     int e = (int)(top >> 23) - 127 + ((top & 0x7FFFFFu) >= 0x7F0000u ? 1 : 0);
     e = min(max(e, -120), 127);
-    const float f = power_of_2(6 - e);
-    uint32_t w[V / 4];
+    // 1.5 2^23 + v 2^(6-E) has the quotient, rounded with ties to even, in its
+    // low bits
+    const float f = power_of_2(6 - e), m = 12582912.0f;
+    KeptRaw k;
+    k.q = (u32x2){0u, 0u};
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-        uint32_t word = 0;
+        uint32_t q[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float r = __builtin_rintf(v[i + j] * f);
-            const int q = finite ? (int)fminf(fmaxf(r, -127.0f), 127.0f) : 0;
-            word |= ((uint32_t)q & 0xFFu) << (8 * j);
-        }
-        w[i / 4] = word;
+        for (int j = 0; j < 4; ++j)
+            q[j] = as_u(__builtin_amdgcn_fmed3f(fmaf(v[i + j], f, m), m - 127.0f, m + 127.0f));
+        const uint32_t lo = __builtin_amdgcn_perm(q[1], q[0], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(q[3], q[2], 0x04000C0Cu);
+        k.q[i / 4] = finite ? lo | hi : 0u;
     }
-    if (col >= cols) return;
-    int8_t* q = k.q + row * k.q_ld + col;
-    if (!TAIL || col + V <= cols) {
-        if constexpr (V == 8)
-            *reinterpret_cast<u32x2_any*>(q) = (u32x2){w[0], w[1]};
-        else
-            *reinterpret_cast<uint32_t __attribute__((aligned(1)))*>(q) = w[0];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V - 1; ++i)
-            if (col + i < cols) q[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
-    }
-    if ((col & (PTORED_CHECKPOINT_BLOCK - 1)) == 0)
-        k.s[row * k.s_ld + col / PTORED_CHECKPOINT_BLOCK] =
-            finite ? (uint8_t)(e + 127) : (uint8_t)255;
+    k.scale = finite ? (uint32_t)(e + 127) : 255u;
+    return k;
 }
 
 // The factor 2^(E-6) of a scale byte; NaN for 255.
@@ -275,31 +431,43 @@ __device__ __forceinline__ float scale_factor(uint32_t s) {
     return s == 255u ? as_f(0x7FC00000u) : as_f((max(s, 7u) - 6u) << 23);
 }
 
-template <int V, bool TAIL>
-__device__ __forceinline__ void unpack_slot(const Kept& k, int64_t row, int col, int cols,
-                                            float* v) {
+template <int V>
+__device__ __forceinline__ void dequantise(const KeptRaw& k, float by, float* v) {
+    const float f = scale_factor(k.scale) * by;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.0f;
-    if (col >= cols) return;
-    const int8_t* q = k.q + row * k.q_ld + col;
-    const float f = scale_factor(k.s[row * k.s_ld + col / PTORED_CHECKPOINT_BLOCK]);
-    uint32_t w[V / 4] = {};
-    if (!TAIL || col + V <= cols) {
-        if constexpr (V == 8) {
-            const u32x2 u = *reinterpret_cast<const u32x2_any*>(q);
-            w[0] = u[0];
-            w[1] = u[1];
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t __attribute__((aligned(1)))*>(q);
-        }
+    for (int i = 0; i < V; ++i) v[i] = (float)(int8_t)(k.q[i / 4] >> (8 * (i % 4))) * f;
+}
+
+template <int DT, int S, int EDGE>
+__device__ __forceinline__ void Slots<DT, S, EDGE>::store_kept(const KeptRow& r, int s,
+                                                               const float* v) const {
+    const KeptRaw k = quantise<V>(v);
+    const int c = col(s);
+    if (EDGE == kWhole || s < S - 1 || !part) {
+        if constexpr (V == 8)
+            __builtin_amdgcn_raw_buffer_store_b64(k.q, r.q, c, 0, kPolicyStream);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(k.q[0], r.q, c, 0, kPolicyStream);
     } else {
 #pragma unroll
         for (int i = 0; i < V - 1; ++i)
-            if (col + i < cols) w[i / 4] |= (uint32_t)(uint8_t)q[i] << (8 * (i % 4));
+            __builtin_amdgcn_raw_buffer_store_b8((unsigned char)(k.q[i / 4] >> (8 * (i % 4))), r.q,
+                                                 c + i, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (!TAIL || col + i < cols) v[i] = (float)(int8_t)(w[i / 4] >> (8 * (i % 4))) * f;
+    if ((c & (PTORED_CHECKPOINT_BLOCK - 1)) == 0)
+        __builtin_amdgcn_raw_buffer_store_b8((unsigned char)k.scale, r.s,
+                                             c / PTORED_CHECKPOINT_BLOCK, 0, 0);
+}
+
+template <int DT, int S, int EDGE>
+__device__ __forceinline__ void Slots<DT, S, EDGE>::take_kept(const KeptRaw& w, int s,
+                                                              float by, float* v) const {
+    KeptRaw k = w;
+    if (EDGE == kPart && s == S - 1) {
+        const uint64_t u = ((uint64_t)k.q[1] << 32 | k.q[0]) >> (8 * lost);
+        k.q = (u32x2){(uint32_t)u, (uint32_t)(u >> 32)};
+    }
+    dequantise<V>(k, by, v);
 }
 
 }  // namespace block

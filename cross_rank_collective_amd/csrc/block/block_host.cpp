@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "block_plan.h"
 
@@ -117,15 +118,17 @@ int status_of(int rc) { return rc == kOk ? PTORED_OK : PTORED_ERR_HIP; }
      : (dtype) == PTORED_BF16 ? f##_bf16(__VA_ARGS__)            \
                               : f##_f16(__VA_ARGS__))
 
-// Rows per chunk of the backward pass: enough chunks to fill 256 compute
-// units several times over, few enough that the partial rows they leave (8
-// bytes a column, written and read) stay a small part of the rows' own.
-constexpr int64_t kTargetChunks = 1024;
+// The backward pass keeps 16 waves on every compute unit, each wave 512
+// columns wide, and cuts the rows into as many chunks as that makes
+// workgroups: the partial rows they leave (8 bytes a column, written and
+// read) are then a small part of the rows' own bytes.
+constexpr int64_t kGradWaves = 4096;
 
-GradSplit grad_split(int64_t rows, int64_t gate_rows) {
+GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows) {
     GradSplit s{};
     if (rows == 0) return s;
-    const int64_t per = (rows + kTargetChunks - 1) / kTargetChunks;
+    const int64_t target = std::max<int64_t>(1, kGradWaves / ((cols + 511) / 512));
+    const int64_t per = (rows + target - 1) / target;
     const int64_t unit = gate_rows > 0 ? rows / gate_rows : rows;
     if (gate_rows > 0 && unit <= per) {  // whole gate rows inside a chunk
         s.unit_rows = rows;
@@ -142,24 +145,31 @@ GradSplit grad_split(int64_t rows, int64_t gate_rows) {
     return s;
 }
 
+// Columns of a partial row: whole vectors of 4.
+int64_t grad_pitch(int64_t cols) { return (cols + 3) / 4 * 4; }
+
 int64_t grad_workspace(int64_t cols, int64_t gate_rows, const GradSplit& s) {
-    return s.chunks * cols * 4 * (gate_rows > 0 && !s.gate_direct ? 3 : 2);
+    return s.chunks * grad_pitch(cols) * 4 * (gate_rows > 0 && !s.gate_direct ? 3 : 2);
 }
 
 struct WgradShape {
     int64_t tiles_m, tiles_n, splits, rows_per_split;
+    int wide;
 };
 
 // Tokens are split over workgroups when the tiles of dw alone would leave
 // compute units idle, in parts of at least 4 steps.
-constexpr int64_t kTile = 128, kTokens = 64;
-WgradShape wgrad_shape(int64_t rows, int64_t outs, int64_t cols) {
+constexpr int64_t kTokens = 64;
+WgradShape wgrad_shape(int64_t rows, int64_t outs, int64_t cols, int dtype) {
     WgradShape w{};
-    w.tiles_m = (outs + kTile - 1) / kTile;
-    w.tiles_n = (cols + kTile - 1) / kTile;
+    const char* force = getenv("WG_WIDE");
+    w.wide = force ? atoi(force) : outs * cols >= (int64_t)200 * 65536;
+    const int64_t tm = w.wide && dtype != PTORED_F32 ? 256 : 128, tn = w.wide ? 256 : 128;
+    w.tiles_m = (outs + tm - 1) / tm;
+    w.tiles_n = (cols + tn - 1) / tn;
     const int64_t steps = (rows + kTokens - 1) / kTokens;
     if (steps == 0) return w;
-    int64_t splits = std::min<int64_t>(512 / std::max<int64_t>(1, w.tiles_m * w.tiles_n), steps / 4);
+    int64_t splits = std::min<int64_t>((w.wide ? 256 : 512) / std::max<int64_t>(1, w.tiles_m * w.tiles_n), steps / 4);
     splits = std::max<int64_t>(1, splits);
     const int64_t per = (steps + splits - 1) / splits;
     w.rows_per_split = per * kTokens;
@@ -258,7 +268,7 @@ extern "C" int ptored_block_norm_backward_workspace(int64_t rows, int64_t cols, 
         (gate_rows > 0 && rows % gate_rows != 0))
         return PTORED_ERR_INVALID_ARG;
     if (cols > PTORED_BLOCK_MAX_COLS) return PTORED_ERR_UNSUPPORTED;
-    *bytes = grad_workspace(cols, gate_rows, grad_split(rows, gate_rows));
+    *bytes = grad_workspace(cols, gate_rows, grad_split(rows, cols, gate_rows));
     return PTORED_OK;
 }
 
@@ -301,14 +311,15 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     b.vec(io->dpre_weight, p.cols * ws, ws, true);
 
     const bool gated = io->dgate.data != nullptr;
-    const GradSplit split = grad_split(p.rows, gated ? p.gate_rows : 0);
+    const GradSplit split = grad_split(p.rows, p.cols, gated ? p.gate_rows : 0);
     const bool partial_gate = gated && !split.gate_direct;
     GradArgs a{};
     a.slot_w1 = a.slot_w2 = a.slot_gate = -1;
     if (io->dpost_weight) a.slot_w1 = a.ws_slots++;
     if (io->dpre_weight) a.slot_w2 = a.ws_slots++;
     if (partial_gate) a.slot_gate = a.ws_slots++;
-    const int64_t need = split.chunks * p.cols * 4 * a.ws_slots;
+    a.ws_pitch = grad_pitch(p.cols);
+    const int64_t need = split.chunks * a.ws_pitch * 4 * a.ws_slots;
     if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
         return PTORED_ERR_INVALID_ARG;
     if (need > 0) b.vec(io->workspace, need, 16, true);
@@ -342,6 +353,8 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     a.gate_direct = split.gate_direct;
     a.gate_rows = p.gate_rows;
     a.rows_per_gate = p.gate.data ? p.rows / p.gate_rows : p.rows;
+    // a chunk begins with a gate row unless that row's gradient is not wanted
+    a.chunk_gates = split.chunk_rows <= a.rows_per_gate && (gated || p.gate_rows <= 1) ? 1 : 2;
     a.w_f32 = p.weight_dtype == PTORED_F32;
     a.offset = p.weight_offset;
     a.alpha = p.branch_scale;
@@ -372,7 +385,7 @@ extern "C" int ptored_checkpoint_wgrad_workspace(int64_t rows, int64_t outs, int
         !shape_ok(outs, cols))
         return PTORED_ERR_INVALID_ARG;
     if (!float_type(dtype)) return PTORED_ERR_UNSUPPORTED;
-    *bytes = wgrad_workspace(outs, cols, wgrad_shape(rows, outs, cols));
+    *bytes = wgrad_workspace(outs, cols, wgrad_shape(rows, outs, cols, dtype));
     return PTORED_OK;
 }
 
@@ -391,7 +404,7 @@ extern "C" int ptored_checkpoint_wgrad(ptored_rows dy, ptored_checkpoint x, int6
         return PTORED_ERR_INVALID_ARG;
     if (!float_type(dtype) || (dw_dtype != PTORED_F32 && dw_dtype != dtype))
         return PTORED_ERR_UNSUPPORTED;
-    const WgradShape w = wgrad_shape(rows, outs, cols);
+    const WgradShape w = wgrad_shape(rows, outs, cols, dtype);
     if (w.tiles_m * w.tiles_n > (int64_t(1) << 31) - 1) return PTORED_ERR_UNSUPPORTED;
     const int64_t need = wgrad_workspace(outs, cols, w);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
@@ -418,5 +431,6 @@ extern "C" int ptored_checkpoint_wgrad(ptored_rows dy, ptored_checkpoint x, int6
     a.accumulate = accumulate != 0;
     a.tiles_m = (int32_t)w.tiles_m;
     a.tiles_n = (int32_t)w.tiles_n;
+    a.wide = w.wide;
     return status_of(PTORED_BY_TYPE(wgrad, dtype, a, stream));
 }

@@ -19,43 +19,51 @@
 namespace ptored {
 namespace block {
 
-template <int DT, int S, bool TAIL>
+// S slots of a row per thread.  KEEP: at least one output in 8 bits.
+template <int DT, int S, int EDGE, bool KEEP>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
     using E = Elem<DT>;
     constexpr int V = E::V;
-    __shared__ float red[2][1][kMaxWaves];
-    const int stride = (int)blockDim.x * V;
-    const int col0 = (int)threadIdx.x * V;
+    // ranks whose slots are in flight together
+    constexpr int R = 4;
+    typedef Slots<DT, S, EDGE> Row;
+    __shared__ f32x4 red[2][1][kMaxWaves / 4];
+    const Row t(a.cols);
+    int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float h[S][V], x[S][V];
+        const bool gated = a.gate.p != nullptr;
+        const rsrc_t gate_row =
+            t.row(gated ? a.gate.p + row / a.rows_per_gate * a.gate.ld : nullptr);
+        u32x4 x_raw[S];
+        const rsrc_t x_row = t.row(a.x.p + row * a.x.ld);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < S; ++s) x_raw[s] = t.load(x_row, s);
+        float h[S][V];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int i = 0; i < V; ++i) h[s][i] = 0.0f;
-            load_slot<DT, TAIL>(a.x.p + row * a.x.ld, col0 + s * stride, a.cols, x[s]);
-        }
         const int64_t part_off = row * a.part_ld;
-#pragma unroll 4
-        for (int r = 0; r < a.nranks; ++r) {
+        for (int r0 = 0; r0 < a.nranks; r0 += R) {
+            u32x4 y_raw[R][S];
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float y[V];
-                load_slot<DT, TAIL>(a.part[r] + part_off, col0 + s * stride, a.cols, y);
+            for (int r = 0; r < R; ++r) {
+                // past the last rank nothing is read and zeros are added
+                const bool in = r0 + r < a.nranks;
+                const rsrc_t y_row =
+                    row_rsrc(a.part[in ? r0 + r : 0] + part_off, in ? a.cols * E::kBytes : 0);
 #pragma unroll
-                for (int i = 0; i < V; ++i) h[s][i] += y[i];
+                for (int s = 0; s < S; ++s) y_raw[r][s] = t.load(y_row, s);
             }
-        }
-        if (a.h.p != nullptr || a.kh.q != nullptr) {
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int col = col0 + s * stride;
-                if (a.h.p) store_slot<DT, TAIL>(a.h.p + row * a.h.ld, col, a.cols, h[s]);
-                if (a.kh.q) {
-                    float t[V];
-                    E::widen(E::narrow(h[s]), t);
-                    pack_slot<V, TAIL>(a.kh, row, col, a.cols, t);
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    float y[V];
+                    t.take(y_raw[r][s], s, y);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) h[s][i] += y[i];
                 }
-            }
         }
         float branch = a.alpha;
         if (a.w1 != nullptr) {
@@ -64,71 +72,106 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int i = 0; i < V; ++i) sum[0] += h[s][i] * h[s][i];
-            block_sum<1>(red[0], sum);
+            block_sum<1>(red[turn], sum);
+            turn ^= 1;
             const float r1 = 1.0f / sqrtf(sum[0] * a.inv_cols + a.eps);
             if (a.r1 != nullptr && threadIdx.x == 0) a.r1[row] = r1;
             branch *= r1;
         }
-        const char* gate = nullptr;
-        if (a.gate.p != nullptr) gate = a.gate.p + row / a.rows_per_gate * a.gate.ld;
-        float sum[1] = {0.0f};
+        if (a.h.p) {
+            const rsrc_t out = t.row(a.h.p + row * a.h.ld);
+#pragma unroll
+            for (int s = 0; s < S; ++s) t.store(out, s, h[s]);
+        }
+        if (KEEP && a.kh.q) {
+            const typename Row::KeptRow out = t.kept_row(a.kh, row);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float v[V];
+                E::widen(E::narrow(h[s]), v);
+                t.store_kept(out, s, v);
+            }
+        }
+        float x[S][V], sum[1] = {0.0f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const int col = col0 + s * stride;
-            float t[V];
+            float p[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) t[i] = branch * h[s][i];
+            for (int i = 0; i < V; ++i) p[i] = branch * h[s][i];
             if (a.w1 != nullptr) {
                 float w[V];
-                load_weight<DT, TAIL>(a.w1, a.w_f32, a.offset, col, a.cols, w);
+                t.take_weight(t.load_weight(a.w1, a.w_f32, s), a.w_f32, a.offset, s, w);
 #pragma unroll
-                for (int i = 0; i < V; ++i) t[i] *= w[i];
+                for (int i = 0; i < V; ++i) p[i] *= w[i];
             }
-            if (gate != nullptr) {
+            if (gated) {
                 float g[V];
-                load_slot<DT, TAIL>(gate, col, a.cols, g);
+                t.take(t.load(gate_row, s), s, g);
 #pragma unroll
-                for (int i = 0; i < V; ++i) t[i] *= g[i];
+                for (int i = 0; i < V; ++i) p[i] *= g[i];
             }
+            t.take(x_raw[s], s, x[s]);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                x[s][i] = a.beta * x[s][i] + t[i];
+                x[s][i] = a.beta * x[s][i] + p[i];
                 sum[0] += x[s][i] * x[s][i];
             }
-            if (a.x_out.p) store_slot<DT, TAIL>(a.x_out.p + row * a.x_out.ld, col, a.cols, x[s]);
-            if (a.kx.q) {
-                E::widen(E::narrow(x[s]), t);
-                pack_slot<V, TAIL>(a.kx, row, col, a.cols, t);
+        }
+        if (a.x_out.p) {
+            const rsrc_t out = t.row(a.x_out.p + row * a.x_out.ld);
+#pragma unroll
+            for (int s = 0; s < S; ++s) t.store(out, s, x[s]);
+        }
+        if (KEEP && a.kx.q) {
+            const typename Row::KeptRow out = t.kept_row(a.kx, row);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float v[V];
+                E::widen(E::narrow(x[s]), v);
+                t.store_kept(out, s, v);
             }
         }
         if (a.w2 == nullptr) continue;  // the same for every wave
-        block_sum<1>(red[1], sum);
+        block_sum<1>(red[turn], sum);
+        turn ^= 1;
         const float r2 = 1.0f / sqrtf(sum[0] * a.inv_cols + a.eps);
         if (a.r2 != nullptr && threadIdx.x == 0) a.r2[row] = r2;
-        if (a.z.p == nullptr && a.kz.q == nullptr) continue;
+        if (a.z.p == nullptr && !(KEEP && a.kz.q)) continue;
+        const rsrc_t z_row = t.row(a.z.p + row * a.z.ld);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const int col = col0 + s * stride;
-            float w[V];
-            load_weight<DT, TAIL>(a.w2, a.w_f32, a.offset, col, a.cols, w);
+            float z[V];
+            t.take_weight(t.load_weight(a.w2, a.w_f32, s), a.w_f32, a.offset, s, z);
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[i] *= r2 * x[s][i];
-            if (a.z.p) store_slot<DT, TAIL>(a.z.p + row * a.z.ld, col, a.cols, w);
-            if (a.kz.q) {
-                float t[V];
-                E::widen(E::narrow(w), t);
-                pack_slot<V, TAIL>(a.kz, row, col, a.cols, t);
+            for (int i = 0; i < V; ++i) z[i] *= r2 * x[s][i];
+            if (a.z.p) t.store(z_row, s, z);
+            if (KEEP && a.kz.q) {
+                E::widen(E::narrow(z), z);
+                t.store_kept(t.kept_row(a.kz, row), s, z);
             }
         }
     }
 }
 
+template <int DT, int S, bool KEEP>
+static const void* norm_pick(int cols) {
+    switch (edge_of<DT>(cols)) {
+        case kWhole: return reinterpret_cast<const void*>(norm_kernel<DT, S, kWhole, KEEP>);
+        case kPart: return reinterpret_cast<const void*>(norm_kernel<DT, S, kPart, KEEP>);
+        default:
+            if constexpr (S == 1)
+                return reinterpret_cast<const void*>(norm_kernel<DT, 1, kTiny, KEEP>);
+            return nullptr;
+    }
+}
+
 template <int DT, int S>
 static int launch_norm(const NormArgs& a, int threads, hipStream_t stream) {
-    const bool tail = a.cols % Elem<DT>::V != 0;
-    const void* k = tail ? reinterpret_cast<const void*>(norm_kernel<DT, S, true>)
-                         : reinterpret_cast<const void*>(norm_kernel<DT, S, false>);
-    const int64_t grid = a.rows < (int64_t(1) << 30) ? a.rows : (int64_t(1) << 30);
+    const bool keep = a.kh.q != nullptr || a.kx.q != nullptr || a.kz.q != nullptr;
+    const void* k = keep ? norm_pick<DT, S, true>(a.cols) : norm_pick<DT, S, false>(a.cols);
+    // a launch takes fewer than 2^32 threads
+    const int64_t most = (int64_t(1) << 31) / threads;
+    const int64_t grid = a.rows < most ? a.rows : most;
     void* args[] = {const_cast<NormArgs*>(&a)};
     return hipLaunchKernel(k, dim3((uint32_t)grid), dim3((uint32_t)threads), args, 0, stream) ==
                    hipSuccess
@@ -136,17 +179,16 @@ static int launch_norm(const NormArgs& a, int threads, hipStream_t stream) {
                : kFailed;
 }
 
-// The fewest slots per thread that 1024 threads reach, and no more threads
-// than the row has slots.
 template <int DT>
 int norm_launch(const NormArgs& a, hipStream_t stream) {
-    const int slots = (a.cols + Elem<DT>::V - 1) / Elem<DT>::V;
-    int per = 1;
+    constexpr int V = Elem<DT>::V;
+    const int slots = (a.cols + V - 1) / V;
+    int per = 16 / V;  // 16 elements a thread
     while (slots > per * 1024) per *= 2;
-    const int threads = ((slots + per - 1) / per + 63) / 64 * 64;
+    const int threads = slot_threads(slots, per);
     if (per == 1) return launch_norm<DT, 1>(a, threads, stream);
     if (per == 2) return launch_norm<DT, 2>(a, threads, stream);
-    if constexpr (Elem<DT>::V == 4) {
+    if constexpr (V == 4) {
         if (per == 4) return launch_norm<DT, 4>(a, threads, stream);
     }
     return kFailed;  // more than PTORED_BLOCK_MAX_COLS columns

@@ -45,7 +45,7 @@ struct GradArgs {
     Kept kx, kh;
     const char *w1, *w2;
     const float *r1, *r2;
-    float* ws;              // partial sums: [chunk][which][cols], see grad_split()
+    float* ws;              // partial sums: [chunk][which][ws_pitch]
     char *dw1, *dw2;
     int64_t unit_rows;      // rows are cut into units of this many ...
     int64_t chunks_per_unit;  // ... and each unit into this many chunks ...
@@ -53,6 +53,8 @@ struct GradArgs {
     int64_t chunks;
     int64_t gate_rows;
     int64_t rows_per_gate;
+    int64_t ws_pitch;     // the columns, rounded up to whole vectors of 4
+    int32_t chunk_gates;  // gate rows that a chunk can touch
     int32_t gate_direct;  // 1: whole gate rows lie inside chunks, which write them at once
     int32_t ws_slots;     // partial rows per chunk: dw1, dw2 and, without gate_direct, dgate
     int32_t slot_w2, slot_gate;  // position of dw2's and dgate's (dw1's is 0); -1: none
@@ -89,6 +91,7 @@ struct WgradArgs {
     int32_t splits;
     int32_t dw_f32, accumulate;
     int32_t tiles_m, tiles_n;
+    int32_t wide;  // 1: tiles of 256 x 256, 0: of 128 x 128
 };
 
 enum : int { kOk = 0, kFailed = 1 };

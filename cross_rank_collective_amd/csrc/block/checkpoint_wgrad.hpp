@@ -20,16 +20,18 @@
 // banks.
 #pragma once
 
+#include <type_traits>
+
 #include "block_device.hpp"
 
 namespace ptored {
 namespace block {
 
+constexpr int kStep = 32;  // tokens staged at a time
+
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-
-constexpr int kStep = 64;  // tokens staged at a time
 
 template <int DT>
 constexpr int planes_of() {
@@ -43,30 +45,44 @@ struct DyChunk {
     u32x4 w[DT == PTORED_F32 ? 2 : 1];
 };
 
+// An edge chunk's elements from where they were loaded to their places, `n`
+// bytes on.
 template <int DT>
-__device__ __forceinline__ DyChunk<DT> load_dy(const char* row, int col, int cols, bool in) {
-    using E = Elem<DT>;
-    DyChunk<DT> c;
-    const char* p = row + (int64_t)col * E::kBytes;
-    if (in && col + 8 <= cols) {
-        c.w[0] = *reinterpret_cast<const u32x4_any*>(p);
-        if constexpr (DT == PTORED_F32) c.w[1] = *reinterpret_cast<const u32x4_any*>(p + 16);
-        return c;
-    }
-    uint32_t w[DT == PTORED_F32 ? 8 : 4] = {};
-    if (in) {
+__device__ __forceinline__ void move_up(DyChunk<DT>& c, int n) {
+    if constexpr (DT == PTORED_F32) {  // whole words, over 32 bytes
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (col + i >= cols) continue;
-            if constexpr (DT == PTORED_F32)
-                w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-            else
-                w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+        for (int b = 16; b >= 4; b /= 2) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t far = i + b / 4 < 8 ? c.w[(i + b / 4) / 4 % 2][(i + b / 4) % 4] : 0u;
+                w[i] = n & b ? far : c.w[i / 4][i % 4];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c.w[i / 4][i % 4] = w[i];
         }
+    } else {
+        c.w[0] = shift_down(c.w[0], n);
     }
-    c.w[0] = (u32x4){w[0], w[1], w[2], w[3]};
-    if constexpr (DT == PTORED_F32) c.w[1] = (u32x4){w[4], w[5], w[6], w[7]};
-    return c;
+}
+
+// The `n` elements of ES bytes at `p`, fewer than a chunk has, zeros behind.
+template <int ES>
+__device__ __forceinline__ void load_few(const char* p, int n, u32x4* w) {
+    constexpr int kCount = ES == 1 ? 16 : 8;
+    uint32_t u[kCount * ES / 4] = {};
+#pragma unroll
+    for (int i = 0; i < kCount - 1; ++i) {
+        if (i >= n) continue;
+        if constexpr (ES == 4)
+            u[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else if constexpr (ES == 2)
+            u[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+        else
+            u[i / 4] |= (uint32_t) reinterpret_cast<const uint8_t*>(p)[i] << (8 * (i % 4));
+    }
+#pragma unroll
+    for (int i = 0; i < kCount * ES / 4; ++i) w[i / 4][i % 4] = u[i];
 }
 
 // Upper halves of two words, lo's first.
@@ -106,31 +122,11 @@ __device__ __forceinline__ void split_dy(const DyChunk<DT>& c, u32x4* plane) {
     }
 }
 
-// 16 packed values of one block and their factor.
+// 16 packed values of one block and its scale byte.
 struct KeptChunk {
     u32x4 w;
     uint32_t scale;
 };
-
-__device__ __forceinline__ KeptChunk load_kept(const Kept& k, int64_t row, int col, int cols,
-                                               bool in) {
-    KeptChunk c;
-    c.w = (u32x4){0, 0, 0, 0};
-    c.scale = 127;
-    if (!in || col >= cols) return c;
-    const int8_t* q = k.q + row * k.q_ld + col;
-    c.scale = k.s[row * k.s_ld + col / PTORED_CHECKPOINT_BLOCK];
-    if (col + 16 <= cols) {
-        c.w = *reinterpret_cast<const u32x4_any*>(q);
-    } else {
-        uint32_t w[4] = {};
-#pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (col + i < cols) w[i / 4] |= (uint32_t)(uint8_t)q[i] << (8 * (i % 4));
-        c.w = (u32x4){w[0], w[1], w[2], w[3]};
-    }
-    return c;
-}
 
 // The chunk's values as bfloat16 (exact: at most 8 significant bits).
 __device__ __forceinline__ void widen_kept(const KeptChunk& c, u32x4* out) {
@@ -162,59 +158,128 @@ __device__ __forceinline__ b8 read_fragment(const char* tile, int t0, int piece,
         b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Waves WM x WN, each computing TM x TN blocks of 32 x 32.
-template <int DT, int WM, int WN, int TM, int TN>
+// Waves WM x WN, each computing TM x TN blocks of 32 x 32.  EDGE: rows of dy or
+// of x do not end with a whole chunk.
+template <int DT, int WM, int WN, int TM, int TN, bool EDGE>
 __global__ __launch_bounds__(WM* WN * 64) void wgrad_kernel(const WgradArgs a) {
+    constexpr int STEP = kStep;
     constexpr int kThreads = WM * WN * 64;
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
     constexpr int P = planes_of<DT>();
     constexpr int kRowA = BM * 2, kRowB = BN * 2;
-    constexpr int kBytesA = kStep * kRowA, kBytesB = kStep * kRowB;
-    constexpr int kChunksA = kStep * BM / 8 / kThreads, kChunksB = kStep * BN / 16 / kThreads;
-    static_assert(kChunksA * kThreads * 8 == kStep * BM && kChunksB * kThreads * 16 == kStep * BN,
+    constexpr int kBytesA = STEP * kRowA, kBytesB = STEP * kRowB;
+    constexpr int kBytes = P * kBytesA + kBytesB;
+    constexpr int kChunksA = STEP * BM / 8 / kThreads, kChunksB = STEP * BN / 16 / kThreads;
+    constexpr int kRowsA = kThreads / (BM / 8), kRowsB = kThreads / (BN / 16);
+    static_assert(kChunksA * kRowsA == STEP && kChunksB * kRowsB == STEP,
                   "whole chunks per thread");
-    __shared__ __attribute__((aligned(128))) char lds[2][P * kBytesA + kBytesB];
+    static_assert(kRowsA % 4 == 0 && kRowsB % 4 == 0, "a thread's rows share their swizzle");
+    __shared__ __attribute__((aligned(128))) char lds[3 * kBytes];
 
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int tile = (int)(blockIdx.x % (uint32_t)(a.tiles_m * a.tiles_n));
-    const int split = (int)(blockIdx.x / (uint32_t)(a.tiles_m * a.tiles_n));
-    const int m0 = tile / a.tiles_n * BM, n0 = tile % a.tiles_n * BN;
+    // Workgroups go to the 8 dies in turn: each die gets consecutive tiles of
+    // the order in which 4 rows of tiles advance together, so that its cache
+    // serves most reads of both operands.
+    const int tiles = a.tiles_m * a.tiles_n;
+    const int total = tiles * a.splits;
+    int id = (int)blockIdx.x;
+    {
+        const int die = id % 8, each = total / 8, rest = total % 8;
+        id = die * each + (die < rest ? die : rest) + id / 8;
+    }
+    const int split = id / tiles, in_split = id % tiles;
+    const int band = in_split / (4 * a.tiles_n), band_rows = min(4, a.tiles_m - band * 4);
+    const int in_band = in_split - band * 4 * a.tiles_n;
+    const int m0 = (band * 4 + in_band % band_rows) * BM, n0 = in_band / band_rows * BN;
     const int64_t begin = split * a.rows_per_split;
     const int64_t end = begin + a.rows_per_split < a.rows ? begin + a.rows_per_split : a.rows;
+    const int steps = 2 * (int)((end - begin + 2 * STEP - 1) / (2 * STEP));
 
-    DyChunk<DT> dy[kChunksA];
-    KeptChunk kept[kChunksB];
-    auto fetch = [&](int64_t t0) {
+    // This thread's chunks of a step: rows tA + c kRowsA of dy, tB + c kRowsB
+    // of x.  A chunk that would pass the end of a row is loaded from the row's
+    // last whole chunk instead: what lies past the end is not stored, and with
+    // EDGE the elements before it are moved to their places (shA, shB).
+    using E = Elem<DT>;
+    const int tA = tid / (BM / 8), colA = m0 + tid % (BM / 8) * 8;
+    const int tB = tid / (BN / 16), colB = n0 + tid % (BN / 16) * 16;
+    const int fromA = min(colA, max(a.outs - 8, 0)), fromB = min(colB, max(a.cols - 16, 0));
+    const char* pa = a.dy + (begin + tA) * a.dy_ld + (int64_t)fromA * E::kBytes;
+    const int8_t* pq = a.x.q + (begin + tB) * a.x.q_ld + fromB;
+    const uint8_t* ps =
+        a.x.s + (begin + tB) * a.x.s_ld + min(colB, a.cols - 1) / PTORED_CHECKPOINT_BLOCK;
+    const int shA = min(colA - fromA, 7) * E::kBytes, shB = min(colB - fromB, 15);
+
+    struct Tokens {
+        DyChunk<DT> dy[kChunksA];
+        KeptChunk kept[kChunksB];
+    };
+    Tokens set0, set1;
+    // Loads the next tokens, STEP of them unless FIRST.
+    int64_t rowsA = kRowsA * a.dy_ld, rowsQ = kRowsB * a.x.q_ld, rowsS = kRowsB * a.x.s_ld;
+    auto fetch = [&](auto first, Tokens& set, int tokens) {
+        constexpr bool FIRST = decltype(first)::value;
 #pragma unroll
         for (int c = 0; c < kChunksA; ++c) {
-            const int n = c * kThreads + tid, t = n / (BM / 8), col = m0 + n % (BM / 8) * 8;
-            dy[c] = load_dy<DT>(a.dy + (t0 + t) * a.dy_ld, col, a.outs, t0 + t < end);
+            const char* p = pa + c * rowsA;
+            set.dy[c] = DyChunk<DT>{};
+            if (FIRST && tA + c * kRowsA >= tokens) continue;
+            if (EDGE && a.outs < 8) {
+                load_few<E::kBytes>(p, a.outs, set.dy[c].w);
+            } else {
+                set.dy[c].w[0] = *reinterpret_cast<const u32x4_any*>(p);
+                if constexpr (DT == PTORED_F32)
+                    set.dy[c].w[1] = *reinterpret_cast<const u32x4_any*>(p + 16);
+            }
         }
 #pragma unroll
         for (int c = 0; c < kChunksB; ++c) {
-            const int n = c * kThreads + tid, t = n / (BN / 16), col = n0 + n % (BN / 16) * 16;
-            kept[c] = load_kept(a.x, t0 + t, col, a.cols, t0 + t < end);
+            set.kept[c] = KeptChunk{(u32x4)(0u), 127u};
+            if (FIRST && tB + c * kRowsB >= tokens) continue;
+            const int8_t* q = pq + c * rowsQ;
+            if (EDGE && a.cols < 16)
+                load_few<1>(reinterpret_cast<const char*>(q), a.cols, &set.kept[c].w);
+            else
+                set.kept[c].w = *reinterpret_cast<const u32x4_any*>(q);
+            set.kept[c].scale = ps[c * rowsS];
         }
     };
-    auto stage = [&](char* buf) {
+    auto advance = [&](int64_t tokens) {
+        pa += tokens * a.dy_ld;
+        pq += tokens * a.x.q_ld;
+        ps += tokens * a.x.s_ld;
+    };
+    const int atA = lds_chunk(tA, tid % (BM / 8), kRowA);
+    const int atB0 = lds_chunk(tB, tid % (BN / 16) * 2, kRowB);
+    const int atB1 = lds_chunk(tB, tid % (BN / 16) * 2 + 1, kRowB);
+    auto stage_a = [&](Tokens& set, char* buf, int c) {
+        u32x4 plane[P];
+        if constexpr (EDGE) move_up<DT>(set.dy[c], shA);
+        split_dy<DT>(set.dy[c], plane);
 #pragma unroll
-        for (int c = 0; c < kChunksA; ++c) {
-            const int n = c * kThreads + tid, t = n / (BM / 8), at = n % (BM / 8);
-            u32x4 plane[P];
-            split_dy<DT>(dy[c], plane);
+        for (int p = 0; p < P; ++p)
+            *reinterpret_cast<u32x4*>(buf + p * kBytesA + c * kRowsA * kRowA + atA) = plane[p];
+    };
+    auto stage_b = [&](Tokens& set, char* buf, int c) {
+        u32x4 v[2];
+        // keeps the unpacking here: right after the loads it would wait for them
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                *reinterpret_cast<u32x4*>(buf + p * kBytesA + lds_chunk(t, at, kRowA)) = plane[p];
+        for (int i = 0; i < 4; ++i) {
+            uint32_t u = set.kept[c].w[i];
+            asm volatile("" : "+v"(u));
+            set.kept[c].w[i] = u;
         }
+        asm volatile("" : "+v"(set.kept[c].scale));
+        if constexpr (EDGE) set.kept[c].w = shift_down(set.kept[c].w, shB);
+        widen_kept(set.kept[c], v);
+        char* at = buf + P * kBytesA + c * kRowsB * kRowB;
+        *reinterpret_cast<u32x4*>(at + atB0) = v[0];
+        *reinterpret_cast<u32x4*>(at + atB1) = v[1];
+    };
+    auto stage = [&](Tokens& set, char* buf) {
 #pragma unroll
-        for (int c = 0; c < kChunksB; ++c) {
-            const int n = c * kThreads + tid, t = n / (BN / 16), at = n % (BN / 16) * 2;
-            u32x4 v[2];
-            widen_kept(kept[c], v);
+        for (int c = 0; c < kChunksA; ++c) stage_a(set, buf, c);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<u32x4*>(buf + P * kBytesA + lds_chunk(t, at + i, kRowB)) = v[i];
-        }
+        for (int c = 0; c < kChunksB; ++c) stage_b(set, buf, c);
     };
 
     f32x16 acc[TM][TN];
@@ -224,37 +289,108 @@ __global__ __launch_bounds__(WM* WN * 64) void wgrad_kernel(const WgradArgs a) {
         for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16)(0.0f);
     const int pm = wave / WN * TM, pn = wave % WN * TN;  // the wave's 64-byte pieces
 
-    // One barrier a step: a buffer is written again only after the barrier
-    // that every wave reaches once it has read it.
-    if (begin < end) {
-        fetch(begin);
-        stage(lds[0]);
-    }
-    int cur = 0;
-    for (int64_t t0 = begin; t0 < end; t0 += kStep, cur ^= 1) {
-        __syncthreads();
-        const bool more = t0 + kStep < end;
-        if (more) fetch(t0 + kStep);
-        const char* buf = lds[cur];
+    struct Fragments {
+        b8 a[P][TM], b[TN];
+    };
+    auto read = [&](const char* buf, int k, Fragments& f) {
 #pragma unroll
-        for (int k = 0; k < kStep; k += 16) {
-            b8 fb[TN];
+        for (int j = 0; j < TN; ++j)
+            f.b[j] = read_fragment(buf + P * kBytesA, k * 16, pn + j, kRowB);
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                fb[j] = read_fragment(buf + P * kBytesA, k, pn + j, kRowB);
+        for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
+            for (int i = 0; i < TM; ++i)
+                f.a[p][i] = read_fragment(buf + p * kBytesA, k * 16, pm + i, kRowA);
+    };
+    auto multiply = [&](const Fragments& f) {
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const b8 fa = read_fragment(buf + p * kBytesA, k, pm + i, kRowA);
+        for (int p = 0; p < P; ++p)
 #pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[j], acc[i][j],
-                                                                           0, 0, 0);
-                }
-            }
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[p][i], f.b[j],
+                                                                       acc[i][j], 0, 0, 0);
+    };
+
+    // The pipeline, in steps of 32 tokens: loaded into registers four steps
+    // ahead, staged in one of three buffers two steps ahead, read as fragments
+    // 16 tokens ahead.  One barrier a step, between its halves: behind it the
+    // next step's buffer, staged in the last step, is whole, and the one that
+    // the next step stages into has been read.  (Past the last step stale
+    // registers are staged and read; nothing uses them.)
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
+    Fragments even, odd;
+    char *b0 = lds, *b1 = lds + kBytes, *b2 = lds + 2 * kBytes;
+    // The order of a half's instructions: the fragments' reads between the
+    // first products, the arithmetic of the staging spread over all of them.
+    auto order = [] {
+#pragma unroll
+        for (int i = 0; i < P * TM * TN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);  // vector arithmetic
         }
-        if (more) stage(lds[cur ^ 1]);
+    };
+    auto step = [&](Tokens& set, bool more) {
+        __builtin_amdgcn_sched_barrier(0);
+        read(b0, 1, odd);
+        multiply(even);
+#pragma unroll
+        for (int c = 0; c < kChunksB; ++c) stage_b(set, b2, c);
+        stage_a(set, b2, 0);
+        order();
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        read(b1, 0, even);
+        multiply(odd);
+#pragma unroll
+        for (int c = 1; c < kChunksA; ++c) stage_a(set, b2, c);
+        fetch(No{}, set, STEP);
+        pa += more ? a.dy_ld * STEP : 0;
+        pq += more ? a.x.q_ld * STEP : 0;
+        ps += more ? a.x.s_ld * STEP : 0;
+        order();
+        __builtin_amdgcn_sched_barrier(0);
+        char* t = b0;
+        b0 = b1;
+        b1 = b2;
+        b2 = t;
+    };
+    // The first two steps take what does not fill two whole ones (perhaps only
+    // the second does anything).
+    const int some = (int)(end - begin - (int64_t)(steps - 2) * STEP);  // 1 to 2 STEP
+    const int first = some > STEP ? some - STEP : 0;
+    fetch(Yes{}, set0, first);
+    advance(first);
+    fetch(Yes{}, set1, some - first);
+    stage(set0, b0);
+    stage(set1, b1);
+    if (steps > 2) {
+        advance(some - first);
+    } else {  // nothing is left to load; what the loop loads is the first row, unused
+        advance(-first);
+        pa -= tA * a.dy_ld;
+        pq -= tB * a.x.q_ld;
+        ps -= tB * a.x.s_ld;
+        rowsA = rowsQ = rowsS = 0;
+    }
+    fetch(No{}, set0, STEP);
+    advance(steps > 3 ? STEP : 0);
+    fetch(No{}, set1, STEP);
+    advance(steps > 4 ? STEP : 0);
+#pragma unroll
+    for (int c = 0; c < kChunksB; ++c) {  // in registers as words, not as bytes to widen at the loop's top
+        asm volatile("" : "+v"(set0.kept[c].scale));
+        asm volatile("" : "+v"(set1.kept[c].scale));
+    }
+    __syncthreads();
+    read(b0, 0, even);
+    for (int s = 0; s < steps; s += 2) {
+        step(set0, s + 5 < steps);
+        step(set1, s + 6 < steps);
     }
 
     // Register r of a 32 x 32 block is row 8 (r / 4) + 4 (lane / 32) + r % 4,
@@ -307,13 +443,22 @@ __global__ __launch_bounds__(kJoinThreads) void wgrad_join_kernel(const WgradArg
     }
 }
 
+template <int DT, int WM, int WN, int TM, int TN>
+static const void* wgrad_pick(const WgradArgs& a) {
+    const bool edge = a.outs % 8 != 0 || a.cols % 16 != 0;
+    return edge ? reinterpret_cast<const void*>(wgrad_kernel<DT, WM, WN, TM, TN, true>)
+                : reinterpret_cast<const void*>(wgrad_kernel<DT, WM, WN, TM, TN, false>);
+}
+
 template <int DT>
 int wgrad_launch(const WgradArgs& a, hipStream_t stream) {
     void* args[] = {const_cast<WgradArgs*>(&a)};
     if (a.splits > 0) {
         const dim3 grid((uint32_t)(a.tiles_m * a.tiles_n) * (uint32_t)a.splits);
-        const void* k = reinterpret_cast<const void*>(wgrad_kernel<DT, 2, 2, 2, 2>);
-        if (hipLaunchKernel(k, grid, dim3(256), args, 0, stream) != hipSuccess) return kFailed;
+        const void* k = a.wide ? wgrad_pick<DT, 2, 4, DT == PTORED_F32 ? 2 : 4, 2>(a)
+                               : wgrad_pick<DT, 2, 2, 2, 2>(a);
+        if (hipLaunchKernel(k, grid, dim3(a.wide ? 512 : 256), args, 0, stream) != hipSuccess)
+            return kFailed;
     }
     if (a.splits == 1) return kOk;
     const int64_t n = (int64_t)a.outs * a.cols;

@@ -151,6 +151,17 @@ inline int edge_of(int cols) {
     return cols % V == 0 ? kWhole : cols > V ? kPart : kTiny;
 }
 
+// The kernel's arguments, through a pointer that the compiler cannot tell from
+// another, so that it loads them where they are used and keeps none of them in
+// scalar registers until then.
+template <typename A>
+__device__ __forceinline__ const A& args_again() {
+    typedef const __attribute__((address_space(4))) A* constant_ptr;
+    auto p = (constant_ptr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const A*)p;
+}
+
 // A packed slot as loaded: V values and their block's scale byte.
 struct KeptRaw {
     u32x2 q;
@@ -381,13 +392,15 @@ __device__ __forceinline__ void block_sum(f32x4 (*red)[kMaxWaves / 4], float* v)
 __device__ __forceinline__ float power_of_2(int n) { return as_f((uint32_t)(n + 127) << 23); }
 
 // Largest magnitude of a block of 32 elements, as bits, in all its lanes: a
-// block is 4 lanes of 8 elements or 8 lanes of 4.  Bit patterns of
-// non-negative floats compare like the values, infinities and NaN above all.
+// block is 4 lanes of 8 elements or 8 lanes of 4.  The maximum is IEEE 754's,
+// which a NaN passes through; bit patterns of non-negative floats compare like
+// the values, infinities and NaN above all.
 template <int V>
 __device__ __forceinline__ uint32_t block_amax(const float* v) {
-    uint32_t m = 0;
+    float t = __builtin_fabsf(v[0]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = max(m, as_u(v[i]) & 0x7FFFFFFFu);
+    for (int i = 1; i < V; ++i) t = __builtin_elementwise_maximum(t, __builtin_fabsf(v[i]));
+    uint32_t m = as_u(t) & 0x7FFFFFFFu;
     m = max(m, dpp<kDppXor1>(m));
     m = max(m, dpp<kDppXor2>(m));
     if constexpr (V == 4) m = max(m, dpp<kDppHalfMirror>(m));

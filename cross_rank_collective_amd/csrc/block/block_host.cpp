@@ -118,16 +118,18 @@ int status_of(int rc) { return rc == kOk ? PTORED_OK : PTORED_ERR_HIP; }
      : (dtype) == PTORED_BF16 ? f##_bf16(__VA_ARGS__)            \
                               : f##_f16(__VA_ARGS__))
 
-// The backward pass keeps 16 waves on every compute unit, each wave 512
-// columns wide, and cuts the rows into as many chunks as that makes
-// workgroups: the partial rows they leave (8 bytes a column, written and
-// read) are then a small part of the rows' own bytes.
-constexpr int64_t kGradWaves = 4096;
-
-GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows) {
+// The backward pass cuts the rows into as many chunks as there are workgroups
+// at once on the chip: with fewer, compute units idle; with more, the last
+// ones run alone and the partial rows that chunks leave (8 bytes a column,
+// written and read) grow.  A wave is 64 slots wide; its registers leave room
+// for 16 waves of 8-element slots on a compute unit and for 20 of 4.
+GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows, int dtype,
+                     bool in_order = false) {
     GradSplit s{};
     if (rows == 0) return s;
-    const int64_t target = std::max<int64_t>(1, kGradWaves / ((cols + 511) / 512));
+    const int64_t slot = dtype == PTORED_F32 ? 4 : 8, room = dtype == PTORED_F32 ? 20 : 16;
+    const int64_t waves = std::min<int64_t>(16, (cols + 64 * slot - 1) / (64 * slot));
+    const int64_t target = 256 * (room / waves);
     const int64_t per = (rows + target - 1) / target;
     const int64_t unit = gate_rows > 0 ? rows / gate_rows : rows;
     if (gate_rows > 0 && unit <= per) {  // whole gate rows inside a chunk
@@ -135,6 +137,8 @@ GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows) {
         s.chunk_rows = per / unit * unit;
         s.chunks_per_unit = (rows + s.chunk_rows - 1) / s.chunk_rows;
         s.chunks = s.chunks_per_unit;
+        s.chunk_first = unit == 1 ? 1 : s.chunk_rows;
+        s.row_step = unit == 1 ? s.chunks : 1;
         s.gate_direct = 1;
         return s;
     }
@@ -142,6 +146,8 @@ GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows) {
     s.chunks_per_unit = (unit + per - 1) / per;
     s.chunk_rows = (unit + s.chunks_per_unit - 1) / s.chunks_per_unit;
     s.chunks = rows / unit * s.chunks_per_unit;
+    s.chunk_first = in_order ? s.chunk_rows : 1;
+    s.row_step = in_order ? 1 : s.chunks_per_unit;
     return s;
 }
 
@@ -268,7 +274,9 @@ extern "C" int ptored_block_norm_backward_workspace(int64_t rows, int64_t cols, 
         (gate_rows > 0 && rows % gate_rows != 0))
         return PTORED_ERR_INVALID_ARG;
     if (cols > PTORED_BLOCK_MAX_COLS) return PTORED_ERR_UNSUPPORTED;
-    *bytes = grad_workspace(cols, gate_rows, grad_split(rows, cols, gate_rows));
+    // of any type
+    *bytes = std::max(grad_workspace(cols, gate_rows, grad_split(rows, cols, gate_rows, PTORED_F32)),
+                      grad_workspace(cols, gate_rows, grad_split(rows, cols, gate_rows, PTORED_BF16)));
     return PTORED_OK;
 }
 
@@ -311,7 +319,9 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     b.vec(io->dpre_weight, p.cols * ws, ws, true);
 
     const bool gated = io->dgate.data != nullptr;
-    const GradSplit split = grad_split(p.rows, p.cols, gated ? p.gate_rows : 0);
+    // gate rows without a gradient: a chunk that walks several takes them in order
+    const bool in_order = !gated && p.gate.data && p.gate_rows > 1 && p.gate_rows < p.rows;
+    const GradSplit split = grad_split(p.rows, p.cols, gated ? p.gate_rows : 0, p.dtype, in_order);
     const bool partial_gate = gated && !split.gate_direct;
     GradArgs a{};
     a.slot_w1 = a.slot_w2 = a.slot_gate = -1;
@@ -349,12 +359,18 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     a.unit_rows = split.unit_rows;
     a.chunks_per_unit = split.chunks_per_unit;
     a.chunk_rows = split.chunk_rows;
+    a.chunk_first = split.chunk_first;
+    a.row_step = split.row_step;
     a.chunks = split.chunks;
     a.gate_direct = split.gate_direct;
     a.gate_rows = p.gate_rows;
     a.rows_per_gate = p.gate.data ? p.rows / p.gate_rows : p.rows;
-    // a chunk begins with a gate row unless that row's gradient is not wanted
-    a.chunk_gates = split.chunk_rows <= a.rows_per_gate && (gated || p.gate_rows <= 1) ? 1 : 2;
+    // with its gradient wanted, a chunk lies within a gate row or begins with one
+    a.chunk_gates = p.gate_rows <= 1 || (gated && split.chunk_rows <= a.rows_per_gate &&
+                                         !(split.row_step > 1 && split.gate_direct))
+                        ? kOneGate
+                    : a.rows_per_gate == 1 ? kEachGate
+                                           : kSomeGates;
     a.w_f32 = p.weight_dtype == PTORED_F32;
     a.offset = p.weight_offset;
     a.alpha = p.branch_scale;

@@ -35,25 +35,25 @@ struct Activation<true> {
     KeptRaw w;
 };
 
-// MANY: a chunk holds several gate rows; otherwise A alone tells their
-// gradients at the chunk's end.
-template <int DT, int S, int EDGE, bool PACKED, bool MANY>
+// With one gate row in the chunk (GATES), A tells its gradients at the end.
+template <int DT, int S, int EDGE, bool PACKED, int GATES>
 __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
     using E = Elem<DT>;
     constexpr int V = E::V;
     // Up to 8 elements a thread, the factors that rows share stay in registers
     // and the next row is loaded ahead; with more neither fits.
     constexpr bool HOLD = S * V <= 8;
+    constexpr bool MANY = GATES != kOneGate, EACH = GATES == kEachGate;
     typedef Slots<DT, S, EDGE> Row;
     __shared__ f32x4 red[2][3][kMaxWaves / 4];
     const Row t(a.cols);
     const int64_t chunk = blockIdx.x;
     const int64_t unit = chunk / a.chunks_per_unit;
-    const int64_t begin = unit * a.unit_rows + (chunk - unit * a.chunks_per_unit) * a.chunk_rows;
-    const int64_t unit_end = (unit + 1) * a.unit_rows;
-    const int64_t end = begin + a.chunk_rows < unit_end ? begin + a.chunk_rows : unit_end;
+    const int64_t part = chunk - unit * a.chunks_per_unit;
+    const int64_t begin = unit * a.unit_rows + part * a.chunk_first;
+    const int64_t left = a.unit_rows - part * a.chunk_first;
+    const int rows = (int)min(a.chunk_rows, (left + a.row_step - 1) / a.row_step);
     const bool pre = a.w2 != nullptr, post = a.w1 != nullptr, gated = a.gate.p != nullptr;
-    const bool has_h = PACKED ? a.kh.q != nullptr : a.h.p != nullptr;
 
     // what a row is made of, as loaded; absent rows read as zeros
     struct Raw {
@@ -61,31 +61,59 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
         Activation<PACKED> x[S], h[S];
         float r1, r2;
     };
-    auto activation = [&](const Mat& m, const Kept& k, int64_t row, bool there,
-                          Activation<PACKED>* to) {
-        if constexpr (PACKED) {
-            typename Row::KeptRow r = t.kept_row(k, there ? row : 0);
-            if (!there) r.q = r.s = row_rsrc(nullptr, 0);
-#pragma unroll
-            for (int s = 0; s < S; ++s) to[s].w = t.load_kept(r, s);
-        } else {
-            const rsrc_t r = there ? t.row(m.p + row * m.ld) : row_rsrc(nullptr, 0);
-#pragma unroll
-            for (int s = 0; s < S; ++s) to[s].w = t.load(r, s);
-        }
+    // The row's place in a matrix, advanced from row to row.
+    struct Place {
+        const char* p;
+        int64_t ld;
     };
-    auto load = [&](int64_t row, Raw& to) {
-        const rsrc_t dz = pre ? t.row(a.dz.p + row * a.dz.ld) : row_rsrc(nullptr, 0);
-        const rsrc_t dxo = a.dxo.p ? t.row(a.dxo.p + row * a.dxo.ld) : row_rsrc(nullptr, 0);
+    auto place = [&](const void* p, int64_t ld) -> Place {
+        return {static_cast<const char*>(p) + begin * ld, ld * a.row_step};
+    };
+    const int row_bytes = a.cols * E::kBytes, kept_bytes = PACKED ? a.cols : row_bytes;
+    const int blocks = (a.cols + PTORED_CHECKPOINT_BLOCK - 1) / PTORED_CHECKPOINT_BLOCK;
+    Place dz = place(a.dz.p, a.dz.ld), dxi = place(a.dxo.p, a.dxo.ld);
+    Place x0 = PACKED ? place(a.kx.q, a.kx.q_ld) : place(a.x.p, a.x.ld);
+    Place h0 = PACKED ? place(a.kh.q, a.kh.q_ld) : place(a.h.p, a.h.ld);
+    Place xs = place(a.kx.s, a.kx.s_ld), hs = place(a.kh.s, a.kh.s_ld);
+    Place dxp = place(a.dx.p, a.dx.ld), dhp = place(a.dh.p, a.dh.ld);
+    // what there is of them; an absent matrix has rows of no bytes
+    enum : uint32_t { kDz = 1, kDxo = 2, kX = 4, kH = 8, kDx = 16, kDh = 32, kRead = 15 };
+    uint32_t there = (pre ? kDz | kX : 0) | (a.dxo.p ? kDxo : 0) | (a.dx.p ? kDx : 0) |
+                     (a.dh.p ? kDh : 0) |
+                     ((PACKED ? a.kh.q != nullptr : a.h.p != nullptr) ? kH : 0);
+    auto next_row = [&](Place& m, uint32_t which, int bytes) {
+        const rsrc_t r = row_rsrc(m.p, there & which ? bytes : 0);
+        m.p += m.ld;
+        return r;
+    };
+    // Loads the next row, or nothing past the chunk's last.
+    auto load = [&](int row, Raw& to) {
+        if (row >= rows) there &= ~kRead;
+        const rsrc_t z = next_row(dz, kDz, row_bytes), d = next_row(dxi, kDxo, row_bytes);
+        const rsrc_t x = next_row(x0, kX, kept_bytes), h = next_row(h0, kH, kept_bytes);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            to.dz[s] = t.load(dz, s);
-            to.dxo[s] = t.load(dxo, s);
+            to.dz[s] = t.load(z, s);
+            to.dxo[s] = t.load(d, s);
         }
-        activation(a.x, a.kx, row, pre, to.x);
-        activation(a.h, a.kh, row, has_h, to.h);
-        to.r2 = pre ? a.r2[row] : 0.0f;
-        to.r1 = post ? a.r1[row] : 1.0f;
+        if constexpr (PACKED) {
+            const typename Row::KeptRow kx = {x, next_row(xs, kX, blocks)};
+            const typename Row::KeptRow kh = {h, next_row(hs, kH, blocks)};
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                to.x[s].w = t.load_kept(kx, s);
+                to.h[s].w = t.load_kept(kh, s);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                to.x[s].w = t.load(x, s);
+                to.h[s].w = t.load(h, s);
+            }
+        }
+        const int64_t at = begin + (row < rows ? row : 0) * a.row_step;
+        to.r2 = pre ? a.r2[at] : 0.0f;
+        to.r1 = post ? a.r1[at] : 1.0f;
     };
     // an activation times its row's reciprocal norm
     auto take = [&](const Activation<PACKED>& w, int s, float by, float* v) {
@@ -122,8 +150,9 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
     };
 
     int64_t gate_row = gated ? begin / a.rows_per_gate : 0;
-    int64_t gate_end = MANY ? (gate_row + 1) * a.rows_per_gate : end;
-    u32x4 gate[S];  // MANY: of the next row, where that begins a gate row
+    // the rows up to here share the gate row
+    int64_t gate_end = !MANY ? rows : a.row_step > 1 ? 1 : (gate_row + 1) * a.rows_per_gate - begin;
+    u32x4 gate[S];  // of the next row, where that begins a gate row
     if (gated) load_gate(gate_row, gate);
     // HOLD: w2 + o; alpha g; alpha g (w1 + o), or with MANY w1 + o
     float w2[S][V], ag[S][V], kw[S][V];
@@ -139,9 +168,14 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
             }
         }
     }
+    u32x4 gate_now[S];  // EACH: of the current row
     // alpha g (w1 + o) of the current row
     auto scale = [&](int s, float* v) {
-        if constexpr (!HOLD) {
+        if constexpr (HOLD && EACH) {
+            take_gate(gate_now, s, v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] *= kw[s][i];
+        } else if constexpr (!HOLD) {
             float g[V];
             weight(a.w1, s, v);
             take_gate(gate, s, g);
@@ -159,28 +193,29 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
         for (int i = 0; i < V; ++i) sw1[s][i] = sw2[s][i] = sa[s][i] = 0.0f;
 
     int turn = 0;
-    Raw next;
-    if constexpr (HOLD) load(begin, next);
     bool fresh = MANY;  // the row begins a gate row, or the chunk
-    for (int64_t row = begin; row < end; ++row, turn ^= 1) {
+    auto one_row = [&](int row, Raw& raw) {
         if constexpr (!HOLD) {
-            load(row, next);
+            load(row, raw);
             if (MANY && fresh) load_gate(gate_row, gate);
         }
-        if (HOLD && MANY && fresh) {
+        if constexpr (HOLD && EACH) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) gate_now[s] = gate[s];
+        } else if (HOLD && MANY && fresh) {
 #pragma unroll
             for (int s = 0; s < S; ++s) take_gate(gate, s, ag[s]);
         }
-        const float r1 = next.r1, r2 = next.r2;
+        const float r1 = raw.r1, r2 = raw.r2;
         float dxo[S][V], xh[S][V], hh[S][V];
         float sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float u[V], k[V];
-            t.take(next.dz[s], s, u);
-            t.take(next.dxo[s], s, dxo[s]);
-            take(next.x[s], s, r2, xh[s]);
-            take(next.h[s], s, r1, hh[s]);
+            t.take(raw.dz[s], s, u);
+            t.take(raw.dxo[s], s, dxo[s]);
+            take(raw.x[s], s, r2, xh[s]);
+            take(raw.h[s], s, r1, hh[s]);
             scale(s, k);
             if constexpr (!HOLD) weight(a.w2, s, w2[s]);
 #pragma unroll
@@ -195,26 +230,37 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
             }
         }
         fresh = MANY && row + 1 == gate_end;
-        if (HOLD && row + 1 < end) {
-            load(row + 1, next);
-            if (fresh) load_gate(gate_row + 1, gate);
+        if constexpr (HOLD) {
+            load(row + 1, raw);
+            if ((EACH || fresh) && row + 1 < rows) load_gate(gate_row + a.row_step, gate);
         }
         if (post || pre) block_sum<3>(red[turn], sum);
+        turn ^= 1;
         const float c2 = r2 * sum[0] * a.inv_cols;
         const float c1 = r1 * ((sum[1] - c2 * sum[2]) * a.inv_cols);
-        const rsrc_t dh_row = a.dh.p ? t.row(a.dh.p + row * a.dh.ld) : row_rsrc(nullptr, 0);
-        const rsrc_t dx_row = a.dx.p ? t.row(a.dx.p + row * a.dx.ld) : row_rsrc(nullptr, 0);
+        const rsrc_t dh_row = next_row(dhp, kDh, row_bytes), dx_row = next_row(dxp, kDx, row_bytes);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float dh[V], k[V];
             scale(s, k);
-            if constexpr (MANY && !HOLD) take_gate(gate, s, ag[s]);
+            float now[V];  // MANY: alpha g
+            if constexpr (EACH && HOLD) {
+                take_gate(gate_now, s, now);
+            } else if constexpr (MANY && !HOLD) {
+                take_gate(gate, s, now);
+            } else if constexpr (MANY) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) now[i] = ag[s][i];
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float d = dxo[s][i] - xh[s][i] * c2;  // s
                 const float e = d * hh[s][i];
-                sa[s][i] += e;
-                if constexpr (MANY) sw1[s][i] += ag[s][i] * e;
+                if constexpr (EACH)
+                    sa[s][i] = e;
+                else
+                    sa[s][i] += e;
+                if constexpr (MANY) sw1[s][i] += now[i] * e;
                 dh[i] = r1 * (k[i] * d);
                 dxo[s][i] = a.beta * d;
             }
@@ -222,10 +268,10 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) dh[i] -= hh[s][i] * c1;
             }
-            if (a.dh.p) t.store(dh_row, s, dh);
-            if (a.dx.p) t.store(dx_row, s, dxo[s]);
+            t.store(dh_row, s, dh);
+            t.store(dx_row, s, dxo[s]);
         }
-        if (MANY && (fresh || row + 1 == end)) {
+        if (MANY && (EACH || fresh || row + 1 == rows)) {
             if (a.gate_direct) {
                 const rsrc_t r = t.row(a.dgate.p + gate_row * a.dgate.ld);
 #pragma unroll
@@ -233,9 +279,7 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
                     float w[V];
                     if constexpr (!HOLD) weight(a.w1, s, w);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        sa[s][i] *= a.alpha * (HOLD ? kw[s][i] : w[i]);
-                    }
+                    for (int i = 0; i < V; ++i) sa[s][i] *= a.alpha * (HOLD ? kw[s][i] : w[i]);
                     t.store(r, s, sa[s]);
                 }
             }
@@ -243,32 +287,38 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int i = 0; i < V; ++i) sa[s][i] = 0.0f;
-            gate_row += 1;
-            gate_end += a.rows_per_gate;
+            gate_row += a.row_step;
+            gate_end += a.row_step > 1 ? 1 : a.rows_per_gate;
         }
-    }
+    };
+    Raw raw;
+    if constexpr (HOLD) load(0, raw);
+    for (int row = 0; row < rows; ++row) one_row(row, raw);
+    // the arguments read again: nothing that only this end needs stays in
+    // registers over the rows
+    const auto& z = args_again<GradArgs>();
     if constexpr (!MANY) {
         const rsrc_t dg =
-            a.gate_direct ? t.row(a.dgate.p + gate_row * a.dgate.ld) : row_rsrc(nullptr, 0);
+            z.gate_direct ? t.row(z.dgate.p + gate_row * z.dgate.ld) : row_rsrc(nullptr, 0);
         if (gated) load_gate(gate_row, gate);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float w[V], g[V];
-            weight(a.w1, s, w);
+            weight(z.w1, s, w);
             take_gate(gate, s, g);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 sw1[s][i] = g[i] * sa[s][i];
-                sa[s][i] *= a.alpha * w[i];
+                sa[s][i] *= z.alpha * w[i];
             }
-            if (a.gate_direct) t.store(dg, s, sa[s]);
+            if (z.gate_direct) t.store(dg, s, sa[s]);
         }
     }
     // partial rows, 32 bits each
-    float* ws = a.ws + chunk * a.ws_slots * a.ws_pitch;
+    float* ws = z.ws + chunk * z.ws_slots * z.ws_pitch;
     auto leave = [&](int slot, float (*v)[V]) {
         if (slot < 0) return;
-        const rsrc_t r = row_rsrc(ws + slot * a.ws_pitch, (int)a.ws_pitch * 4);
+        const rsrc_t r = row_rsrc(ws + slot * z.ws_pitch, (int)z.ws_pitch * 4);
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -277,9 +327,9 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
                     (u32x4){as_u(v[s][i]), as_u(v[s][i + 1]), as_u(v[s][i + 2]), as_u(v[s][i + 3])},
                     r, (t.col(s) + i) * 4, 0, 0);
     };
-    leave(a.slot_w1, sw1);
-    leave(a.slot_w2, sw2);
-    leave(a.slot_gate, sa);
+    leave(z.slot_w1, sw1);
+    leave(z.slot_w2, sw2);
+    leave(z.slot_gate, sa);
 }
 
 // Adds partial rows: output row o (blockIdx.y: first dw1 and dw2 as wanted,
@@ -338,23 +388,33 @@ __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64
     }
 }
 
-template <int DT, int S, bool PACKED, bool MANY>
+template <int DT, int S, bool PACKED, int GATES>
 static const void* grad_pick(int cols) {
     switch (edge_of<DT>(cols)) {
-        case kWhole: return reinterpret_cast<const void*>(grad_kernel<DT, S, kWhole, PACKED, MANY>);
-        case kPart: return reinterpret_cast<const void*>(grad_kernel<DT, S, kPart, PACKED, MANY>);
-        default: return reinterpret_cast<const void*>(grad_kernel<DT, 1, kTiny, PACKED, MANY>);
+        case kWhole: return reinterpret_cast<const void*>(grad_kernel<DT, S, kWhole, PACKED, GATES>);
+        case kPart: return reinterpret_cast<const void*>(grad_kernel<DT, S, kPart, PACKED, GATES>);
+        default: return reinterpret_cast<const void*>(grad_kernel<DT, 1, kTiny, PACKED, GATES>);
     }
 }
 
 template <int DT, int S>
 static int launch_grad(const GradArgs& a, int threads, hipStream_t stream) {
     const bool packed = a.kx.q != nullptr || a.kh.q != nullptr;
-    const bool many = a.gate.p != nullptr && a.chunk_gates > 1;
-    const void* k = packed ? (many ? grad_pick<DT, S, true, true>(a.cols)
-                                   : grad_pick<DT, S, true, false>(a.cols))
-                           : (many ? grad_pick<DT, S, false, true>(a.cols)
-                                   : grad_pick<DT, S, false, false>(a.cols));
+    const int gates = a.gate.p == nullptr ? kOneGate : a.chunk_gates;
+    const void* k = nullptr;
+    switch (gates) {
+        case kOneGate:
+            k = packed ? grad_pick<DT, S, true, kOneGate>(a.cols)
+                       : grad_pick<DT, S, false, kOneGate>(a.cols);
+            break;
+        case kEachGate:
+            k = packed ? grad_pick<DT, S, true, kEachGate>(a.cols)
+                       : grad_pick<DT, S, false, kEachGate>(a.cols);
+            break;
+        default:
+            k = packed ? grad_pick<DT, S, true, kSomeGates>(a.cols)
+                       : grad_pick<DT, S, false, kSomeGates>(a.cols);
+    }
     void* args[] = {const_cast<GradArgs*>(&a)};
     return hipLaunchKernel(k, dim3((uint32_t)a.chunks), dim3((uint32_t)threads), args, 0,
                            stream) == hipSuccess

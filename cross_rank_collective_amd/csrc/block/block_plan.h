@@ -39,6 +39,13 @@ struct NormArgs {
     float offset, alpha, beta, eps, inv_cols;
 };
 
+// Gate rows within a chunk of the backward pass.
+enum : int {
+    kOneGate = 0,   // one, or there is no gate
+    kEachGate = 1,  // every row has its own
+    kSomeGates = 2  // several, of any length
+};
+
 struct GradArgs {
     int64_t rows;
     Mat dz, dxo, x, h, dx, dh, gate, dgate;
@@ -47,14 +54,15 @@ struct GradArgs {
     const float *r1, *r2;
     float* ws;              // partial sums: [chunk][which][ws_pitch]
     char *dw1, *dw2;
-    int64_t unit_rows;      // rows are cut into units of this many ...
-    int64_t chunks_per_unit;  // ... and each unit into this many chunks ...
-    int64_t chunk_rows;       // ... of this many rows (the unit's last may have fewer)
+    // rows are cut into units of unit_rows, each unit into chunks_per_unit
+    // chunks of at most chunk_rows rows: chunk j of a unit begins with its row
+    // j chunk_first and takes every row_step-th
+    int64_t unit_rows, chunks_per_unit, chunk_rows, chunk_first, row_step;
     int64_t chunks;
     int64_t gate_rows;
     int64_t rows_per_gate;
     int64_t ws_pitch;     // the columns, rounded up to whole vectors of 4
-    int32_t chunk_gates;  // gate rows that a chunk can touch
+    int32_t chunk_gates;  // kOneGate, kEachGate or kSomeGates
     int32_t gate_direct;  // 1: whole gate rows lie inside chunks, which write them at once
     int32_t ws_slots;     // partial rows per chunk: dw1, dw2 and, without gate_direct, dgate
     int32_t slot_w2, slot_gate;  // position of dw2's and dgate's (dw1's is 0); -1: none
@@ -67,7 +75,7 @@ struct GradArgs {
 // keeping the column sums in registers.  With a gate the chunks never
 // straddle two gate rows unless they hold whole ones.
 struct GradSplit {
-    int64_t unit_rows, chunks_per_unit, chunk_rows, chunks;
+    int64_t unit_rows, chunks_per_unit, chunk_rows, chunk_first, row_step, chunks;
     int32_t gate_direct;
 };
 

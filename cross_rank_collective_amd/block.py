@@ -150,14 +150,24 @@ def _is_kept(v) -> bool:
 
 _NO_ROWS = ptored_rows()
 _NO_KEPT = ptored_checkpoint()
-_FLOATS = {}  # torch dtype -> C ABI code, filled on first use
+_torch = None
+_raw_stream = None
+_FLOATS = {}  # torch dtype -> C ABI code, with the next three filled on first use
+_FLOAT32 = _INT8 = _UINT8 = None
+
+
+def _init() -> None:
+    global _torch, _raw_stream, _FLOAT32, _INT8, _UINT8
+    import torch
+
+    _FLOAT32, _INT8, _UINT8 = torch.float32, torch.int8, torch.uint8
+    _FLOATS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    # the current stream's handle without a stream object, where torch has it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = torch
 
 
 def _float_code(dtype, what: str) -> int:
-    if not _FLOATS:
-        import torch
-
-        _FLOATS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     code = _FLOATS.get(dtype)
     if code is None:
         raise TypeError(f"{what} must be float32, bfloat16 or float16, not {dtype}")
@@ -177,51 +187,66 @@ def _pitch(t, rows: int, cols: int, what: str) -> int:
 
 
 class _Group:
-    """The shape, type and device that a call's tensors have to share."""
+    """The shape, type and device that a call's tensors have to share.
 
-    __slots__ = ("rows", "cols", "dtype", "device", "code")
+    These run on every call, in front of kernels of a few microseconds: a
+    tensor that fits passes with plain comparisons, and only one that does not
+    is looked at again for the error to raise.
+    """
+
+    __slots__ = ("rows", "cols", "shape", "dtype", "index", "code")
 
     def __init__(self, t, what: str):
+        if _torch is None:
+            _init()
         if t.dim() != 2:
             raise ValueError(f"{what} must be 2-D (rows x columns)")
+        self.shape = t.shape
         self.rows, self.cols = t.shape
-        self.dtype, self.device = t.dtype, t.device
+        self.dtype = t.dtype
         self.code = _float_code(t.dtype, what)
-        if not t.is_cuda:
+        self.index = t.get_device()
+        if self.index < 0 or not t.is_cuda:
             raise ValueError(f"{what} must be on a GPU")
 
-    def _same(self, t, dtype, shape, what):
-        if t.dtype != dtype or tuple(t.shape) != shape:
-            raise ValueError(f"{what} must be {dtype} of shape {shape}, not {t.dtype} of "
+    def _misfit(self, t, dtype, shape, what):
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of "
                              f"{tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{what} must be on {self.device}")
+        raise ValueError(f"{what} must be on cuda:{self.index}")
 
-    def mat(self, t, what: str, rows: Optional[int] = None, cols: Optional[int] = None,
-            dtype=None) -> ptored_rows:
+    def mat(self, t, what: str) -> ptored_rows:
+        """A [T, D] tensor of the group's type, or None."""
         if t is None:
             return _NO_ROWS
-        rows = self.rows if rows is None else rows
-        cols = self.cols if cols is None else cols
-        self._same(t, self.dtype if dtype is None else dtype, (rows, cols), what)
+        if t.dtype is not self.dtype or t.shape != self.shape or t.get_device() != self.index:
+            self._misfit(t, self.dtype, self.shape, what)
+        s0, s1 = t.stride()
+        if s1 != 1 or s0 < self.cols:
+            s0 = _pitch(t, self.rows, self.cols, what)
+        return ptored_rows(t.data_ptr(), s0)
+
+    def other(self, t, what: str, rows: int, cols: int, dtype) -> ptored_rows:
+        """A tensor of another shape or type on the group's device."""
+        if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != self.index:
+            self._misfit(t, dtype, (rows, cols), what)
         return ptored_rows(t.data_ptr(), _pitch(t, rows, cols, what))
 
-    def kept(self, k, what: str) -> ptored_checkpoint:
+    def kept(self, k, what: str, cols: Optional[int] = None) -> ptored_checkpoint:
         if k is None:
             return _NO_KEPT
-        import torch
-
         q, s = k
-        blocks = (self.cols + PTORED_CHECKPOINT_BLOCK - 1) // PTORED_CHECKPOINT_BLOCK
-        self._same(q, torch.int8, (self.rows, self.cols), what + "'s values")
-        self._same(s, torch.uint8, (self.rows, blocks), what + "'s scales")
-        return ptored_checkpoint(q.data_ptr(), _pitch(q, self.rows, self.cols, what + "'s values"),
-                                 s.data_ptr(), _pitch(s, self.rows, blocks, what + "'s scales"))
+        cols = self.cols if cols is None else cols
+        blocks = (cols + PTORED_CHECKPOINT_BLOCK - 1) // PTORED_CHECKPOINT_BLOCK
+        qr = self.other(q, what + "'s values", self.rows, cols, _INT8)
+        sr = self.other(s, what + "'s scales", self.rows, blocks, _UINT8)
+        return ptored_checkpoint(qr.data, qr.ld, sr.data, sr.ld)
 
     def vec(self, t, n: int, dtype, what: str) -> Optional[int]:
         if t is None:
             return None
-        self._same(t, dtype, (n,), what)
+        if t.dtype is not dtype or t.shape != (n,) or t.get_device() != self.index:
+            self._misfit(t, dtype, (n,), what)
         if n > 1 and t.stride(0) != 1:
             raise ValueError(f"{what} must be contiguous")
         return t.data_ptr()
@@ -230,7 +255,7 @@ class _Group:
                residual_scale) -> ptored_block_params:
         w = pre_weight if post_weight is None else post_weight
         wt = self.dtype if w is None else w.dtype
-        code = self.code if wt == self.dtype else _float_code(wt, "weights")
+        code = self.code if wt is self.dtype else _float_code(wt, "weights")
         if code not in (0, self.code):
             raise TypeError("weights must be float32 or of the activations' type")
         gate_rows, g = 0, _NO_ROWS
@@ -240,61 +265,57 @@ class _Group:
             gate_rows = gate.shape[0]
             if gate.dim() != 2 or gate_rows == 0 or self.rows % gate_rows:
                 raise ValueError("gate must be [D] or [G, D] with G a divisor of the rows")
-            g = self.mat(gate, "gate", gate_rows)
+            g = self.other(gate, "gate", gate_rows, self.cols, self.dtype)
         return ptored_block_params(
             self.rows, self.cols, self.vec(post_weight, self.cols, wt, "post_weight"),
             self.vec(pre_weight, self.cols, wt, "pre_weight"), g, gate_rows, weight_offset,
             branch_scale, residual_scale, eps, self.code, code)
 
+    def run(self, stream, call, *args) -> None:
+        """``call(*args, stream handle)`` with the group's GPU current, raising on errors."""
+        if stream is None and _raw_stream is not None:
+            handle = _raw_stream(self.index)
+        else:
+            handle = B._stream_handle(stream, self.index)
+        if _torch.cuda.current_device() == self.index:
+            status = call(*args, handle)
+        else:
+            with _torch.cuda.device(self.index):
+                status = call(*args, handle)
+        if status:
+            B._raise_on(status)
 
-def _call(device, stream, call) -> None:
-    """``call(stream handle)`` with the tensors' GPU current, raising on errors."""
-    import torch
 
-    handle = B._stream_handle(stream, device)
-    if torch.cuda.current_device() == device.index:
-        B._raise_on(call(handle))
-        return
-    with torch.cuda.device(device):
-        B._raise_on(call(handle))
-
-
-def _torch_stream(stream, device):
+def _torch_stream(stream, index):
     """torch's object for the stream of a call."""
-    import torch
-
     if stream is None:
-        return torch.cuda.current_stream(device)
+        return _torch.cuda.current_stream(index)
     if hasattr(stream, "cuda_stream"):
         return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
+    return _torch.cuda.ExternalStream(int(stream), device=index)
 
 
-def _zero(tensors, device, stream) -> None:
+def _zero(tensors, index, stream) -> None:
     """Sums over no rows, on the call's stream."""
-    import torch
-
-    with torch.cuda.stream(_torch_stream(stream, device)):
+    with _torch.cuda.stream(_torch_stream(stream, index)):
         for t in tensors:
             if t is not None:
                 t.zero_()
 
 
-def _workspace(nbytes: int, given, device, stream):
+def _workspace(nbytes: int, given, index, stream):
     """(tensor to keep until the call is made, pointer, bytes)."""
-    import torch
-
     if given is not None:
-        if given.device != device or not given.is_contiguous():
+        if given.get_device() != index or not given.is_contiguous():
             raise ValueError("workspace must be contiguous and on the call's GPU")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if nbytes == 0:
         return None, None, 0
     if stream is None:
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        t = _torch.empty(nbytes, dtype=_UINT8, device=index)
     else:  # belongs to the stream that uses it, so that it is not reused too early
-        with torch.cuda.stream(_torch_stream(stream, device)):
-            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with _torch.cuda.stream(_torch_stream(stream, index)):
+            t = _torch.empty(nbytes, dtype=_UINT8, device=index)
     return t, t.data_ptr(), nbytes
 
 
@@ -318,28 +339,26 @@ def block_norm(parts, x, x_out=None, z=None, *, post_weight=None, gate=None, pre
     ``z_kept``, the 8-bit forms of h, x_out and z.  ``x_out`` may be ``x``.
     """
     g = _Group(x, "x")
-    import torch
-
-    parts = list(parts)
-    part_ld = g.cols
-    if parts:
-        part_ld = g.mat(parts[0], "parts[0]").ld
-        for t in parts[1:]:
-            if t.stride() != parts[0].stride():
-                raise ValueError("every part must have the same strides")
-            g._same(t, g.dtype, (g.rows, g.cols), "every part")
+    ptrs, part_ld = [], g.cols
+    for t in parts:
+        if not ptrs:
+            part_ld = g.mat(t, "parts[0]").ld
+            strides = t.stride()
+        elif (t.stride() != strides or t.shape != g.shape or t.dtype is not g.dtype
+              or t.get_device() != g.index):
+            g.mat(t, "every part")
+            raise ValueError("every part must have the same strides")
+        ptrs.append(t.data_ptr())
     params = g.params(post_weight, pre_weight, gate, eps, weight_offset, branch_scale,
                       residual_scale)
     io = ptored_block_io(g.mat(x, "x"), g.mat(x_out, "x_out"), g.mat(z, "z"), g.mat(h, "h"),
-                         g.vec(post_rstd, g.rows, torch.float32, "post_rstd"),
-                         g.vec(pre_rstd, g.rows, torch.float32, "pre_rstd"),
+                         g.vec(post_rstd, g.rows, _FLOAT32, "post_rstd"),
+                         g.vec(pre_rstd, g.rows, _FLOAT32, "pre_rstd"),
                          g.kept(h_kept, "h_kept"), g.kept(x_kept, "x_kept"),
                          g.kept(z_kept, "z_kept"))
     if g.rows == 0 or g.cols == 0:
         return  # empty tensors have no storage
-    ptrs = [t.data_ptr() for t in parts]
-    _call(g.device, stream,
-          lambda s: ptored_block_norm(ptrs, len(ptrs), part_ld, params, io, s))
+    g.run(stream, ptored_block_norm, ptrs, len(ptrs), part_ld, params, io)
 
 
 def block_norm_backward_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
@@ -370,39 +389,38 @@ def block_norm_backward(dz, dx_out, x_out, pre_rstd, dx=None, dh=None, *, h=None
     if ref is None:
         raise ValueError("block_norm_backward needs dz, dx_out or both")
     g = _Group(ref, "dz" if dz is not None else "dx_out")
-    import torch
-
     params = g.params(post_weight, pre_weight, gate, 0.0, weight_offset, branch_scale,
                       residual_scale)
     packed = _is_kept(x_out) or _is_kept(h)
     if packed and not all(v is None or _is_kept(v) for v in (x_out, h)):
         raise ValueError("x_out and h must both be tensors or both be checkpoints")
-    wt = torch.float32 if params.weight_dtype == 0 else g.dtype
-    if dgate is not None and dgate.dim() == 1:
-        dgate = dgate.unsqueeze(0)
-    nbytes = 0
-    if g.cols <= PTORED_BLOCK_MAX_COLS:
-        nbytes = block_norm_backward_workspace(g.rows, g.cols,
-                                               0 if dgate is None else params.gate_rows)
-    wanted = dgate is not None or dpost_weight is not None or dpre_weight is not None
+    wt = _FLOAT32 if params.weight_dtype == 0 else g.dtype
+    gate_rows, dgate_rows = _NO_ROWS, 0
+    if dgate is not None:
+        if dgate.dim() == 1:
+            dgate = dgate.unsqueeze(0)
+        dgate_rows = params.gate_rows
+        gate_rows = g.other(dgate, "dgate", dgate_rows, g.cols, g.dtype)
     io = ptored_block_grad_io(
         g.mat(dz, "dz"), g.mat(dx_out, "dx_out"),
         _NO_ROWS if packed else g.mat(x_out, "x_out"), _NO_ROWS if packed else g.mat(h, "h"),
         g.kept(x_out, "x_out") if packed else _NO_KEPT,
         g.kept(h, "h") if packed else _NO_KEPT,
-        g.vec(post_rstd, g.rows, torch.float32, "post_rstd"),
-        g.vec(pre_rstd, g.rows, torch.float32, "pre_rstd"), g.mat(dx, "dx"), g.mat(dh, "dh"),
-        g.mat(dgate, "dgate", params.gate_rows),
-        g.vec(dpost_weight, g.cols, wt, "dpost_weight"),
+        g.vec(post_rstd, g.rows, _FLOAT32, "post_rstd"),
+        g.vec(pre_rstd, g.rows, _FLOAT32, "pre_rstd"), g.mat(dx, "dx"), g.mat(dh, "dh"),
+        gate_rows, g.vec(dpost_weight, g.cols, wt, "dpost_weight"),
         g.vec(dpre_weight, g.cols, wt, "dpre_weight"), None, 0)
     if g.cols == 0:
         return
     if g.rows == 0:  # nothing to read; the sums over no rows are zero
-        _zero((dgate, dpost_weight, dpre_weight), g.device, stream)
+        _zero((dgate, dpost_weight, dpre_weight), g.index, stream)
         return
-    keep, io.workspace, io.workspace_bytes = _workspace(nbytes if wanted else 0, workspace,
-                                                        g.device, stream)
-    _call(g.device, stream, lambda s: ptored_block_norm_backward(params, io, s))
+    nbytes = 0
+    if g.cols <= PTORED_BLOCK_MAX_COLS and not (
+            dgate is None and dpost_weight is None and dpre_weight is None):
+        nbytes = block_norm_backward_workspace(g.rows, g.cols, dgate_rows)
+    keep, io.workspace, io.workspace_bytes = _workspace(nbytes, workspace, g.index, stream)
+    g.run(stream, ptored_block_norm_backward, params, io)
 
 
 def checkpoint_empty(rows: int, cols: int, device="cuda") -> Checkpoint:
@@ -423,8 +441,7 @@ def checkpoint_pack(x, kept, stream=None) -> None:
     g = _Group(x, "x")
     xm, k = g.mat(x, "x"), g.kept(kept, "kept")
     if g.rows and g.cols:
-        _call(g.device, stream,
-              lambda s: ptored_checkpoint_pack(xm, g.rows, g.cols, g.code, k, s))
+        g.run(stream, ptored_checkpoint_pack, xm, g.rows, g.cols, g.code, k)
 
 
 def checkpoint_unpack(kept, out, stream=None) -> None:
@@ -432,8 +449,11 @@ def checkpoint_unpack(kept, out, stream=None) -> None:
     g = _Group(out, "out")
     om, k = g.mat(out, "out"), g.kept(kept, "kept")
     if g.rows and g.cols:
-        _call(g.device, stream,
-              lambda s: ptored_checkpoint_unpack(k, g.rows, g.cols, g.code, om, s))
+        g.run(stream, _unpack_into, om, k, g.rows, g.cols, g.code)
+
+
+def _unpack_into(om, k, rows, cols, code, stream):
+    return ptored_checkpoint_unpack(k, rows, cols, code, om, stream)
 
 
 def checkpoint_wgrad_workspace(rows: int, outs: int, cols: int, dtype) -> int:
@@ -457,16 +477,15 @@ def checkpoint_wgrad(dy, kept, dw, accumulate: bool = False, workspace=None, str
         raise TypeError("dw must be float32 or of dy's type")
     dym = g.mat(dy, "dy")
     outs, cols = dw.shape
-    dwm = g.mat(dw, "dw", outs, cols, dw.dtype)
-    g.cols = cols
-    k = g.kept(kept, "kept")
+    dwm = g.other(dw, "dw", outs, cols, dw.dtype)
+    k = g.kept(kept, "kept", cols)
     if outs == 0 or cols == 0 or (g.rows == 0 and accumulate):
         return
     if g.rows == 0:  # the sum over no rows
-        _zero((dw,), g.device, stream)
+        _zero((dw,), g.index, stream)
         return
-    nbytes = checkpoint_wgrad_workspace(g.rows, outs, cols, dy.dtype)
-    keep, ptr, given = _workspace(nbytes, workspace, g.device, stream)
-    _call(g.device, stream,
-          lambda s: ptored_checkpoint_wgrad(dym, k, g.rows, outs, cols, g.code, dwm, code,
-                                            1 if accumulate else 0, ptr, given, s))
+    st, nbytes = ptored_checkpoint_wgrad_workspace(g.rows, outs, cols, g.code)
+    B._raise_on(st)
+    keep, ptr, given = _workspace(nbytes, workspace, g.index, stream)
+    g.run(stream, ptored_checkpoint_wgrad, dym, k, g.rows, outs, cols, g.code, dwm, code,
+          1 if accumulate else 0, ptr, given)

@@ -17,7 +17,7 @@ namespace block {
 constexpr int kPackThreads = 256;
 
 // Slot `x` past the row's start, which may be rows further on: `row` and the
-// column.  inv = floor(2^32 / row_slots) + 1 where row_slots < kPackThreads
+// column.  inv = floor(2^32 / row_slots) + 1 where row_slots < 1024: then x <
 // 2048 and the quotient is exact.
 __device__ __forceinline__ int slot_place(uint32_t x, uint32_t row_slots, uint32_t inv, int64_t& row) {
     const uint32_t q = inv ? __umulhi(x, inv) : x >= row_slots ? 1u : 0u;

@@ -10,7 +10,9 @@ an activation in 8 bits (32 elements of a row share a power of two),
 ``checkpoint_wgrad`` (a projection's weight gradient) take it as it is.
 
 As in ``binding``, every step runs in the library's HIP kernels: these
-functions check tensors, hand over pointers and raise on errors.  Outputs are
+functions check tensors, hand over pointers and raise on errors.  Calls whose
+tensors fit as they are go through ``_torch_calls.so``, the rest (and every
+error) through the Python code below; both make the same library call.  Outputs are
 the caller's tensors; nothing is allocated but, where none is given, the
 workspace of a backward pass (from torch's allocator, on the call's stream).
 Calls are asynchronous on ``stream`` (default: torch's current stream).  A
@@ -151,19 +153,22 @@ def _is_kept(v) -> bool:
 _NO_ROWS = ptored_rows()
 _NO_KEPT = ptored_checkpoint()
 _torch = None
-_raw_stream = None
+_native = None  # the extension module of the tensor calls
 _FLOATS = {}  # torch dtype -> C ABI code, with the next three filled on first use
 _FLOAT32 = _INT8 = _UINT8 = None
 
 
 def _init() -> None:
-    global _torch, _raw_stream, _FLOAT32, _INT8, _UINT8
+    global _torch, _native, _FLOAT32, _INT8, _UINT8
     import torch
+
+    _load()
+    from . import _torch_calls
+
+    _native = _torch_calls
 
     _FLOAT32, _INT8, _UINT8 = torch.float32, torch.int8, torch.uint8
     _FLOATS.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    # the current stream's handle without a stream object, where torch has it
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _torch = torch
 
 
@@ -189,9 +194,8 @@ def _pitch(t, rows: int, cols: int, what: str) -> int:
 class _Group:
     """The shape, type and device that a call's tensors have to share.
 
-    These run on every call, in front of kernels of a few microseconds: a
-    tensor that fits passes with plain comparisons, and only one that does not
-    is looked at again for the error to raise.
+    A tensor that fits passes with plain comparisons, and only one that does
+    not is looked at again for the error to raise.
     """
 
     __slots__ = ("rows", "cols", "shape", "dtype", "index", "code")
@@ -273,10 +277,7 @@ class _Group:
 
     def run(self, stream, call, *args) -> None:
         """``call(*args, stream handle)`` with the group's GPU current, raising on errors."""
-        if stream is None and _raw_stream is not None:
-            handle = _raw_stream(self.index)
-        else:
-            handle = B._stream_handle(stream, self.index)
+        handle = B._stream_handle(stream, self.index)
         if _torch.cuda.current_device() == self.index:
             status = call(*args, handle)
         else:
@@ -284,6 +285,19 @@ class _Group:
                 status = call(*args, handle)
         if status:
             B._raise_on(status)
+
+
+def _native_call(name: str, stream, *args) -> bool:
+    """The call on tensors that fit as they are, made natively: False where the
+    code that follows has to look again (and make the call, or say what does
+    not fit)."""
+    if _native is None:
+        _init()
+    handle = stream if stream is None else B._stream_handle(stream, None)
+    status = getattr(_native, name)(*args, handle)
+    if status:
+        B._raise_on(status)
+    return status is not None
 
 
 def _torch_stream(stream, index):
@@ -338,6 +352,10 @@ def block_norm(parts, x, x_out=None, z=None, *, post_weight=None, gate=None, pre
     ``post_rstd`` and ``pre_rstd`` (float32 [T]), and ``h_kept``, ``x_kept``,
     ``z_kept``, the 8-bit forms of h, x_out and z.  ``x_out`` may be ``x``.
     """
+    if _native_call("block_norm", stream, parts, x, x_out, z, post_weight, gate, pre_weight, eps,
+                    weight_offset, branch_scale, residual_scale, h, post_rstd, pre_rstd, h_kept,
+                    x_kept, z_kept):
+        return
     g = _Group(x, "x")
     ptrs, part_ld = [], g.cols
     for t in parts:
@@ -385,6 +403,10 @@ def block_norm_backward(dz, dx_out, x_out, pre_rstd, dx=None, dh=None, *, h=None
     shapes and types of what they are gradients of.  ``dx`` and ``dh`` may be
     any of the [T, D] inputs.
     """
+    if _native_call("block_norm_backward", stream, dz, dx_out, x_out, pre_rstd, dx, dh, h,
+                    post_rstd, post_weight, gate, pre_weight, 0.0, weight_offset, branch_scale,
+                    residual_scale, dpost_weight, dgate, dpre_weight, workspace):
+        return
     ref = dz if dz is not None else dx_out
     if ref is None:
         raise ValueError("block_norm_backward needs dz, dx_out or both")
@@ -438,6 +460,8 @@ def checkpoint_pack(x, kept, stream=None) -> None:
     the largest magnitude of its block of 32 (or 1/32 where that magnitude
     comes within 1/256 of the next power).  A block with an infinity or a NaN
     stands for NaN."""
+    if _native_call("checkpoint_pack", stream, x, kept):
+        return
     g = _Group(x, "x")
     xm, k = g.mat(x, "x"), g.kept(kept, "kept")
     if g.rows and g.cols:
@@ -446,6 +470,8 @@ def checkpoint_pack(x, kept, stream=None) -> None:
 
 def checkpoint_unpack(kept, out, stream=None) -> None:
     """``out`` = the values kept (exact in float32 and bfloat16)."""
+    if _native_call("checkpoint_unpack", stream, kept, out):
+        return
     g = _Group(out, "out")
     om, k = g.mat(out, "out"), g.kept(kept, "kept")
     if g.rows and g.cols:
@@ -467,6 +493,8 @@ def checkpoint_wgrad(dy, kept, dw, accumulate: bool = False, workspace=None, str
     """dw = dy^T x (or dw += dy^T x): the weight gradient of y = x W^T from
     ``dy`` [T, O] and the kept input x [T, I], into ``dw`` [O, I], float32 or
     of dy's type.  Products are exact and sums in float32."""
+    if _native_call("checkpoint_wgrad", stream, dy, kept, dw, accumulate, workspace):
+        return
     g = _Group(dy, "dy")
     if dw.dim() != 2 or dw.shape[0] != g.cols:
         raise ValueError("dw must be [dy's columns, x's columns]")

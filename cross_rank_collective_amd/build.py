@@ -5,7 +5,8 @@ linked into ``cross_rank_collective_amd/libptored.so``: the host code, one
 unit per element type (copy and push-with-add kernels) and ``treduce_op.hip``
 once per (element type, operator) pair (reduction and ring kernels); and from
 csrc/block/ the block-boundary operators' kernels, once per floating type,
-with their host code.  Run as
+with their host code.  Next to it, ``_torch_calls.so``: the block-boundary
+calls on torch tensors as an extension module (host code, g++).  Run as
 ``python -m cross_rank_collective_amd.build`` or through
 ``__graft_entry__.build()``.
 """
@@ -23,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libptored.so")
+EXT = os.path.join(PKG, "_torch_calls.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 DTYPES = ("F32", "BF16", "F16", "I32")
@@ -71,20 +73,56 @@ def _compile(unit) -> str:
     return obj
 
 
+def _compile_ext() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD_DIR, "torch_calls.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", "-I" + sysconfig.get_paths()["include"],
+           *("-isystem" + p for p in cpp_extension.include_paths()), "-isystem/opt/rocm/include",
+           "-c", os.path.join(CSRC, "block", "torch_calls.cpp"), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_ext(obj: str) -> None:
+    from torch.utils import cpp_extension
+
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", obj, "-o", EXT + ".tmp", f"-L{PKG}",
+           "-l:libptored.so", "-Wl,-rpath,$ORIGIN",
+           *("-L" + p for p in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_hip", "-lamdhip64"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link of _torch_calls.so failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(EXT + ".tmp", EXT)
+
+
 def build(jobs: int = 0) -> str:
-    """Compile every HIP unit for gfx950 and link libptored.so; returns its path.
+    """Compile every HIP unit for gfx950 and link libptored.so and the tensor
+    calls; returns the library's path.
     ``jobs`` = parallel compilers (0: one per CPU, at most 16)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     if jobs <= 0:
         jobs = min(16, len(os.sched_getaffinity(0)))
-    with ThreadPoolExecutor(max(1, min(jobs, len(UNITS)))) as ex:
+    with ThreadPoolExecutor(max(1, min(jobs, len(UNITS) + 1))) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(_compile, UNITS))
+        ext_obj = ext.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
 
 

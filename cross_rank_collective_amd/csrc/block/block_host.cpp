@@ -6,8 +6,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "block_plan.h"
 
@@ -160,31 +160,81 @@ int64_t grad_workspace(int64_t cols, int64_t gate_rows, const GradSplit& s) {
 
 struct WgradShape {
     int64_t tiles_m, tiles_n, splits, rows_per_split;
-    int wide;
+    int shape;
 };
 
-// Tokens are split over workgroups when the tiles of dw alone would leave
-// compute units idle, in parts of at least 4 steps.
-constexpr int64_t kTokens = 64;
+// Tiles and splits of the weight gradient, by estimated time.  A tile of
+// `tokens` takes about base + step tokens / 64 us, one tile at a time on each
+// of 256 compute units (the figures are fits to sizes from 64 to 32768 tokens
+// and 128 to 4096 columns).  Splitting the tokens shortens a tile's walk and
+// fills idle compute units; each split writes its partial dw, which is read
+// again by a second kernel: 4 us and the bytes at 2.6 TB/s.  So with few
+// tiles the best number of splits is near sqrt(walk / time of one dw), as
+// long as the tiles of all splits still run at once.
+// Measured, us, best splits of 128 x 128 tiles against 256 x 256: 1024 tokens
+// x 2048 x 2048 20 / 39, 4096 x 2048 x 2048 49 / 59, 16384 x 4096 x 512 94 /
+// 88, 8192 x 4096 x 4096 410 / 250; 32768 x 640 x 512 with 1, 6, 12 and 25
+// splits 267, 60, 41 and 49.
+struct WgradCost {
+    int shape;
+    int64_t tm, tn;
+    double base, step;
+};
+constexpr int64_t kTokens = 128;  // rows of a split: a multiple of two steps
+
+double wgrad_time(const WgradCost& c, int64_t rows, int64_t tiles, int64_t splits, double dw_us) {
+    const int64_t per = (rows + splits - 1) / splits;
+    const int64_t rounds = (tiles * splits + 255) / 256;
+    return (double)rounds * (c.base + c.step * (double)per / 64) +
+           (splits > 1 ? 4.0 + dw_us * (double)splits : 0.0);
+}
+
 WgradShape wgrad_shape(int64_t rows, int64_t outs, int64_t cols, int dtype) {
+    static constexpr WgradCost k16[] = {{kWgradTile, 128, 128, 8.0, 0.7},
+                                        {kWgradWide, 256, 256, 17.0, 1.8}};
+    static constexpr WgradCost k32[] = {{kWgradTile, 128, 256, 14.0, 2.4}};
+    static constexpr WgradCost kFew[] = {{kWgradFew, 128, 128, 10.0, 1.0}};
     WgradShape w{};
-    const char* force = getenv("WG_WIDE");
-    w.wide = force ? atoi(force) : outs * cols >= (int64_t)200 * 65536;
-    const int64_t tm = w.wide && dtype != PTORED_F32 ? 256 : 128, tn = w.wide ? 256 : 128;
-    w.tiles_m = (outs + tm - 1) / tm;
-    w.tiles_n = (cols + tn - 1) / tn;
-    const int64_t steps = (rows + kTokens - 1) / kTokens;
-    if (steps == 0) return w;
-    int64_t splits = std::min<int64_t>((w.wide ? 256 : 512) / std::max<int64_t>(1, w.tiles_m * w.tiles_n), steps / 4);
-    splits = std::max<int64_t>(1, splits);
-    const int64_t per = (steps + splits - 1) / splits;
-    w.rows_per_split = per * kTokens;
-    w.splits = (steps + per - 1) / per;
+    if (outs == 0 || cols == 0) return w;
+    const bool few = outs < 8 || cols < 16;
+    const WgradCost* costs = few ? kFew : dtype == PTORED_F32 ? k32 : k16;
+    const int count = !few && dtype != PTORED_F32 ? 2 : 1;
+    const double dw_us = (double)outs * (double)cols * 4 / 2.6e6;
+    double best = -1;
+    for (int i = 0; i < count; ++i) {
+        const WgradCost& c = costs[i];
+        const int64_t tm = (outs + c.tm - 1) / c.tm, tn = (cols + c.tn - 1) / c.tn, tiles = tm * tn;
+        int64_t splits = 1;
+        if (rows > kTokens && tiles <= 128) {
+            const int64_t room = std::min(256 / tiles, (rows + kTokens - 1) / kTokens);
+            const double ideal = std::sqrt(c.step * (double)rows / 64 / dw_us);
+            const int64_t s = ideal < (double)room ? std::max<int64_t>(1, (int64_t)(ideal + 0.5)) : room;
+            if (wgrad_time(c, rows, tiles, s, dw_us) < wgrad_time(c, rows, tiles, 1, dw_us))
+                splits = s;
+        }
+        const double us = wgrad_time(c, rows, tiles, splits, dw_us);
+        if (best >= 0 && us >= best) continue;
+        best = us;
+        w.shape = c.shape;
+        w.tiles_m = tm;
+        w.tiles_n = tn;
+        w.splits = splits;
+    }
+    if (rows == 0) {
+        w.splits = 0;
+        return w;
+    }
+    const int64_t per = ((rows + w.splits - 1) / w.splits + kTokens - 1) / kTokens * kTokens;
+    w.rows_per_split = per;
+    w.splits = (rows + per - 1) / per;
     return w;
 }
 
+// Columns of a partial row: whole vectors of 4.
+int64_t wgrad_pitch(int64_t cols) { return (cols + 3) / 4 * 4; }
+
 int64_t wgrad_workspace(int64_t outs, int64_t cols, const WgradShape& w) {
-    return w.splits > 1 ? w.splits * outs * cols * 4 : 0;
+    return w.splits > 1 ? w.splits * outs * wgrad_pitch(cols) * 4 : 0;
 }
 
 int checkpoint_args(const ptored_rows& x, int64_t rows, int64_t cols, int dtype,
@@ -421,7 +471,8 @@ extern "C" int ptored_checkpoint_wgrad(ptored_rows dy, ptored_checkpoint x, int6
     if (!float_type(dtype) || (dw_dtype != PTORED_F32 && dw_dtype != dtype))
         return PTORED_ERR_UNSUPPORTED;
     const WgradShape w = wgrad_shape(rows, outs, cols, dtype);
-    if (w.tiles_m * w.tiles_n > (int64_t(1) << 31) - 1) return PTORED_ERR_UNSUPPORTED;
+    // a launch takes fewer than 2^32 threads
+    if (w.tiles_m * w.tiles_n > int64_t(1) << 22) return PTORED_ERR_UNSUPPORTED;
     const int64_t need = wgrad_workspace(outs, cols, w);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return PTORED_ERR_INVALID_ARG;
@@ -447,6 +498,7 @@ extern "C" int ptored_checkpoint_wgrad(ptored_rows dy, ptored_checkpoint x, int6
     a.accumulate = accumulate != 0;
     a.tiles_m = (int32_t)w.tiles_m;
     a.tiles_n = (int32_t)w.tiles_n;
-    a.wide = w.wide;
+    a.shape = w.shape;
+    a.ws_ld = wgrad_pitch(cols);
     return status_of(PTORED_BY_TYPE(wgrad, dtype, a, stream));
 }

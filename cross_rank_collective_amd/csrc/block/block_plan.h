@@ -86,20 +86,28 @@ struct PackArgs {
     int32_t cols;
 };
 
+// The weight gradient's workgroups.
+enum : int {
+    kWgradTile = 0,  // tiles of 128 x 128 (f32: 128 x 256), 64 tokens a step (f32: 32)
+    kWgradWide = 1,  // 256 x 256, 32 tokens a step; not f32
+    kWgradFew = 2    // 128 x 128 of a matrix with rows shorter than a chunk
+};
+
 struct WgradArgs {
     const char* dy;
     int64_t dy_ld;  // bytes
     Kept x;
     char* dw;
     int64_t dw_ld;  // bytes
-    float* ws;      // [split][outs][cols] partial sums when splits > 1
+    float* ws;      // [split][outs][ws_ld] partial sums when splits > 1
+    int64_t ws_ld;  // the columns, rounded up to whole vectors of 4
     int64_t rows;
     int64_t rows_per_split;  // a multiple of the kernel's step
     int32_t outs, cols;
     int32_t splits;
     int32_t dw_f32, accumulate;
     int32_t tiles_m, tiles_n;
-    int32_t wide;  // 1: tiles of 256 x 256, 0: of 128 x 128
+    int32_t shape;  // kWgradTile, kWgradWide or kWgradFew
 };
 
 enum : int { kOk = 0, kFailed = 1 };

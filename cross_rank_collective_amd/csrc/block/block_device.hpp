@@ -239,28 +239,30 @@ struct Slots {
     struct Weight {
         u32x4 w[V == 8 ? 2 : 1];
     };
+    // Without a branch on its type or on whether there is one (null: zeros), so
+    // that several are on their way together.
     __device__ __forceinline__ Weight load_weight(const char* p, int f32, int s) const {
         Weight k;
-        if (V == 4 || !f32) {
-            const rsrc_t r = row(p);
-            if constexpr (EDGE == kTiny)
-                k.w[0] = load(r, s);
-            else
-                k.w[0] = __builtin_amdgcn_raw_buffer_load_b128(r, at(s) * ES, 0, kPolicyKeep);
-        } else {
-            const rsrc_t r = row_rsrc(p, cols * 4);
+        const int es = f32 ? 4 : ES;
+        const rsrc_t r = row_rsrc(p, p != nullptr ? cols * es : 0);
+        if constexpr (EDGE == kTiny) {
+            uint32_t w[8] = {};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (EDGE == kTiny) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        k.w[h % (V / 4)][i] = __builtin_amdgcn_raw_buffer_load_b32(
-                            r, (col0 + 4 * h + i) * 4, 0, 0);
-                } else {
-                    k.w[h % (V / 4)] = __builtin_amdgcn_raw_buffer_load_b128(
-                        r, at(s) * 4 + 16 * h, 0, kPolicyKeep);
-                }
+            for (int i = 0; i < V - 1; ++i) {
+                if (es == 4)
+                    w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (col0 + i) * 4, 0, 0);
+                else
+                    w[i / 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                    r, (col0 + i) * 2, 0, 0)
+                                << (16 * (i % 2));
             }
+            k.w[0] = (u32x4){w[0], w[1], w[2], w[3]};
+            if constexpr (V == 8) k.w[1] = (u32x4){w[4], w[5], w[6], w[7]};
+        } else {
+            k.w[0] = __builtin_amdgcn_raw_buffer_load_b128(r, at(s) * es, 0, kPolicyKeep);
+            if constexpr (V == 8)  // past the row for the type of 16 bits
+                k.w[1] = __builtin_amdgcn_raw_buffer_load_b128(
+                    r, f32 ? at(s) * 4 + 16 : 0x40000000, 0, kPolicyKeep);
         }
         return k;
     }

@@ -372,14 +372,21 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     // gate rows without a gradient: a chunk that walks several takes them in order
     const bool in_order = !gated && p.gate.data && p.gate_rows > 1 && p.gate_rows < p.rows;
     const GradSplit split = grad_split(p.rows, p.cols, gated ? p.gate_rows : 0, p.dtype, in_order);
-    const bool partial_gate = gated && !split.gate_direct;
     GradArgs a{};
-    a.slot_w1 = a.slot_w2 = a.slot_gate = -1;
-    if (io->dpost_weight) a.slot_w1 = a.ws_slots++;
+    // with its gradient wanted, a chunk lies within a gate row or begins with one
+    const int64_t rows_per_gate = p.gate.data ? p.rows / p.gate_rows : p.rows;
+    const bool one = gated ? !split.gate_direct : p.gate.data == nullptr || p.gate_rows == 1;
+    a.chunk_gates = one ? kOneGate : rows_per_gate == 1 ? kEachGate : kSomeGates;
+    a.gate_direct = split.gate_direct;
+    a.gate_joined = gated && !split.gate_direct;
+    a.gate_units = p.gate_rows > 1 ? 1 : 0;
+    a.slot_w1 = a.slot_w2 = -1;
+    if (io->dpost_weight || a.gate_joined) a.slot_w1 = a.ws_slots++;
     if (io->dpre_weight) a.slot_w2 = a.ws_slots++;
-    if (partial_gate) a.slot_gate = a.ws_slots++;
     a.ws_pitch = grad_pitch(p.cols);
-    const int64_t need = split.chunks * a.ws_pitch * 4 * a.ws_slots;
+    // as much as the query gives, which counts a row for each sum that is wanted
+    const int wanted = (io->dpost_weight != nullptr) + (io->dpre_weight != nullptr) + a.gate_joined;
+    const int64_t need = split.chunks * a.ws_pitch * 4 * wanted;
     if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
         return PTORED_ERR_INVALID_ARG;
     if (need > 0) b.vec(io->workspace, need, 16, true);
@@ -412,15 +419,8 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     a.chunk_first = split.chunk_first;
     a.row_step = split.row_step;
     a.chunks = split.chunks;
-    a.gate_direct = split.gate_direct;
     a.gate_rows = p.gate_rows;
-    a.rows_per_gate = p.gate.data ? p.rows / p.gate_rows : p.rows;
-    // with its gradient wanted, a chunk lies within a gate row or begins with one
-    a.chunk_gates = p.gate_rows <= 1 || (gated && split.chunk_rows <= a.rows_per_gate &&
-                                         !(split.row_step > 1 && split.gate_direct))
-                        ? kOneGate
-                    : a.rows_per_gate == 1 ? kEachGate
-                                           : kSomeGates;
+    a.rows_per_gate = rows_per_gate;
     a.w_f32 = p.weight_dtype == PTORED_F32;
     a.offset = p.weight_offset;
     a.alpha = p.branch_scale;

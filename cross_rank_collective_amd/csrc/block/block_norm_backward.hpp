@@ -16,8 +16,9 @@
 // current one waits for its sum.  The weights' and the gate's gradients share
 // one column sum: with A = sum_t s hh over the rows of one gate row,
 // dg = alpha (w1 + o) A and that gate row adds alpha g A to dw1.  Each chunk
-// leaves one partial row per sum in the workspace, and a second kernel adds
-// those in a fixed order.
+// leaves one partial row per sum in the workspace (A where its rows share one
+// gate row, dw1's share where they do not), and a second kernel adds those in a
+// fixed order.
 #pragma once
 
 #include "block_device.hpp"
@@ -125,16 +126,18 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
             for (int i = 0; i < V; ++i) v[i] *= by;
         }
     };
-    auto weight = [&](const char* w, int s, float* v) {
-        if (w != nullptr) {
-            t.take_weight(t.load_weight(w, a.w_f32, s), a.w_f32, a.offset, s, v);
-        } else {
+    auto take_weight = [&](const typename Row::Weight& raw, const char* w, int s, float* v) {
+        t.take_weight(raw, a.w_f32, a.offset, s, v);
+        if (w == nullptr) {
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = 1.0f;
         }
     };
+    auto weight = [&](const char* w, int s, float* v) {
+        take_weight(t.load_weight(w, a.w_f32, s), w, s, v);
+    };
     auto load_gate = [&](int64_t gate_row, u32x4* to) {
-        const rsrc_t r = t.row(a.gate.p + gate_row * a.gate.ld);
+        const rsrc_t r = row_rsrc(a.gate.p + gate_row * a.gate.ld, gated ? row_bytes : 0);
 #pragma unroll
         for (int s = 0; s < S; ++s) to[s] = t.load(r, s);
     };
@@ -153,14 +156,23 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
     // the rows up to here share the gate row
     int64_t gate_end = !MANY ? rows : a.row_step > 1 ? 1 : (gate_row + 1) * a.rows_per_gate - begin;
     u32x4 gate[S];  // of the next row, where that begins a gate row
-    if (gated) load_gate(gate_row, gate);
+    load_gate(gate_row, gate);
     // HOLD: w2 + o; alpha g; alpha g (w1 + o), or with MANY w1 + o
     float w2[S][V], ag[S][V], kw[S][V];
+    Raw raw;
     if constexpr (HOLD) {
+        // everything is asked for before the first wait
+        typename Row::Weight w1_raw[S], w2_raw[S];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            weight(a.w2, s, w2[s]);
-            weight(a.w1, s, kw[s]);
+            w1_raw[s] = t.load_weight(a.w1, a.w_f32, s);
+            w2_raw[s] = t.load_weight(a.w2, a.w_f32, s);
+        }
+        load(0, raw);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            take_weight(w2_raw[s], a.w2, s, w2[s]);
+            take_weight(w1_raw[s], a.w1, s, kw[s]);
             if constexpr (!MANY) {
                 take_gate(gate, s, ag[s]);
 #pragma unroll
@@ -291,29 +303,10 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
             gate_end += a.row_step > 1 ? 1 : a.rows_per_gate;
         }
     };
-    Raw raw;
-    if constexpr (HOLD) load(0, raw);
     for (int row = 0; row < rows; ++row) one_row(row, raw);
     // the arguments read again: nothing that only this end needs stays in
     // registers over the rows
     const auto& z = args_again<GradArgs>();
-    if constexpr (!MANY) {
-        const rsrc_t dg =
-            z.gate_direct ? t.row(z.dgate.p + gate_row * z.dgate.ld) : row_rsrc(nullptr, 0);
-        if (gated) load_gate(gate_row, gate);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float w[V], g[V];
-            weight(z.w1, s, w);
-            take_gate(gate, s, g);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                sw1[s][i] = g[i] * sa[s][i];
-                sa[s][i] *= z.alpha * w[i];
-            }
-            if (z.gate_direct) t.store(dg, s, sa[s]);
-        }
-    }
     // partial rows, 32 bits each
     float* ws = z.ws + chunk * z.ws_slots * z.ws_pitch;
     auto leave = [&](int slot, float (*v)[V]) {
@@ -327,35 +320,54 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
                     (u32x4){as_u(v[s][i]), as_u(v[s][i + 1]), as_u(v[s][i + 2]), as_u(v[s][i + 3])},
                     r, (t.col(s) + i) * 4, 0, 0);
     };
-    leave(z.slot_w1, sw1);
+    leave(z.slot_w1, MANY ? sw1 : sa);
     leave(z.slot_w2, sw2);
-    leave(z.slot_gate, sa);
 }
 
 // Adds partial rows: output row o (blockIdx.y: first dw1 and dw2 as wanted,
-// then the gate rows) is the sum over its chunks.  A workgroup takes 64
+// then the gate rows) is the sum over its chunks, dw1's times their gate rows.  A workgroup takes 64
 // columns, 16 lanes of 4, and 64 partial sums of every 64th chunk each, joined
 // in the LDS in a fixed order.
 constexpr int kJoinCols = 64, kJoinParts = 64;
 
 template <int DT>
 __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64_t outputs) {
+    using E = Elem<DT>;
     __shared__ f32x4 part[kJoinParts][kJoinCols / 4];
     const int lane = (int)threadIdx.x % 16, p = (int)threadIdx.x / 16;
     const int col = (int)blockIdx.x * kJoinCols + lane * 4;
-    const int weights = (a.slot_w1 >= 0) + (a.slot_w2 >= 0);
+    const int weights = (a.dw1 != nullptr) + (a.dw2 != nullptr);
+    // the gate's values at this thread's columns (zeros past the row)
+    auto gate_factors = [&](const char* row) {
+        const char* q = row + (int64_t)col * E::kBytes;
+        f32x4 g = (f32x4)(0.0f);
+        if constexpr (E::V == 4) {
+            if (col + 4 <= a.cols) return __builtin_bit_cast(f32x4, (u32x4)*reinterpret_cast<const u32x4_any*>(q));
+        } else {
+            if (col + 4 <= a.cols) {
+                const u32x2 w = *reinterpret_cast<const u32x2_any*>(q);
+                float v[8];
+                E::widen((u32x4){w[0], w[1], 0u, 0u}, v);
+                return (f32x4){v[0], v[1], v[2], v[3]};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (col + i < a.cols) g[i] = E::load1(q + i * E::kBytes);
+        return g;
+    };
     for (int64_t o = blockIdx.y; o < outputs; o += gridDim.y) {
-        int slot;
+        int slot = a.slot_w1;
         int64_t first = 0, count = a.chunks;
         char* out;
-        bool f32 = true;
+        bool f32 = true, gates = false;
         if (o < weights) {
-            const bool is_w1 = a.slot_w1 >= 0 && o == 0;
-            slot = is_w1 ? a.slot_w1 : a.slot_w2;
+            const bool is_w1 = a.dw1 != nullptr && o == 0;
+            if (!is_w1) slot = a.slot_w2;
+            gates = is_w1 && a.chunk_gates == kOneGate;
             out = is_w1 ? a.dw1 : a.dw2;
             f32 = a.w_f32 != 0;
         } else {
-            slot = a.slot_gate;
             count = a.chunks_per_unit;
             first = (o - weights) * count;
             out = a.dgate.p + (o - weights) * a.dgate.ld;
@@ -365,9 +377,19 @@ __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64
         if (col < a.cols) {
             const float* ws = a.ws + (first * a.ws_slots + slot) * a.ws_pitch + col;
             const int64_t step = (int64_t)a.ws_slots * a.ws_pitch;
+            if (gates && a.gate_units != 0) {
+                // each chunk's A times the gate row of its rows
+#pragma unroll 4
+                for (uint32_t c = (uint32_t)p; c < (uint32_t)count; c += kJoinParts) {
+                    const int64_t row = c / (uint32_t)a.chunks_per_unit;
+                    sum += *reinterpret_cast<const f32x4*>(ws + c * step) *
+                           gate_factors(a.gate.p + row * a.gate.ld);
+                }
+            } else {
 #pragma unroll 8
-            for (int64_t c = p; c < count; c += kJoinParts)
-                sum += *reinterpret_cast<const f32x4*>(ws + c * step);
+                for (int64_t c = p; c < count; c += kJoinParts)
+                    sum += *reinterpret_cast<const f32x4*>(ws + c * step);
+            }
         }
         part[p][lane] = sum;
         __syncthreads();
@@ -378,7 +400,18 @@ __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64
         }
         const int c = (int)threadIdx.x, at = (int)blockIdx.x * kJoinCols + c;
         if (c < kJoinCols && at < a.cols) {
-            const float total = part[0][c / 4][c % 4];
+            float total = part[0][c / 4][c % 4];
+            if (gates) {
+                total *= a.alpha;
+                if (a.gate.p != nullptr && a.gate_units == 0)  // one gate row for all
+                    total *= E::load1(a.gate.p + (int64_t)at * E::kBytes);
+            }
+            if (o >= weights) {  // alpha (w1 + o) A
+                total *= a.alpha;
+                if (a.w1 != nullptr)
+                    total *= a.offset + (a.w_f32 ? Elem<PTORED_F32>::load1(a.w1 + (int64_t)at * 4)
+                                                 : E::load1(a.w1 + (int64_t)at * E::kBytes));
+            }
             if (f32)
                 Elem<PTORED_F32>::store1(out + (int64_t)at * 4, total);
             else
@@ -439,8 +472,8 @@ int grad_launch(const GradArgs& a, hipStream_t stream) {
         }
     }
     if (rc != kOk) return rc;
-    int64_t outputs = (a.slot_w1 >= 0) + (a.slot_w2 >= 0);
-    if (a.slot_gate >= 0) outputs += a.gate_rows;
+    int64_t outputs = (a.dw1 != nullptr) + (a.dw2 != nullptr);
+    if (a.gate_joined) outputs += a.gate_rows;
     if (outputs == 0) return kOk;
     const dim3 grid((uint32_t)((a.cols + kJoinCols - 1) / kJoinCols),
                     (uint32_t)(outputs < 32768 ? outputs : 32768));

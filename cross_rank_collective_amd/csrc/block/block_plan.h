@@ -63,10 +63,11 @@ struct GradArgs {
     int64_t rows_per_gate;
     int64_t ws_pitch;     // the columns, rounded up to whole vectors of 4
     int32_t chunk_gates;  // kOneGate, kEachGate or kSomeGates
-    int32_t gate_direct;  // 1: whole gate rows lie inside chunks, which write them at once
-    int32_t ws_slots;     // partial rows per chunk: dw1, dw2 and, without gate_direct, dgate
-    int32_t slot_w2, slot_gate;  // position of dw2's and dgate's (dw1's is 0); -1: none
-    int32_t slot_w1;
+    int32_t gate_direct;  // 1: chunks hold whole gate rows and write their gradients
+    int32_t gate_joined;  // 1: the gate's gradients come from the chunks' A
+    int32_t gate_units;   // gate rows from one unit to the next: 1, or 0 with one in all
+    int32_t ws_slots;     // partial rows per chunk: A or dw1, and dw2
+    int32_t slot_w1, slot_w2;  // which of them; -1: none
     int32_t cols, w_f32;
     float offset, alpha, beta, inv_cols;
 };

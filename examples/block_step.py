@@ -103,7 +103,7 @@ def main(argv=None):
 
     x_out, y, saved = b.forward(parts, x)
     dx, dpart, grads = b.backward(dx_out, dy, saved)
-    want = plain(b, parts, x, dx_out, dy)
+    want = {k: v.detach() for k, v in plain(b, parts, x, dx_out, dy).items()}
     got = {"stream": x_out, "y": y, "dx": dx, "dpart": dpart, **grads}
     apart = {k: float((got[k].float() - w).norm() / w.norm()) for k, w in want.items()}
 

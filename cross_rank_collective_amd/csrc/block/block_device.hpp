@@ -333,21 +333,23 @@ __device__ __forceinline__ uint32_t dpp(uint32_t u) {
 constexpr int kDppXor1 = 0xB1;         // lanes 1 0 3 2 of each quad
 constexpr int kDppXor2 = 0x4E;         // lanes 2 3 0 1 of each quad
 constexpr int kDppHalfMirror = 0x141;  // lane i of 8 takes 7 - i
-constexpr int kDppMirror = 0x140;      // lane i of 16 takes 15 - i
 
-// The wave's sum, the same in every lane: four steps inside rows of 16 lanes
-// by data-parallel moves, then the four rows' sums read as scalars.  (A
-// shuffle through the LDS per step takes several times as long.)
+// One step of a sum over the wave: adds what CTRL moves into the lanes of the
+// rows (of 16 lanes) in ROWS, nothing elsewhere.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_moved(float x) {
+    return x + as_f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_u(x), CTRL, ROWS, 0xF, true));
+}
+// The wave's sum, in lane 63: inside rows by shifts of 1, 2, 4 and 8 lanes,
+// then each row's last lane into the next row, then the half's into the other
+// half.  (A shuffle through the LDS per step takes several times as long.)
 __device__ __forceinline__ float wave_sum(float x) {
-    x += as_f(dpp<kDppXor1>(as_u(x)));
-    x += as_f(dpp<kDppXor2>(as_u(x)));
-    x += as_f(dpp<kDppHalfMirror>(as_u(x)));
-    x += as_f(dpp<kDppMirror>(as_u(x)));
-    const int i = (int)as_u(x);
-    return (as_f((uint32_t)__builtin_amdgcn_readlane(i, 0)) +
-            as_f((uint32_t)__builtin_amdgcn_readlane(i, 16))) +
-           (as_f((uint32_t)__builtin_amdgcn_readlane(i, 32)) +
-            as_f((uint32_t)__builtin_amdgcn_readlane(i, 48)));
+    x = add_moved<0x111, 0xF>(x);
+    x = add_moved<0x112, 0xF>(x);
+    x = add_moved<0x114, 0xF>(x);
+    x = add_moved<0x118, 0xF>(x);
+    x = add_moved<0x142, 0xA>(x);
+    return add_moved<0x143, 0xC>(x);
 }
 
 constexpr int kMaxWaves = 16;  // waves of the largest workgroup
@@ -362,8 +364,12 @@ __device__ __forceinline__ void block_sum(f32x4 (*red)[kMaxWaves / 4], float* v)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
     const int waves = (int)blockDim.x >> 6, wave = (int)threadIdx.x >> 6;
-    if (waves == 1) return;
-    if ((threadIdx.x & 63) == 0) {
+    if (waves == 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = as_f((uint32_t)__builtin_amdgcn_readlane((int)as_u(v[k]), 63));
+        return;
+    }
+    if ((threadIdx.x & 63) == 63) {
 #pragma unroll
         for (int k = 0; k < K; ++k) red[k][wave / 4][wave % 4] = v[k];
         // the last wave fills its group of four

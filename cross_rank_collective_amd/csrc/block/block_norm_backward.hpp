@@ -206,7 +206,7 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
 
     int turn = 0;
     bool fresh = MANY;  // the row begins a gate row, or the chunk
-    auto one_row = [&](int row, Raw& raw) {
+    auto one_row = [&](int row, Raw& raw, Raw& next) {
         if constexpr (!HOLD) {
             load(row, raw);
             if (MANY && fresh) load_gate(gate_row, gate);
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
         }
         fresh = MANY && row + 1 == gate_end;
         if constexpr (HOLD) {
-            load(row + 1, raw);
+            load(row + 1, next);
             if ((EACH || fresh) && row + 1 < rows) load_gate(gate_row + a.row_step, gate);
         }
         if (post || pre) block_sum<3>(red[turn], sum);
@@ -303,7 +303,13 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
             gate_end += a.row_step > 1 ? 1 : a.rows_per_gate;
         }
     };
-    for (int row = 0; row < rows; ++row) one_row(row, raw);
+    // two rows a turn, each loading the other's: nothing is copied between them
+    Raw other;
+    for (int row = 0; row < rows; row += 2) {
+        one_row(row, raw, other);
+        if (row + 1 == rows) break;
+        one_row(row + 1, other, raw);
+    }
     // the arguments read again: nothing that only this end needs stays in
     // registers over the rows
     const auto& z = args_again<GradArgs>();

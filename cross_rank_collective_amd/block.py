@@ -163,8 +163,11 @@ def _init() -> None:
     import torch
 
     _load()
-    from . import _torch_calls
-
+    try:
+        from . import _torch_calls
+    except ImportError as e:
+        raise RuntimeError("the extension of the tensor calls is missing or was built for another "
+                           "torch: build it with `python -m cross_rank_collective_amd.build`") from e
     _native = _torch_calls
 
     _FLOAT32, _INT8, _UINT8 = torch.float32, torch.int8, torch.uint8

@@ -12,6 +12,17 @@
 // taken from the finished x' (from the sums of h^2, h x and x^2 it would lose
 // all digits where the branch cancels the residual), so a row needs two
 // workgroup sums.
+//
+// What it took, on one MI355X (bf16, 4096 rows):
+//   8 partials of 8192 columns, no norm after the block: 118 us, 6.2 TB/s of
+//   the bytes above (112 us at the rate of an elementwise copy).
+//   2 partials of 4096 columns, both norms, a gate, h and x' kept in 8 bits:
+//   44 us, 4.6 TB/s; four times the rows 141 us, 5.7 TB/s: 8 us of a call are
+//   its start and end.  The weights and the gate are asked for before the sum
+//   that precedes their use (after it: 47 us).
+// One token of 8192 columns and 8 partials takes 3.9 us, of which an empty
+// kernel's launch is 1.5 us and the rest one chain of kernel arguments, loads,
+// sum and store.
 #pragma once
 
 #include "block_device.hpp"

@@ -19,6 +19,15 @@
 // leaves one partial row per sum in the workspace (A where its rows share one
 // gate row, dw1's share where they do not), and a second kernel adds those in a
 // fixed order.
+//
+// What it took, on one MI355X: 16384 x 4096 in bf16 from packed activations
+// 112 us (5.9 TB/s of its bytes; 127 us, 5.3 TB/s, call after call, when each
+// also pays for the last one's writes) and 6 us for the second kernel; 4096 x
+// 1536 in f32 from whole ones 31 + 6.5 us (4.9 TB/s).  A row takes a wave 240
+// vector instructions, a third of the time.  Chunks of consecutive rows
+// instead of interleaved ones, whose workgroups keep hitting the same memory
+// channels, took 136 us for the first; two rows ahead instead of one do not
+// fit the registers (187 us).
 #pragma once
 
 #include "block_device.hpp"
@@ -36,7 +45,9 @@ struct Activation<true> {
     KeptRaw w;
 };
 
-// With one gate row in the chunk (GATES), A tells its gradients at the end.
+// GATES: with one gate row in the chunk its gradients come from A; a gate row
+// for every row needs no A, and saves 12% of what the general form takes (8192
+// x 4096 in bf16, packed: 108 us, 122 us).
 template <int DT, int S, int EDGE, bool PACKED, int GATES>
 __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
     using E = Elem<DT>;

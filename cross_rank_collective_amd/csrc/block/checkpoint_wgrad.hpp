@@ -21,6 +21,16 @@
 // LDS rows are cut into 64-byte pieces; row t keeps piece c at c ^ (t & 3), so
 // that the four rows a transposing load reads at one piece lie in different
 // banks.
+//
+// What it took, on one MI355X (bf16): 8192 tokens x 4096 x 4096 in tiles of 256
+// x 256 250 us, 1.1 PFLOP/s (a plain matrix product of the same layout by the
+// vendor's library 286 us from bfloat16 operands; 213 us at the rate of its
+// 8192^3 product).  The matrix cores are busy 53% of the cycles, and the card
+// lowers its clock to 1.95 GHz; the LDS is busy 40%.  Staging x takes 44
+// vector instructions for each 16 values, which a larger tile shares among more
+// products: 128 x 128 tiles reach 0.65 PFLOP/s.  Those have two groups of
+// waves, each for half of the tokens, joined in the LDS at the end: 1024 x 2048
+// x 2048 20 us, with one group 25 us.
 #pragma once
 
 #include <type_traits>

@@ -342,9 +342,10 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
 }
 
 // Adds partial rows: output row o (blockIdx.y: first dw1 and dw2 as wanted,
-// then the gate rows) is the sum over its chunks, dw1's times their gate rows.  A workgroup takes 64
-// columns, 16 lanes of 4, and 64 partial sums of every 64th chunk each, joined
-// in the LDS in a fixed order.
+// then the gate rows) is the sum over its chunks, dw1's times their gate rows.
+// A workgroup takes 64 columns, 16 lanes of 4, and 64 partial sums of every
+// 64th chunk each, joined in the LDS in a fixed order.  (512 chunks of 4096
+// columns: 6.5 us; 32 columns a workgroup 8.9, 128 7.5.)
 constexpr int kJoinCols = 64, kJoinParts = 64;
 
 template <int DT>

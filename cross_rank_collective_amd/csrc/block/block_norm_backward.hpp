@@ -343,17 +343,19 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
 
 // Adds partial rows: output row o (blockIdx.y: first dw1 and dw2 as wanted,
 // then the gate rows) is the sum over its chunks, dw1's times their gate rows.
-// A workgroup takes 64 columns, 16 lanes of 4, and 64 partial sums of every
-// 64th chunk each, joined in the LDS in a fixed order.  (512 chunks of 4096
-// columns: 6.5 us; 32 columns a workgroup 8.9, 128 7.5.)
-constexpr int kJoinCols = 64, kJoinParts = 64;
+// A workgroup takes COLS columns in lanes of 4 and 4096 / COLS partial sums, one
+// for each chunk of a stride, joined in the LDS in a fixed order.  64 columns
+// (512 chunks of 4096 columns: 6.5 us; with 32 8.9, with 128 7.5), or 16 where
+// 64 leave compute units idle and chunks are many (two gate rows and two weights
+// of 747 columns in 512 chunks: 17 us against 28; one weight of 1000: 5.4 against 8.3).
 
-template <int DT>
+template <int DT, int COLS>
 __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64_t outputs) {
     using E = Elem<DT>;
-    __shared__ f32x4 part[kJoinParts][kJoinCols / 4];
-    const int lane = (int)threadIdx.x % 16, p = (int)threadIdx.x / 16;
-    const int col = (int)blockIdx.x * kJoinCols + lane * 4;
+    constexpr int kLanes = COLS / 4, kParts = 1024 / kLanes;
+    __shared__ f32x4 part[kParts][kLanes];
+    const int lane = (int)threadIdx.x % kLanes, p = (int)threadIdx.x / kLanes;
+    const int col = (int)blockIdx.x * COLS + lane * 4;
     const int weights = (a.dw1 != nullptr) + (a.dw2 != nullptr);
     // the gate's values at this thread's columns (zeros past the row)
     auto gate_factors = [&](const char* row) {
@@ -397,27 +399,27 @@ __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64
             const int64_t step = (int64_t)a.ws_slots * a.ws_pitch;
             if (gates && a.gate_units != 0) {
                 // each chunk's A times the gate row of its rows
-#pragma unroll 4
-                for (uint32_t c = (uint32_t)p; c < (uint32_t)count; c += kJoinParts) {
+#pragma unroll(COLS == 64 ? 4 : 8)
+                for (uint32_t c = (uint32_t)p; c < (uint32_t)count; c += kParts) {
                     const int64_t row = c / (uint32_t)a.chunks_per_unit;
                     sum += *reinterpret_cast<const f32x4*>(ws + c * step) *
                            gate_factors(a.gate.p + row * a.gate.ld);
                 }
             } else {
 #pragma unroll 8
-                for (int64_t c = p; c < count; c += kJoinParts)
+                for (int64_t c = p; c < count; c += kParts)
                     sum += *reinterpret_cast<const f32x4*>(ws + c * step);
             }
         }
         part[p][lane] = sum;
         __syncthreads();
 #pragma unroll
-        for (int half = kJoinParts / 2; half >= 1; half /= 2) {
+        for (int half = kParts / 2; half >= 1; half /= 2) {
             if (p < half) part[p][lane] += part[p + half][lane];
             __syncthreads();
         }
-        const int c = (int)threadIdx.x, at = (int)blockIdx.x * kJoinCols + c;
-        if (c < kJoinCols && at < a.cols) {
+        const int c = (int)threadIdx.x, at = (int)blockIdx.x * COLS + c;
+        if (c < COLS && at < a.cols) {
             float total = part[0][c / 4][c % 4];
             if (gates) {
                 total *= a.alpha;
@@ -493,13 +495,14 @@ int grad_launch(const GradArgs& a, hipStream_t stream) {
     int64_t outputs = (a.dw1 != nullptr) + (a.dw2 != nullptr);
     if (a.gate_joined) outputs += a.gate_rows;
     if (outputs == 0) return kOk;
-    const dim3 grid((uint32_t)((a.cols + kJoinCols - 1) / kJoinCols),
+    const bool narrow = (a.cols + 63) / 64 * outputs < 128 && a.chunks_per_unit > 64;
+    const int cols = narrow ? 16 : 64;
+    const void* k = narrow ? reinterpret_cast<const void*>(grad_join_kernel<DT, 16>)
+                           : reinterpret_cast<const void*>(grad_join_kernel<DT, 64>);
+    const dim3 grid((uint32_t)((a.cols + cols - 1) / cols),
                     (uint32_t)(outputs < 32768 ? outputs : 32768));
     void* args[] = {const_cast<GradArgs*>(&a), &outputs};
-    return hipLaunchKernel(reinterpret_cast<const void*>(grad_join_kernel<DT>), grid, dim3(1024),
-                           args, 0, stream) == hipSuccess
-               ? kOk
-               : kFailed;
+    return hipLaunchKernel(k, grid, dim3(1024), args, 0, stream) == hipSuccess ? kOk : kFailed;
 }
 
 }  // namespace block

@@ -84,6 +84,10 @@ CHUNKS = [
     ("f32", 300, 8196, True, 1, True, True, False, 0, 0, 0.0, False),
     ("bf16", 300, 16376, True, 300, True, True, True, 0, 0, 0.0, True),
     ("bf16", 280, 9000, False, 1, True, True, False, 0, 0, 0.0, True),
+    # few columns and many chunks, joined by narrower workgroups
+    ("bf16", 3000, 747, True, 2, True, True, True, 0, 0, 0.0, True),
+    ("f16", 5000, 36, True, 5, True, False, True, 1, 1, 1.0, True),
+    ("f32", 2100, 1003, True, 1, True, True, False, 0, 0, 0.0, True),
 ]
 
 

@@ -345,9 +345,11 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
 // then the gate rows) is the sum over its chunks, dw1's times their gate rows.
 // A workgroup takes COLS columns in lanes of 4 and 4096 / COLS partial sums, one
 // for each chunk of a stride, joined in the LDS in a fixed order.  64 columns
-// (512 chunks of 4096 columns: 6.5 us; with 32 8.9, with 128 7.5), or 16 where
-// 64 leave compute units idle and chunks are many (two gate rows and two weights
-// of 747 columns in 512 chunks: 17 us against 28; one weight of 1000: 5.4 against 8.3).
+// (512 chunks of 4096 columns: 6.5 us; with 32 8.9, with 128 7.5) where that
+// makes more than 112 workgroups.  Below it compute units idle, and 32 take
+// less time (3500 columns of two weights, 768 chunks: 6.4 us against 7.2, with 16
+// 9.7; four rows of 747: 11.5, 21.6 and 14.3), at no more than 32 workgroups 16
+// (1000 columns of a weight: 6.7 us, with 32 8.2, with 64 10.1).
 
 template <int DT, int COLS>
 __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64_t outputs) {
@@ -495,10 +497,11 @@ int grad_launch(const GradArgs& a, hipStream_t stream) {
     int64_t outputs = (a.dw1 != nullptr) + (a.dw2 != nullptr);
     if (a.gate_joined) outputs += a.gate_rows;
     if (outputs == 0) return kOk;
-    const bool narrow = (a.cols + 63) / 64 * outputs < 128 && a.chunks_per_unit > 64;
-    const int cols = narrow ? 16 : 64;
-    const void* k = narrow ? reinterpret_cast<const void*>(grad_join_kernel<DT, 16>)
-                           : reinterpret_cast<const void*>(grad_join_kernel<DT, 64>);
+    const int64_t groups = a.chunks_per_unit > 64 ? (a.cols + 63) / 64 * outputs : 256;
+    const int cols = groups <= 32 ? 16 : groups <= 112 ? 32 : 64;
+    const void* k = cols == 16   ? reinterpret_cast<const void*>(grad_join_kernel<DT, 16>)
+                    : cols == 32 ? reinterpret_cast<const void*>(grad_join_kernel<DT, 32>)
+                                 : reinterpret_cast<const void*>(grad_join_kernel<DT, 64>);
     const dim3 grid((uint32_t)((a.cols + cols - 1) / cols),
                     (uint32_t)(outputs < 32768 ? outputs : 32768));
     void* args[] = {const_cast<GradArgs*>(&a), &outputs};

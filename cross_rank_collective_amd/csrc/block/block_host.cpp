@@ -122,7 +122,11 @@ int status_of(int rc) { return rc == kOk ? PTORED_OK : PTORED_ERR_HIP; }
 // at once on the chip: with fewer, compute units idle; with more, the last
 // ones run alone and the partial rows that chunks leave (8 bytes a column,
 // written and read) grow.  A wave is 64 slots wide; its registers leave room
-// for 16 waves of 8-element slots on a compute unit and for 20 of 4.
+// for 16 waves of 8-element slots on a compute unit and for 20 of 4.  But with
+// work for all compute units a chunk has 5 rows at least: with fewer the partial
+// rows weigh as much as the rows' own data (both kernels, bf16, packed: 4096 x
+// 1024 28 us without the rule, 24 with 3 rows, 21 with 5, 22 with 7; 1511 x 2520
+// 27, 23, 23, 22; 512 x 4096 22, 17 with 2 rows).
 GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows, int dtype,
                      bool in_order = false) {
     GradSplit s{};
@@ -130,7 +134,8 @@ GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows, int dtype,
     const int64_t slot = dtype == PTORED_F32 ? 4 : 8, room = dtype == PTORED_F32 ? 20 : 16;
     const int64_t waves = std::min<int64_t>(16, (cols + 64 * slot - 1) / (64 * slot));
     const int64_t target = 256 * (room / waves);
-    const int64_t per = (rows + target - 1) / target;
+    const int64_t per = std::max((rows + target - 1) / target,
+                                 std::min<int64_t>(5, (rows + 255) / 256));
     const int64_t unit = gate_rows > 0 ? rows / gate_rows : rows;
     if (gate_rows > 0 && unit <= per) {  // whole gate rows inside a chunk
         s.unit_rows = rows;

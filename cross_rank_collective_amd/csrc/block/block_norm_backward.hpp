@@ -30,6 +30,8 @@
 // fit the registers (187 us).
 #pragma once
 
+#include <algorithm>
+
 #include "block_device.hpp"
 
 namespace ptored {
@@ -351,9 +353,46 @@ __global__ __launch_bounds__(1024) void grad_kernel(const GradArgs a) {
 // 9.7; four rows of 747: 11.5, 21.6 and 14.3), at no more than 32 workgroups 16
 // (1000 columns of a weight: 6.7 us, with 32 8.2, with 64 10.1).
 
+// Gate rows of no more than kFlatChunks chunks, in more workgroups than the chip
+// holds at once (two a compute unit): there the last `flat` rows of workgroups
+// take 4 columns of a gate row for every thread instead (4096 x 4096 with 128
+// gate rows 65 -> 9 us, with 32 20 -> 8.5 us; with 8, which fit, 8.6 and 9; 8
+// rows of 1024 columns 4.7 and 7.8).
+constexpr int kFlatChunks = 32;
+
 template <int DT, int COLS>
-__global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64_t outputs) {
+__global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64_t outputs,
+                                                         uint32_t flat) {
     using E = Elem<DT>;
+    // alpha (w1 + o) A
+    auto gate_gradient = [&](float sum, int at) {
+        sum *= a.alpha;
+        if (a.w1 != nullptr)
+            sum *= a.offset + (a.w_f32 ? Elem<PTORED_F32>::load1(a.w1 + (int64_t)at * 4)
+                                       : E::load1(a.w1 + (int64_t)at * E::kBytes));
+        return sum;
+    };
+    if (blockIdx.y >= gridDim.y - flat) {
+        const int64_t quads = a.ws_pitch / 4, items = a.gate_rows * quads;
+        const int64_t block = (int64_t)(blockIdx.y - (gridDim.y - flat)) * gridDim.x + blockIdx.x;
+        const int64_t stride = (int64_t)a.ws_slots * a.ws_pitch;
+        for (int64_t i = block * 1024 + threadIdx.x; i < items;
+             i += (int64_t)flat * gridDim.x * 1024) {
+            const int64_t row = i / quads;
+            const int at = (int)(i - row * quads) * 4;
+            const float* ws = a.ws + row * a.chunks_per_unit * stride + a.slot_w1 * a.ws_pitch + at;
+            f32x4 sum = (f32x4)(0.0f);
+#pragma unroll 8
+            for (int64_t c = 0; c < a.chunks_per_unit; ++c)
+                sum += *reinterpret_cast<const f32x4*>(ws + c * stride);
+            char* out = a.dgate.p + row * a.dgate.ld;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (at + k < a.cols)
+                    E::store1(out + (int64_t)(at + k) * E::kBytes, gate_gradient(sum[k], at + k));
+        }
+        return;
+    }
     constexpr int kLanes = COLS / 4, kParts = 1024 / kLanes;
     __shared__ f32x4 part[kParts][kLanes];
     const int lane = (int)threadIdx.x % kLanes, p = (int)threadIdx.x / kLanes;
@@ -378,7 +417,7 @@ __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64
             if (col + i < a.cols) g[i] = E::load1(q + i * E::kBytes);
         return g;
     };
-    for (int64_t o = blockIdx.y; o < outputs; o += gridDim.y) {
+    for (int64_t o = blockIdx.y; o < outputs; o += gridDim.y - flat) {
         int slot = a.slot_w1;
         int64_t first = 0, count = a.chunks;
         char* out;
@@ -428,12 +467,7 @@ __global__ __launch_bounds__(1024) void grad_join_kernel(const GradArgs a, int64
                 if (a.gate.p != nullptr && a.gate_units == 0)  // one gate row for all
                     total *= E::load1(a.gate.p + (int64_t)at * E::kBytes);
             }
-            if (o >= weights) {  // alpha (w1 + o) A
-                total *= a.alpha;
-                if (a.w1 != nullptr)
-                    total *= a.offset + (a.w_f32 ? Elem<PTORED_F32>::load1(a.w1 + (int64_t)at * 4)
-                                                 : E::load1(a.w1 + (int64_t)at * E::kBytes));
-            }
+            if (o >= weights) total = gate_gradient(total, at);
             if (f32)
                 Elem<PTORED_F32>::store1(out + (int64_t)at * 4, total);
             else
@@ -495,16 +529,21 @@ int grad_launch(const GradArgs& a, hipStream_t stream) {
     }
     if (rc != kOk) return rc;
     int64_t outputs = (a.dw1 != nullptr) + (a.dw2 != nullptr);
-    if (a.gate_joined) outputs += a.gate_rows;
-    if (outputs == 0) return kOk;
-    const int64_t groups = a.chunks_per_unit > 64 ? (a.cols + 63) / 64 * outputs : 256;
+    const bool few = a.gate_joined && a.rows > 0 && a.chunks_per_unit <= kFlatChunks &&
+                     a.gate_rows * ((a.cols + 63) / 64) > 512;
+    if (a.gate_joined && !few) outputs += a.gate_rows;
+    if (outputs == 0 && !few) return kOk;
+    const int64_t chunks = few ? a.chunks : a.chunks_per_unit;  // of an output, or of most
+    const int64_t groups = chunks > 64 ? (a.cols + 63) / 64 * outputs : 256;
     const int cols = groups <= 32 ? 16 : groups <= 112 ? 32 : 64;
     const void* k = cols == 16   ? reinterpret_cast<const void*>(grad_join_kernel<DT, 16>)
                     : cols == 32 ? reinterpret_cast<const void*>(grad_join_kernel<DT, 32>)
                                  : reinterpret_cast<const void*>(grad_join_kernel<DT, 64>);
-    const dim3 grid((uint32_t)((a.cols + cols - 1) / cols),
-                    (uint32_t)(outputs < 32768 ? outputs : 32768));
-    void* args[] = {const_cast<GradArgs*>(&a), &outputs};
+    const uint32_t x = (uint32_t)((a.cols + cols - 1) / cols);
+    const int64_t per_row = 1024 * (int64_t)x, items = few ? a.gate_rows * (a.ws_pitch / 4) : 0;
+    uint32_t flat = (uint32_t)std::min<int64_t>((items + per_row - 1) / per_row, 32768);
+    const dim3 grid(x, (uint32_t)(outputs < 32768 ? outputs : 32768) + flat);
+    void* args[] = {const_cast<GradArgs*>(&a), &outputs, &flat};
     return hipLaunchKernel(k, grid, dim3(1024), args, 0, stream) == hipSuccess ? kOk : kFailed;
 }
 

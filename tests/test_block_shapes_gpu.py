@@ -88,6 +88,12 @@ CHUNKS = [
     ("bf16", 3000, 747, True, 2, True, True, True, 0, 0, 0.0, True),
     ("f16", 5000, 36, True, 5, True, False, True, 1, 1, 1.0, True),
     ("f32", 2100, 1003, True, 1, True, True, False, 0, 0, 0.0, True),
+    # many gate rows of a few chunks each, few of them, and some of many chunks
+    ("bf16", 1040, 520, True, 65, True, True, True, 1, 0, 0.0, True),
+    ("f32", 1400, 1003, True, 40, True, True, False, 0, 1, 0.0, True),
+    ("f16", 6600, 39, False, 600, True, False, False, 0, 0, 1.0, True),
+    ("f32", 1400, 1003, True, 20, True, True, False, 0, 1, 0.0, True),
+    ("bf16", 4000, 259, True, 5, False, True, True, 0, 0, 0.0, True),
 ]
 
 
@@ -110,6 +116,18 @@ def test_backward_of_several_rows_a_workgroup(case):
         for name in ("dw1", "dw2"):
             if name in some:
                 R.close(some[name].t[0], *want[name], name)
+
+
+@pytest.mark.parametrize("case", [c for c in CHUNKS if c[4] > 1],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_a_gates_gradient_alone_keeps_its_bits(case):
+    say("gate alone", *case)
+    _, g, acts, ins, vec = grad_case(case)
+    full = run_backward(case, g, acts, ins, vec)
+    alone = run_backward(case, g, acts, ins, vec, dx=None, dh=None, dpost_weight=None,
+                         dpre_weight=None)
+    assert torch.equal(alone["dgate"].t, full["dgate"].t)
+    check_rest(alone)
 
 
 def test_backward_without_a_norm_after_the_block_passes_an_infinite_fold():

@@ -341,6 +341,7 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     const ptored_block_params& p = *params;
     const bool pre = p.pre_weight != nullptr, post = p.post_weight != nullptr;
     const bool need_h = post || io->dgate.data != nullptr;
+    const int64_t gate_rows = p.gate.data ? p.gate_rows : 0;  // not read without a gate
     const bool packed = io->x_kept.q != nullptr || io->h_kept.q != nullptr;
     if (packed && (io->x_out.data || io->h.data)) return PTORED_ERR_INVALID_ARG;
     if (pre != (io->dz.data != nullptr) || (!pre && io->dx_out.data == nullptr))
@@ -358,12 +359,12 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
                     b.rows(io->dx_out.data, p.rows, p.cols, io->dx_out.ld, es, false) &&
                     b.rows(io->x_out.data, p.rows, p.cols, io->x_out.ld, es, false) &&
                     b.rows(io->h.data, p.rows, p.cols, io->h.ld, es, false) &&
-                    b.rows(p.gate.data, p.gate_rows, p.cols, p.gate.ld, es, false, false) &&
+                    b.rows(p.gate.data, gate_rows, p.cols, p.gate.ld, es, false, false) &&
                     b.kept(io->x_kept, p.rows, p.cols, false) &&
                     b.kept(io->h_kept, p.rows, p.cols, false) &&
                     b.rows(io->dx.data, p.rows, p.cols, io->dx.ld, es, true) &&
                     b.rows(io->dh.data, p.rows, p.cols, io->dh.ld, es, true) &&
-                    b.rows(io->dgate.data, p.gate_rows, p.cols, io->dgate.ld, es, true, false);
+                    b.rows(io->dgate.data, gate_rows, p.cols, io->dgate.ld, es, true, false);
     if (!ok) return PTORED_ERR_INVALID_ARG;
     if (!params_supported(params)) return PTORED_ERR_UNSUPPORTED;
     b.vec(p.post_weight, p.cols * ws, ws, false);
@@ -375,16 +376,16 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
 
     const bool gated = io->dgate.data != nullptr;
     // gate rows without a gradient: a chunk that walks several takes them in order
-    const bool in_order = !gated && p.gate.data && p.gate_rows > 1 && p.gate_rows < p.rows;
-    const GradSplit split = grad_split(p.rows, p.cols, gated ? p.gate_rows : 0, p.dtype, in_order);
+    const bool in_order = !gated && gate_rows > 1 && gate_rows < p.rows;
+    const GradSplit split = grad_split(p.rows, p.cols, gated ? gate_rows : 0, p.dtype, in_order);
     GradArgs a{};
     // with its gradient wanted, a chunk lies within a gate row or begins with one
-    const int64_t rows_per_gate = p.gate.data ? p.rows / p.gate_rows : p.rows;
-    const bool one = gated ? !split.gate_direct : p.gate.data == nullptr || p.gate_rows == 1;
+    const int64_t rows_per_gate = gate_rows > 0 ? p.rows / gate_rows : p.rows;
+    const bool one = gated ? !split.gate_direct : gate_rows <= 1;
     a.chunk_gates = one ? kOneGate : rows_per_gate == 1 ? kEachGate : kSomeGates;
     a.gate_direct = split.gate_direct;
     a.gate_joined = gated && !split.gate_direct;
-    a.gate_units = p.gate_rows > 1 ? 1 : 0;
+    a.gate_units = gate_rows > 1 ? 1 : 0;
     a.slot_w1 = a.slot_w2 = -1;
     if (io->dpost_weight || a.gate_joined) a.slot_w1 = a.ws_slots++;
     if (io->dpre_weight) a.slot_w2 = a.ws_slots++;
@@ -424,7 +425,7 @@ extern "C" int ptored_block_norm_backward(const ptored_block_params* params,
     a.chunk_first = split.chunk_first;
     a.row_step = split.row_step;
     a.chunks = split.chunks;
-    a.gate_rows = p.gate_rows;
+    a.gate_rows = gate_rows;
     a.rows_per_gate = rows_per_gate;
     a.w_f32 = p.weight_dtype == PTORED_F32;
     a.offset = p.weight_offset;

@@ -68,7 +68,8 @@ typedef struct ptored_block_params {
     const void* post_weight; /* w1 [D], or NULL: no norm after the block */
     const void* pre_weight;  /* w2 [D], or NULL: no norm before the next block */
     ptored_rows gate; /* g: gate_rows x D of `dtype`, or data NULL: no gate */
-    int64_t gate_rows; /* divides rows; row t takes gate row t / (rows / gate_rows) */
+    int64_t gate_rows; /* divides rows; row t takes gate row t / (rows / gate_rows).
+                          Not read without a gate */
     float weight_offset;  /* o, added to both weights (1: weights kept as offsets from 1) */
     float branch_scale;   /* alpha */
     float residual_scale; /* beta */

@@ -130,7 +130,7 @@ int status_of(int rc) { return rc == kOk ? PTORED_OK : PTORED_ERR_HIP; }
 GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows, int dtype,
                      bool in_order = false) {
     GradSplit s{};
-    if (rows == 0) return s;
+    if (rows == 0 || cols == 0) return s;
     const int64_t slot = dtype == PTORED_F32 ? 4 : 8, room = dtype == PTORED_F32 ? 20 : 16;
     const int64_t waves = std::min<int64_t>(16, (cols + 64 * slot - 1) / (64 * slot));
     const int64_t target = 256 * (room / waves);

@@ -72,13 +72,29 @@ int no_gate() {
     return 0;
 }
 
+// Rows without columns: nothing to do, whatever is asked for.
+int no_columns() {
+    for (int dtype : {PTORED_F32, PTORED_BF16, PTORED_F16})
+        for (int64_t rows : {int64_t(0), int64_t(1), int64_t(8), int64_t(5000)})
+            for (int64_t gate_rows : {int64_t(0), int64_t(1), rows}) {
+                int64_t bytes = -1;
+                EXPECT(ptored_block_norm_backward_workspace(rows, 0, gate_rows, &bytes) == PTORED_OK &&
+                           bytes == 0,
+                       "workspace of %lld rows", (long long)rows);
+                Call c(rows, 0, gate_rows, dtype);
+                const int before = g_last.count;
+                EXPECT(c.run() == PTORED_OK && g_last.count == before, "%lld rows", (long long)rows);
+            }
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
     const struct {
         const char* name;
         int (*check)();
-    } checks[] = {{"no_gate", no_gate}};
+    } checks[] = {{"no_gate", no_gate}, {"no_columns", no_columns}};
     for (const auto& c : checks)
         if (argc == 2 && std::strcmp(argv[1], c.name) == 0) return c.check();
     std::printf("no such check\n");

@@ -43,3 +43,7 @@ def run(program, name):
 
 def test_without_a_gate_its_rows_are_not_read(program):
     run(program, "no_gate")
+
+
+def test_rows_without_columns(program):
+    run(program, "no_columns")

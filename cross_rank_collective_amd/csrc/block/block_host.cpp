@@ -102,7 +102,6 @@ Kept kept(const ptored_checkpoint& k) {
 // types and limits.
 bool params_valid(const ptored_block_params* p) {
     if (p == nullptr || !shape_ok(p->rows, p->cols)) return false;
-    if (!(p->eps >= 0.0f)) return false;
     if (p->gate.data == nullptr) return true;
     return p->gate_rows > 0 && p->rows % p->gate_rows == 0;
 }
@@ -269,6 +268,7 @@ extern "C" int ptored_block_norm(const void* const* parts, int nranks, int64_t p
     if (!params_valid(params) || io == nullptr || io->x.data == nullptr)
         return PTORED_ERR_INVALID_ARG;
     const ptored_block_params& p = *params;
+    if (!(p.eps >= 0.0f)) return PTORED_ERR_INVALID_ARG;
     if (nranks == 0 && (p.post_weight || p.gate.data || io->h.data || io->h_kept.q))
         return PTORED_ERR_INVALID_ARG;
     if (p.post_weight == nullptr && io->post_rstd) return PTORED_ERR_INVALID_ARG;

@@ -88,13 +88,23 @@ int no_columns() {
     return 0;
 }
 
+// The backward pass takes the norms' reciprocals, and does not read eps.
+int eps_not_read() {
+    for (float eps : {-1.0f, __builtin_nanf("")}) {
+        Call c(64, 256, 2, PTORED_BF16);
+        c.p.eps = eps;
+        EXPECT(c.run() == PTORED_OK, "eps %g", (double)eps);
+    }
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
     const struct {
         const char* name;
         int (*check)();
-    } checks[] = {{"no_gate", no_gate}, {"no_columns", no_columns}};
+    } checks[] = {{"no_gate", no_gate}, {"no_columns", no_columns}, {"eps_not_read", eps_not_read}};
     for (const auto& c : checks)
         if (argc == 2 && std::strcmp(argv[1], c.name) == 0) return c.check();
     std::printf("no such check\n");

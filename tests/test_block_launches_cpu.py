@@ -47,3 +47,7 @@ def test_without_a_gate_its_rows_are_not_read(program):
 
 def test_rows_without_columns(program):
     run(program, "no_columns")
+
+
+def test_backward_does_not_read_eps(program):
+    run(program, "eps_not_read")

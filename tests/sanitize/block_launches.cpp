@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <vector>
 
 #include "block_stub.h"
 
@@ -98,13 +99,121 @@ int eps_not_read() {
     return 0;
 }
 
+// The rows of every chunk, walked as the kernel walks them: each row once,
+// gate rows as the chunk's form takes them, and no more workspace needed than
+// the query says, whatever is wanted of the sums.
+int row_cuts_of(int64_t rows, int64_t cols, int64_t gate_rows, int dtype, int wanted) {
+    char what[160];
+    std::snprintf(what, sizeof what, "%lld x %lld, %lld gate rows, type %d, wanted %d", (long long)rows,
+                  (long long)cols, (long long)gate_rows, dtype, wanted);
+    Call c(rows, cols, gate_rows, dtype);
+    if (!(wanted & 1)) c.io.dgate = {};
+    if (!(wanted & 2)) c.io.dpost_weight = nullptr;
+    if (!(wanted & 4)) c.io.dpre_weight = nullptr;
+    const bool gated = c.io.dgate.data != nullptr;
+    int64_t bytes = -1;
+    EXPECT(ptored_block_norm_backward_workspace(rows, cols, gated ? gate_rows : 0, &bytes) == PTORED_OK,
+           "%s", what);
+    c.io.workspace_bytes = bytes;
+    EXPECT(c.run() == PTORED_OK, "%s", what);
+    const GradArgs& a = g_last.grad;
+    EXPECT(a.chunks * a.ws_slots * a.ws_pitch * 4 <= bytes, "%s: workspace", what);
+    EXPECT(a.chunks >= 1 && a.chunks < (1 << 22), "%s: %lld chunks", what, (long long)a.chunks);
+    std::vector<char> seen(rows, 0), gate_seen(gate_rows > 0 ? gate_rows : 1, 0);
+    for (int64_t chunk = 0; chunk < a.chunks; ++chunk) {
+        const int64_t unit = chunk / a.chunks_per_unit, part = chunk - unit * a.chunks_per_unit;
+        const int64_t begin = unit * a.unit_rows + part * a.chunk_first;
+        const int64_t left = a.unit_rows - part * a.chunk_first;
+        int64_t n = (left + a.row_step - 1) / a.row_step;
+        if (n > a.chunk_rows) n = a.chunk_rows;
+        EXPECT(n >= 1, "%s: chunk %lld has %lld rows", what, (long long)chunk, (long long)n);
+        const bool gate = a.gate.p != nullptr;
+        int64_t now = gate ? begin / a.rows_per_gate : 0;
+        int64_t end = a.chunk_gates == kOneGate ? n
+                      : a.row_step > 1          ? 1
+                                                : (now + 1) * a.rows_per_gate - begin;
+        for (int64_t i = 0; i < n; ++i) {
+            const int64_t row = begin + i * a.row_step;
+            EXPECT(row < rows && !seen[row], "%s: row %lld of chunk %lld", what, (long long)row,
+                   (long long)chunk);
+            seen[row] = 1;
+            if (gate && i == end) {  // the next gate row
+                now += a.row_step;
+                end += a.row_step > 1 ? 1 : a.rows_per_gate;
+            }
+            EXPECT(!gate || now == row / a.rows_per_gate, "%s: gate row of row %lld", what, (long long)row);
+            // a chunk that writes a gate row's gradient holds all of its rows
+            if (a.gate_direct && (i + 1 == end || i + 1 == n)) {
+                EXPECT(now < gate_rows && !gate_seen[now] && i + 1 == end, "%s: gate row %lld", what,
+                       (long long)now);
+                gate_seen[now] = 1;
+            }
+        }
+        // the joining kernel's gate row of a chunk
+        EXPECT(!a.gate_joined || chunk / a.chunks_per_unit == begin / a.rows_per_gate, "%s: chunk %lld", what,
+               (long long)chunk);
+    }
+    for (int64_t r = 0; r < rows; ++r) EXPECT(seen[r], "%s: row %lld left out", what, (long long)r);
+    for (int64_t g = 0; a.gate_direct && g < gate_rows; ++g)
+        EXPECT(gate_seen[g], "%s: gate row %lld left out", what, (long long)g);
+    return 0;
+}
+
+int row_cuts() {
+    uint64_t state = 9;
+    auto draw = [&](int64_t n) {  // 0 to n - 1
+        state = state * 6364136223846793005u + 1442695040888963407u;
+        return (int64_t)((state >> 33) % (uint64_t)n);
+    };
+    const int64_t widths[] = {1, 7, 8, 33, 512, 513, 1023, 2048, 4096, 4097, 8192, 8193, 16384};
+    for (int i = 0; i < 4000; ++i) {
+        const int64_t cols = widths[draw(13)], per_gate = 1 + draw(draw(2) ? 12 : 700);
+        const int64_t gates = draw(4) == 0 ? 0 : 1 + draw(draw(2) ? 12 : 600);
+        const int64_t rows = gates == 0 ? 1 + draw(6000) : gates * per_gate;
+        if (row_cuts_of(rows, cols, gates, (int)draw(3), (int)draw(8))) return 1;
+    }
+    return 0;
+}
+
+// The tokens of every split of a weight gradient: all of them, each once, and
+// no more workspace needed than the query says.
+int token_splits() {
+    for (int dtype : {PTORED_F32, PTORED_BF16, PTORED_F16})
+        for (int64_t rows : {1, 2, 31, 64, 127, 128, 129, 1001, 4096, 9001, 32768})
+            for (int64_t outs : {1, 7, 8, 64, 129, 640, 2500})
+                for (int64_t cols : {1, 15, 16, 65, 512, 2049}) {
+                    int64_t bytes = -1;
+                    EXPECT(ptored_checkpoint_wgrad_workspace(rows, outs, cols, dtype, &bytes) == PTORED_OK,
+                           "query");
+                    const int st = ptored_checkpoint_wgrad(
+                        mat(1, outs), {fake(2), cols, fake(3), (cols + 31) / 32}, rows, outs, cols, dtype,
+                        mat(4, cols), PTORED_F32, 0, fake(5), bytes, nullptr);
+                    EXPECT(st == PTORED_OK, "%d", st);
+                    const WgradArgs& a = g_last.wgrad;
+                    EXPECT(a.splits >= 1 && (a.splits - 1) * a.rows_per_split < rows &&
+                               a.splits * a.rows_per_split >= rows,
+                           "%lld tokens, %d splits of %lld", (long long)rows, a.splits,
+                           (long long)a.rows_per_split);
+                    EXPECT(a.splits == 1 || a.splits * outs * a.ws_ld * 4 <= bytes, "workspace");
+                    const int64_t tm = a.shape == kWgradWide ? 256 : 128;
+                    const int64_t tn = a.shape == kWgradWide || (dtype == PTORED_F32 && a.shape == kWgradTile)
+                                           ? 256
+                                           : 128;
+                    EXPECT(a.tiles_m * tm >= outs && (a.tiles_m - 1) * tm < outs, "tiles");
+                    EXPECT(a.tiles_n * tn >= cols && (a.tiles_n - 1) * tn < cols, "tiles");
+                    EXPECT(a.shape == kWgradFew || (outs >= 8 && cols >= 16), "rows shorter than a chunk");
+                }
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
     const struct {
         const char* name;
         int (*check)();
-    } checks[] = {{"no_gate", no_gate}, {"no_columns", no_columns}, {"eps_not_read", eps_not_read}};
+    } checks[] = {{"no_gate", no_gate}, {"no_columns", no_columns}, {"eps_not_read", eps_not_read},
+                {"row_cuts", row_cuts}, {"token_splits", token_splits}};
     for (const auto& c : checks)
         if (argc == 2 && std::strcmp(argv[1], c.name) == 0) return c.check();
     std::printf("no such check\n");

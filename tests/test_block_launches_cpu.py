@@ -51,3 +51,11 @@ def test_rows_without_columns(program):
 
 def test_backward_does_not_read_eps(program):
     run(program, "eps_not_read")
+
+
+def test_row_cuts_of_the_backward_pass(program):
+    run(program, "row_cuts")
+
+
+def test_token_splits_of_the_weight_gradient(program):
+    run(program, "token_splits")

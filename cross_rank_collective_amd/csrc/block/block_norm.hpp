@@ -30,6 +30,29 @@
 namespace ptored {
 namespace block {
 
+// mean(v^2) over the workgroup's row.  The sum of the squares can pass binary32's
+// range where the mean does not (at 8192 columns from values of 2e17 on): then
+// each square is taken as (v / D) v, whose sum is the mean.  Not always, since
+// small values' quotients would lose digits.  Every thread has the same sum, so
+// the test is one of scalars.
+template <int S, int V>
+__device__ __forceinline__ float mean_square(const float (&v)[S][V], float own, float inv_cols,
+                                             f32x4 (*red)[1][kMaxWaves / 4], int& turn) {
+    float sum[1] = {own};
+    block_sum<1>(red[turn], sum);
+    turn ^= 1;
+    const uint32_t all = (uint32_t)__builtin_amdgcn_readfirstlane((int)as_u(sum[0]));
+    if (__builtin_expect(all != 0x7F800000u, 1)) return as_f(all) * inv_cols;
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[0] += v[s][i] * inv_cols * v[s][i];
+    block_sum<1>(red[turn], sum);
+    turn ^= 1;
+    return sum[0];
+}
+
 // S slots of a row per thread.  KEEP: at least one output in 8 bits.
 template <int DT, int S, int EDGE, bool KEEP>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
@@ -87,14 +110,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
             if (gated) g[s] = t.load(gate_row, s);
         }
         if (b.w1 != nullptr) {
-            float sum[1] = {0.0f};
+            float own = 0.0f;
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[0] += h[s][i] * h[s][i];
-            block_sum<1>(red[turn], sum);
-            turn ^= 1;
-            const float r1 = 1.0f / sqrtf(sum[0] * b.inv_cols + b.eps);
+                for (int i = 0; i < V; ++i) own += h[s][i] * h[s][i];
+            const float r1 = 1.0f / sqrtf(mean_square(h, own, b.inv_cols, red, turn) + b.eps);
             if (b.r1 != nullptr && threadIdx.x == 0) b.r1[row] = r1;
             branch *= r1;
         }
@@ -113,7 +134,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
             }
         }
         const auto& c = args_again<NormArgs>();
-        float x[S][V], sum[1] = {0.0f};
+        float x[S][V], own = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float p[V];
@@ -135,7 +156,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 x[s][i] = c.beta * x[s][i] + p[i];
-                sum[0] += x[s][i] * x[s][i];
+                own += x[s][i] * x[s][i];
             }
         }
         if (c.x_out.p) {
@@ -156,9 +177,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
         if (d.w2 == nullptr) continue;  // the same for every wave
 #pragma unroll
         for (int s = 0; s < S; ++s) w[s] = t.load_weight(d.w2, d.w_f32, s);
-        block_sum<1>(red[turn], sum);
-        turn ^= 1;
-        const float r2 = 1.0f / sqrtf(sum[0] * d.inv_cols + d.eps);
+        const float r2 = 1.0f / sqrtf(mean_square(x, own, d.inv_cols, red, turn) + d.eps);
         if (d.r2 != nullptr && threadIdx.x == 0) d.r2[row] = r2;
         if (d.z.p == nullptr && !(KEEP && d.kz.q)) continue;
         const rsrc_t z_row = t.row(d.z.p + row * d.z.ld);

@@ -9,7 +9,8 @@ import torch
 
 import cross_rank_collective_amd as crc
 from cross_rank_collective_amd import block as K
-from tests.test_block_gpu import draw, say
+from tests import block_reference as R
+from tests.test_block_gpu import EPS, TYPES, draw, make, norms, say
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,39 @@ def test_gate_rows_are_not_read_without_a_gate():
     for other in outs[1:]:
         for name, v in outs[0].items():
             assert torch.equal(v, other[name]), name
+
+
+# Sums of squares that pass binary32's range with a mean that does not, in both
+# norms; columns and rows of every kernel.
+LARGE = [("bf16", 5, 8192, False), ("bf16", 300, 4100, True), ("f32", 4, 7, True), ("f32", 300, 1003, False),
+         ("f32", 257, 16384, True), ("bf16", 3, 16383, False), ("f32", 3, 4096, True)]
+
+
+@pytest.mark.parametrize("dtype,rows,cols,keep", LARGE)
+def test_squares_whose_sum_passes_the_range_but_not_their_mean(dtype, rows, cols, keep):
+    say("large", dtype, rows, cols, keep)
+    ty = TYPES[dtype]
+    c, g = make(dtype, rows, cols, 2, True, 1, True, True, 17)
+    # magnitudes 0.5 to 1 times the scale, so that the mean square is known to hold
+    flat = lambda v: (v.double().sign() * (0.5 + 0.5 * torch.rand(v.shape)) + 0).to(v.dtype)  # noqa: E731
+    torch.manual_seed(4)
+    c["parts"] = [flat(v) for v in c["parts"]]
+    c["x"] = flat(c["x"])
+    c["parts"][0][0] *= 1.6e19  # the fold's row: mean square near 1e38
+    c["parts"][1][0] *= 1e10
+    c["x"][1] *= 1.6e19         # the stream's row
+    c["parts"][0][rows - 1] *= 3e17
+    c["x"][rows - 1] *= 3e17
+    g["parts"], g["x"] = [v.cuda() for v in c["parts"]], c["x"].cuda()
+    out = {n: torch.empty(rows, cols, dtype=ty, device="cuda") for n in ("x_out", "z", "h")}
+    vec = {n: torch.empty(rows, device="cuda") for n in ("post_rstd", "pre_rstd")}
+    kept = {n: crc.checkpoint_empty(rows, cols) for n in ("x_kept", "z_kept")} if keep else {}
+    crc.block_norm(g["parts"], g["x"], **out, **vec, **kept, eps=EPS, **norms(g))
+    want = R.forward(c["parts"], c["x"], c["w1"], c["gate"], c["w2"], eps=EPS, offset=0.0, alpha=1.0,
+                     beta=1.0)
+    assert float(want["r1"][0].min()) > 0 and float(want["r2"][0].min()) > 0
+    for name, key in (("h", "h"), ("post_rstd", "r1"), ("x_out", "x_out"), ("pre_rstd", "r2"), ("z", "z")):
+        R.close({**out, **vec}[name], *want[key], name)
+    for name, k in kept.items():
+        q, s = R.pack(out[{"x_kept": "x_out", "z_kept": "z"}[name]].cpu())
+        assert torch.equal(k.q.cpu(), q) and torch.equal(k.scales.cpu(), s), name

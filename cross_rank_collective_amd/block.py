@@ -362,14 +362,12 @@ def block_norm(parts, x, x_out=None, z=None, *, post_weight=None, gate=None, pre
     g = _Group(x, "x")
     ptrs, part_ld = [], g.cols
     for t in parts:
+        part = g.mat(t, "every part" if ptrs else "parts[0]")
         if not ptrs:
-            part_ld = g.mat(t, "parts[0]").ld
-            strides = t.stride()
-        elif (t.stride() != strides or t.shape != g.shape or t.dtype is not g.dtype
-              or t.get_device() != g.index):
-            g.mat(t, "every part")
+            part_ld = part.ld
+        elif part.ld != part_ld and g.rows > 1:  # a single row has no pitch
             raise ValueError("every part must have the same strides")
-        ptrs.append(t.data_ptr())
+        ptrs.append(part.data)
     params = g.params(post_weight, pre_weight, gate, eps, weight_offset, branch_scale,
                       residual_scale)
     io = ptored_block_io(g.mat(x, "x"), g.mat(x_out, "x_out"), g.mat(z, "z"), g.mat(h, "h"),

@@ -41,7 +41,9 @@ class Buffers {
               bool whole = true) {
         if (p == nullptr) return true;
         if (!pitch_ok(n, cols, ld)) return false;
-        add(p, n > 0 && cols > 0 ? ((n - 1) * ld + cols) * es : 0, ld * es, es, out, whole);
+        // a single row has no pitch of its own
+        add(p, n > 0 && cols > 0 ? ((n - 1) * ld + cols) * es : 0, (n > 1 ? ld : cols) * es, es, out,
+            whole);
         return true;
     }
     bool kept(const ptored_checkpoint& k, int64_t n, int64_t cols, bool out) {

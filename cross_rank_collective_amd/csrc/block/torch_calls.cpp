@@ -167,9 +167,10 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int64_t part_ld = g.cols;
         for (Py_ssize_t r = 0; r < nranks; ++r) {
             const ptored_rows y = g.mat(PySequence_Fast_GET_ITEM(a[0], r));
-            if (y.data == nullptr || (r > 0 && y.ld != part_ld)) throw Misfit{};
+            if (r == 0) part_ld = y.ld;
+            // the pitch of a single row is any
+            if (y.data == nullptr || (g.rows > 1 && y.ld != part_ld)) throw Misfit{};
             parts[r] = y.data;
-            part_ld = y.ld;
         }
         at::ScalarType weights;
         const ptored_block_params p = g.params(a + 4, weights);

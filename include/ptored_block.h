@@ -97,8 +97,8 @@ typedef struct ptored_block_io {
  *        0 <= nranks <= PTORED_MAX_RANKS.  With none, x' = beta x (the norm
  *        before the first block): post_weight, gate, h and h_kept must be
  *        absent.
- * An output may be exactly an input matrix of the same pitch; every other
- * overlap of an output is rejected.
+ * An output may be exactly an input matrix of the same pitch (of any pitch, if
+ * T is 1); every other overlap of an output is rejected.
  */
 int ptored_block_norm(const void* const* parts, int nranks, int64_t part_ld,
                       const ptored_block_params* params, const ptored_block_io* io,

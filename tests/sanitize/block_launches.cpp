@@ -206,6 +206,24 @@ int token_splits() {
     return 0;
 }
 
+// A single row has no pitch: an output is an input's row whatever their pitches.
+int one_row() {
+    for (int64_t rows : {int64_t(1), int64_t(2)}) {
+        const int want = rows == 1 ? PTORED_OK : PTORED_ERR_OVERLAP;
+        Call c(rows, 256, 0, PTORED_BF16);
+        c.io.dx = {c.io.dz.data, 512};
+        EXPECT(c.run() == want, "backward, %lld rows", (long long)rows);
+        ptored_block_io io{};
+        io.x = mat(4, 256);
+        io.x_out = mat(4, 1024);
+        io.z = mat(5, 256);
+        const void* parts[] = {fake(6), fake(5)};
+        const int st = ptored_block_norm(parts, 2, 512, &c.p, &io, nullptr);
+        EXPECT(st == want, "forward, %lld rows: %d", (long long)rows, st);
+    }
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -213,7 +231,7 @@ int main(int argc, char** argv) {
         const char* name;
         int (*check)();
     } checks[] = {{"no_gate", no_gate}, {"no_columns", no_columns}, {"eps_not_read", eps_not_read},
-                {"row_cuts", row_cuts}, {"token_splits", token_splits}};
+                {"row_cuts", row_cuts}, {"token_splits", token_splits}, {"one_row", one_row}};
     for (const auto& c : checks)
         if (argc == 2 && std::strcmp(argv[1], c.name) == 0) return c.check();
     std::printf("no such check\n");

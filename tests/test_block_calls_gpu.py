@@ -87,3 +87,26 @@ def test_squares_whose_sum_passes_the_range_but_not_their_mean(dtype, rows, cols
     for name, k in kept.items():
         q, s = R.pack(out[{"x_kept": "x_out", "z_kept": "z"}[name]].cpu())
         assert torch.equal(k.q.cpu(), q) and torch.equal(k.scales.cpu(), s), name
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_one_row_of_buffers_with_different_pitches(native, monkeypatch):
+    """A decoded token's partial outputs, each a row of a buffer of its own width."""
+    say("one row", native)
+    if not native:
+        monkeypatch.setattr(K, "_native_call", lambda *a: False)
+    cols = 520
+    c, g = make("bf16", 1, cols, 3, False, 0, True, True, 3)
+    wide = [torch.zeros(4, cols + 8 * r, dtype=torch.bfloat16, device="cuda") for r in range(3)]
+    parts = [w[r:r + 1, :cols] for r, w in enumerate(wide)]
+    for p, v in zip(parts, c["parts"]):
+        p.copy_(v)
+    assert len({p.stride(0) for p in parts}) == 3
+    x, z = torch.empty(1, 2 * cols, dtype=torch.bfloat16, device="cuda")[:, :cols], torch.empty(
+        1, cols, dtype=torch.bfloat16, device="cuda")
+    x.copy_(c["x"])
+    # x' over the same row seen with another pitch
+    crc.block_norm(parts, x, x.as_strided((1, cols), (cols, 1)), z, pre_weight=g["w2"], eps=EPS)
+    want = R.forward(c["parts"], c["x"], None, None, c["w2"], eps=EPS, offset=0.0, alpha=1.0, beta=1.0)
+    R.close(x, *want["x_out"], "x_out")
+    R.close(z, *want["z"], "z")

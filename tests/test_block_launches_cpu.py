@@ -59,3 +59,7 @@ def test_row_cuts_of_the_backward_pass(program):
 
 def test_token_splits_of_the_weight_gradient(program):
     run(program, "token_splits")
+
+
+def test_a_single_row_has_no_pitch(program):
+    run(program, "one_row")

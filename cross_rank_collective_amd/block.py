@@ -18,6 +18,12 @@ workspace of a backward pass (from torch's allocator, on the call's stream).
 Calls are asynchronous on ``stream`` (default: torch's current stream).  A
 caller that uses tensors on another stream than the one they were allocated on
 keeps them alive until that stream is done, as with every torch call.
+
+These are not differentiable functions of autograd: a call records nothing,
+whatever requires a gradient, and its gradients are calls of their own
+(``block_norm_backward``, ``checkpoint_wgrad``).  Outputs count as changed in
+place, so autograd refuses to use a tensor that it saved before such a call
+wrote it.
 """
 
 from __future__ import annotations
@@ -290,6 +296,15 @@ class _Group:
             B._raise_on(status)
 
 
+def _wrote(*outputs) -> None:
+    """Outputs of a call that was made: tensors, kept pairs or None."""
+    for t in outputs:
+        if _is_kept(t):
+            _wrote(*t)
+        elif t is not None:
+            _torch.autograd.graph.increment_version(t)
+
+
 def _native_call(name: str, stream, *args) -> bool:
     """The call on tensors that fit as they are, made natively: False where the
     code that follows has to look again (and make the call, or say what does
@@ -378,6 +393,7 @@ def block_norm(parts, x, x_out=None, z=None, *, post_weight=None, gate=None, pre
     if g.rows == 0 or g.cols == 0:
         return  # empty tensors have no storage
     g.run(stream, ptored_block_norm, ptrs, len(ptrs), part_ld, params, io)
+    _wrote(x_out, z, h, post_rstd, pre_rstd, h_kept, x_kept, z_kept)
 
 
 def block_norm_backward_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
@@ -444,6 +460,7 @@ def block_norm_backward(dz, dx_out, x_out, pre_rstd, dx=None, dh=None, *, h=None
         nbytes = block_norm_backward_workspace(g.rows, g.cols, dgate_rows)
     keep, io.workspace, io.workspace_bytes = _workspace(nbytes, workspace, g.index, stream)
     g.run(stream, ptored_block_norm_backward, params, io)
+    _wrote(dx, dh, dpost_weight, dgate, dpre_weight)
 
 
 def checkpoint_empty(rows: int, cols: int, device="cuda") -> Checkpoint:
@@ -467,6 +484,7 @@ def checkpoint_pack(x, kept, stream=None) -> None:
     xm, k = g.mat(x, "x"), g.kept(kept, "kept")
     if g.rows and g.cols:
         g.run(stream, ptored_checkpoint_pack, xm, g.rows, g.cols, g.code, k)
+        _wrote(kept)
 
 
 def checkpoint_unpack(kept, out, stream=None) -> None:
@@ -477,6 +495,7 @@ def checkpoint_unpack(kept, out, stream=None) -> None:
     om, k = g.mat(out, "out"), g.kept(kept, "kept")
     if g.rows and g.cols:
         g.run(stream, _unpack_into, om, k, g.rows, g.cols, g.code)
+        _wrote(out)
 
 
 def _unpack_into(om, k, rows, cols, code, stream):
@@ -518,3 +537,4 @@ def checkpoint_wgrad(dy, kept, dw, accumulate: bool = False, workspace=None, str
     keep, ptr, given = _workspace(nbytes, workspace, g.index, stream)
     g.run(stream, ptored_checkpoint_wgrad, dym, k, g.rows, outs, cols, g.code, dwm, code,
           1 if accumulate else 0, ptr, given)
+    _wrote(dw)

@@ -14,6 +14,8 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+
 #include "ptored_block.h"
 
 namespace {
@@ -151,6 +153,27 @@ struct Group {
     }
 };
 
+// Outputs (None, tensors or kept pairs) of a call that was made: as after torch's
+// own in-place operations, autograd then finds a tensor changed that it saved
+// before.
+int wrote(int status, std::initializer_list<PyObject*> outputs) {
+    if (status != PTORED_OK) return status;
+    auto changed = [](PyObject* o) {
+        const at::Tensor& t = tensor(o);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    };
+    for (PyObject* o : outputs) {
+        if (o == Py_None) continue;
+        if (PyTuple_Check(o)) {
+            changed(PyTuple_GET_ITEM(o, 0));
+            changed(PyTuple_GET_ITEM(o, 1));
+        } else {
+            changed(o);
+        }
+    }
+    return status;
+}
+
 void want(Py_ssize_t got, Py_ssize_t n) {
     if (got != n) throw Misfit{};
 }
@@ -184,7 +207,8 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         io.h_kept = g.kept(a[14], g.cols);
         io.x_kept = g.kept(a[15], g.cols);
         io.z_kept = g.kept(a[16], g.cols);
-        return ptored_block_norm(parts, (int)nranks, part_ld, &p, &io, g.stream(a[17]));
+        return wrote(ptored_block_norm(parts, (int)nranks, part_ld, &p, &io, g.stream(a[17])),
+                     {a[2], a[3], a[11], a[12], a[13], a[14], a[15], a[16]});
     });
 }
 
@@ -225,7 +249,8 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             io.workspace = ws.data_ptr();
             io.workspace_bytes = (int64_t)ws.nbytes();
         }
-        return ptored_block_norm_backward(&p, &io, g.stream(a[19]));
+        return wrote(ptored_block_norm_backward(&p, &io, g.stream(a[19])),
+                     {a[4], a[5], a[15], a[16], a[17]});
     });
 }
 
@@ -235,8 +260,9 @@ PyObject* checkpoint_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
         want(n, 3);
         const Group g(tensor(a[0]));
         if (a[1] == Py_None) throw Misfit{};
-        return ptored_checkpoint_pack(g.mat(a[0]), g.rows, g.cols, g.code, g.kept(a[1], g.cols),
-                                      g.stream(a[2]));
+        return wrote(ptored_checkpoint_pack(g.mat(a[0]), g.rows, g.cols, g.code,
+                                            g.kept(a[1], g.cols), g.stream(a[2])),
+                     {a[1]});
     });
 }
 
@@ -246,8 +272,9 @@ PyObject* checkpoint_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
         want(n, 3);
         const Group g(tensor(a[1]));
         if (a[0] == Py_None) throw Misfit{};
-        return ptored_checkpoint_unpack(g.kept(a[0], g.cols), g.rows, g.cols, g.code, g.mat(a[1]),
-                                        g.stream(a[2]));
+        return wrote(ptored_checkpoint_unpack(g.kept(a[0], g.cols), g.rows, g.cols, g.code,
+                                              g.mat(a[1]), g.stream(a[2])),
+                     {a[1]});
     });
 }
 
@@ -270,9 +297,11 @@ PyObject* checkpoint_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const ptored_rows out = g.rows_of(dw, g.cols, cols, dw.scalar_type());
         const ptored_checkpoint x = g.kept(a[1], cols);
         const at::Tensor ws = g.workspace(a[4], a[5], bytes);
-        return ptored_checkpoint_wgrad(g.mat(a[0]), x, g.rows, g.cols, cols, g.code, out, code,
-                                       accumulate, ws.defined() ? ws.data_ptr() : nullptr,
-                                       ws.defined() ? (int64_t)ws.nbytes() : 0, g.stream(a[5]));
+        return wrote(ptored_checkpoint_wgrad(g.mat(a[0]), x, g.rows, g.cols, cols, g.code, out, code,
+                                             accumulate, ws.defined() ? ws.data_ptr() : nullptr,
+                                             ws.defined() ? (int64_t)ws.nbytes() : 0,
+                                             g.stream(a[5])),
+                     {a[2]});
     });
 }
 

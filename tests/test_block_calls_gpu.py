@@ -110,3 +110,43 @@ def test_one_row_of_buffers_with_different_pitches(native, monkeypatch):
     want = R.forward(c["parts"], c["x"], None, None, c["w2"], eps=EPS, offset=0.0, alpha=1.0, beta=1.0)
     R.close(x, *want["x_out"], "x_out")
     R.close(z, *want["z"], "z")
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_outputs_count_as_changed_in_place(native, monkeypatch):
+    """Every output's version moves on and no input's; a tensor that autograd
+    saved before a call wrote it is refused by the backward pass."""
+    say("versions", native)
+    if not native:
+        monkeypatch.setattr(K, "_native_call", lambda *a: False)
+    t, d, o = 6, 40, 16
+    rand = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    ins = {n: rand(t, d) for n in ("y", "x", "dz", "dxo")} | {
+        "w1": rand(d), "w2": rand(d), "gate": rand(2, d), "dy": rand(t, o)}
+    outs = {n: rand(t, d) for n in ("xo", "z", "h", "dx", "dh", "back")} | {
+        "r1": rand(t), "r2": rand(t), "dw1": rand(d), "dw2": rand(d), "dg": rand(2, d), "dw": rand(o, d)}
+    kept = {n: crc.checkpoint_empty(t, d) for n in "hxzp"}
+    flat = lambda: list(ins.values()), lambda: [*outs.values(), *(v for k in kept.values() for v in k)]
+    before = [[v._version for v in f()] for f in flat]
+    n = {"post_weight": ins["w1"], "gate": ins["gate"], "pre_weight": ins["w2"]}
+    crc.block_norm([ins["y"]], ins["x"], outs["xo"], outs["z"], h=outs["h"], post_rstd=outs["r1"],
+                   pre_rstd=outs["r2"], h_kept=kept["h"], x_kept=kept["x"], z_kept=kept["z"], **n)
+    crc.block_norm_backward(ins["dz"], ins["dxo"], kept["x"], outs["r2"], outs["dx"], outs["dh"],
+                            h=kept["h"], post_rstd=outs["r1"], dpost_weight=outs["dw1"],
+                            dgate=outs["dg"], dpre_weight=outs["dw2"], **n)
+    crc.checkpoint_pack(ins["x"], kept["p"])
+    crc.checkpoint_unpack(kept["p"], outs["back"])
+    crc.checkpoint_wgrad(ins["dy"], kept["z"], outs["dw"])
+    after = [[v._version for v in f()] for f in flat]
+    assert after[0] == before[0]
+    assert after[1] == [v + 1 for v in before[1]]
+
+    proj = rand(d, o).requires_grad_()
+    loss = (outs["z"] @ proj).sum()  # saves z
+    crc.block_norm([ins["y"]], ins["x"], z=outs["z"], pre_weight=ins["w2"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        z = rand(t, d)
+        crc.block_norm([ins["y"]], ins["x"], z=z, pre_weight=ins["w2"])
+    crc.block_norm([ins["y"]], ins["x"], z=z, pre_weight=ins["w2"])  # its tensors have no versions

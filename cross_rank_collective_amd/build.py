@@ -107,7 +107,8 @@ def _link_ext(obj: str) -> None:
 
 def build(jobs: int = 0) -> str:
     """Compile every HIP unit for gfx950 and link libptored.so and the tensor
-    calls; returns the library's path.
+    calls; returns the library's path.  Where the tensor calls cannot be built
+    (no g++, no torch headers) the library still is, before the error is raised.
     ``jobs`` = parallel compilers (0: one per CPU, at most 16)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     if jobs <= 0:
@@ -115,14 +116,14 @@ def build(jobs: int = 0) -> str:
     with ThreadPoolExecutor(max(1, min(jobs, len(UNITS) + 1))) as ex:
         ext = ex.submit(_compile_ext)
         objs = list(ex.map(_compile, UNITS))
-        ext_obj = ext.result()
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB)
-    _link_ext(ext_obj)
+        tmp = LIB + ".tmp"
+        cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB)
+        # only now: the library needs neither torch's headers nor g++
+        _link_ext(ext.result())
     return LIB
 
 

@@ -10,7 +10,8 @@ import torch
 import cross_rank_collective_amd as crc
 from cross_rank_collective_amd import block as K
 from tests import block_reference as R
-from tests.test_block_gpu import EPS, TYPES, draw, make, norms, say
+from tests.test_block_gpu import (EPS, TYPES, Room, check_rest, draw, grad_case, make, norms,
+                                  run_backward, say)
 
 pytestmark = pytest.mark.gpu
 
@@ -150,3 +151,145 @@ def test_outputs_count_as_changed_in_place(native, monkeypatch):
         z = rand(t, d)
         crc.block_norm([ins["y"]], ins["x"], z=z, pre_weight=ins["w2"])
     crc.block_norm([ins["y"]], ins["x"], z=z, pre_weight=ins["w2"])  # its tensors have no versions
+
+
+# As in test_block_gpu.BACKWARD, activations whole: rows of several waves, several
+# rows a workgroup, ends inside a slot, with and without the norms.
+IN_PLACE = [
+    ("bf16", 601, 4099, True, 601, True, False, False, 1, 1, 1.0, True),
+    ("bf16", 521, 8192, True, 0, True, False, False, 0, 0, 0.0, True),
+    ("bf16", 280, 9000, False, 1, True, True, False, 0, 0, 0.0, True),
+    ("bf16", 1540, 4104, True, 220, True, True, False, 0, 0, 0.0, True),
+    ("f32", 300, 8196, True, 1, True, True, False, 0, 0, 0.0, False),
+    ("f32", 1400, 1003, True, 20, True, True, False, 0, 1, 0.0, True),
+    ("f32", 300, 12001, True, 0, False, True, False, 1, 0, 0.0, True),
+    ("f16", 6600, 39, False, 600, True, False, False, 0, 0, 1.0, True),
+    ("f16", 3000, 3, True, 3, True, True, False, 1, 1, 0.0, True),
+    ("f16", 900, 1025, False, 4, False, True, False, 0, 0, 0.0, True),
+]
+
+
+@pytest.mark.parametrize("case", IN_PLACE, ids=lambda c: "-".join(map(str, c)))
+def test_gradients_over_the_activations(case):
+    say("in place", *case)
+    _, g, acts, ins, vec = grad_case(case)
+    full = run_backward(case, g, acts, ins, vec)
+    have = [n for n, v in (("x_out", acts["x_out"]), ("h", acts["h"]), ("dz", ins["dz"]),
+                           ("dxo", ins["dxo"])) if v is not None]
+    for dx, dh in [(have[0], have[1]), (have[1], have[0]), (have[-1], have[0])]:
+        _, g, acts, ins, vec = grad_case(case)
+        bufs = {**acts, **ins}
+        out = run_backward(case, g, acts, ins, vec, dx=bufs[dx], dh=bufs[dh])
+        assert torch.equal(bufs[dx], full["dx"].t), (dx, dh)
+        assert torch.equal(bufs[dh], full["dh"].t), (dx, dh)
+        for name in ("dw1", "dw2", "dgate"):
+            if name in out:
+                assert torch.equal(out[name].t, full[name].t), (name, dx, dh)
+
+
+def far(rows, cols, dtype, value=None):
+    """Rows further apart than 2^31 bytes: the third one's offset passes 2^32."""
+    pitch = (1 << 31) // torch.empty(0, dtype=dtype).element_size() + 8
+    buf = torch.empty((rows - 1) * pitch + cols, dtype=dtype, device="cuda")
+    t = buf.as_strided((rows, cols), (pitch, 1))
+    if value is not None:
+        t.copy_(value)
+    return t
+
+
+@pytest.mark.parametrize("packed,groups", [(False, 3), (True, 1)])
+def test_gradients_of_rows_past_32_bits(packed, groups):
+    """All matrices far apart, the packed ones and the gate among them."""
+    say("far gradients", packed, groups)
+    rows, cols = 3, 4100
+    case = ("bf16", rows, cols, True, groups, True, True, packed, 0, 0, 0.0, True)
+    _, g, acts, ins, vec = grad_case(case)
+    near = run_backward(case, g, acts, ins, vec)
+    move = lambda v: far(*v.shape, v.dtype, v)  # noqa: E731
+    acts = {n: tuple(move(t) for t in v) if packed else move(v) for n, v in acts.items()}
+    ins = {n: move(v) for n, v in ins.items()}
+    g["gate"] = move(g["gate"])
+    dx, dh = (far(rows, cols, torch.bfloat16) for _ in range(2))
+    dgate = far(groups, cols, torch.bfloat16)
+    out = run_backward(case, g, acts, ins, vec, dx=dx, dh=dh, dgate=dgate)
+    for name, v in (("dx", dx), ("dh", dh), ("dgate", dgate), ("dw1", out["dw1"].t), ("dw2", out["dw2"].t)):
+        assert torch.equal(v, near[name].t), name
+    del acts, ins, dx, dh, dgate, g
+    torch.cuda.empty_cache()
+
+
+def test_forward_and_weight_gradient_of_rows_past_32_bits():
+    """Partials, stream, gate and every output of the forward pass; the packed
+    input and the weight gradient."""
+    say("far forward")
+    rows, cols, outs = 3, 2052, 8
+    c, g = make("bf16", rows, cols, 2, True, 3, True, True, 13)
+    like = lambda n, d: torch.empty(rows, n, dtype=d, device="cuda")  # noqa: E731
+    nb = (cols + 31) // 32
+    out = {n: like(cols, torch.bfloat16) for n in ("x_out", "z", "h")}
+    kept = {n: (like(cols, torch.int8), like(nb, torch.uint8)) for n in ("x_kept", "z_kept", "h_kept")}
+    crc.block_norm(g["parts"], g["x"], **out, **kept, **norms(g))
+    dy = draw(torch.Generator().manual_seed(1), rows, outs).bfloat16().cuda()
+    dw = torch.empty(outs, cols, device="cuda")
+    crc.checkpoint_wgrad(dy, kept["z_kept"], dw)
+
+    moved = {n: far(rows, cols, torch.bfloat16) for n in out}
+    packs = {n: (far(rows, cols, torch.int8), far(rows, nb, torch.uint8)) for n in kept}
+    parts = [far(rows, cols, torch.bfloat16, v) for v in g["parts"]]
+    n = {**norms(g), "gate": far(3, cols, torch.bfloat16, g["gate"])}
+    crc.block_norm(parts, far(rows, cols, torch.bfloat16, g["x"]), **moved, **packs, **n)
+    for name, v in out.items():
+        assert torch.equal(moved[name], v), name
+    for name, pair in kept.items():
+        for a, b in zip(packs[name], pair):
+            assert torch.equal(a, b), name
+    del moved, parts, n
+    torch.cuda.empty_cache()
+    wide = far(outs, cols, torch.float32)
+    crc.checkpoint_wgrad(dy, packs["z_kept"], wide)
+    assert torch.equal(wide, dw)
+    del wide, packs
+    torch.cuda.empty_cache()
+
+
+# f16, where a workgroup that meets a block of x outside f16's exponents starts
+# again: tiles of 256 x 256 and of 128 x 128, tokens split, rows shorter than a chunk.
+RESTART = [(200, 2997, 4008), (200, 2048, 4096), (300, 136, 160), (4096, 130, 131), (129, 200, 15),
+           (700, 3, 300), (2001, 7, 9)]
+
+
+@pytest.mark.parametrize("rows,outs,cols", RESTART)
+def test_wgrad_of_f16_starts_again(rows, outs, cols):
+    gen = torch.Generator().manual_seed(38)
+    dy = torch.randn(rows, outs, generator=gen).half()
+    x = torch.randn(rows, cols, generator=gen)
+    spots = {"first": (0, 0), "middle": (rows // 2, cols // 2), "last": (rows - 1, cols - 1)}
+    for name, (t, i) in spots.items():
+        for scale in (2.0 ** 40, 2.0 ** -60, float("nan")):
+            say("f16 restart", rows, outs, cols, name, scale)
+            v = x.clone()
+            block = slice(i // 32 * 32, i // 32 * 32 + 32)
+            v[t, block] *= scale
+            q, s = R.pack(v)
+            want, bound = R.wgrad(dy, q, s)
+            dw = Room(outs, cols, torch.float32, 1, 1)
+            crc.checkpoint_wgrad(dy.cuda(), (q.cuda(), s.cuda()), dw.t)
+            R.close(dw.t, want, bound, f"{name} {scale}")
+            check_rest({"dw": dw})
+
+
+@pytest.mark.parametrize("rows,outs,cols", [(300, 136, 160), (33, 5, 40), (2500, 300, 520)])
+def test_wgrad_of_f32s_smallest_values(rows, outs, cols):
+    """dy below 2^-110 enters as a multiple of 2^-133 (of bfloat16's smallest
+    step), off by less than one; the products' sums are binary32's, whose
+    smallest step is 2^-149."""
+    for low, high in ((2.0 ** -119, 2.0 ** 3), (2.0 ** -130, 2.0 ** 70), (2.0 ** -140, 2.0 ** 100)):
+        say("f32 smallest", rows, outs, cols, low)
+        gen = torch.Generator().manual_seed(48)
+        dy = (draw(gen, rows, outs) * low).float()
+        q, s = R.pack((draw(gen, rows, cols) * high).float())
+        want, bound = R.wgrad(dy, q, s)
+        bound = bound + 2.0 ** -133 * R.unpack(q, s).abs().sum(0) + rows * 2.0 ** -149
+        dw = torch.empty(outs, cols, device="cuda")
+        crc.checkpoint_wgrad(dy.cuda(), (q.cuda(), s.cuda()), dw)
+        R.close(dw, want, bound, f"dy of {low}")

@@ -5,10 +5,11 @@
 // A matrix product over the tokens, both operands with the sum's index as the
 // slow one.  The values kept are exact in bfloat16, so x enters the matrix
 // instructions without loss; so does dy, as one bfloat16 (bf16) or the exact
-// sum of three (f32): products are exact and sums in binary32.  For f16, dy is
-// used as it is and x in f16, which holds a block exactly if its exponent is
-// in [-18, 15]; a workgroup that meets another block (or a NaN) starts again
-// with dy as the exact sum of two bfloat16.
+// sum of three (f32, but for what lies below bfloat16's smallest step, 2^-133):
+// products are exact and sums in binary32.  For f16, dy is used as it is and x
+// in f16, which holds a block exactly if its exponent is in [-18, 15]; a
+// workgroup that meets another block (or a NaN) starts again with dy as the
+// exact sum of two bfloat16.
 //
 // A workgroup computes a tile of dw.  Each step stages kStep tokens of both
 // operands in the LDS as bfloat16, token-major as they come from memory, and

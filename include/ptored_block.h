@@ -31,8 +31,10 @@
  * nothing, can be captured in a graph, and checks its arguments before any
  * HIP call in the order INVALID_ARG (counts, null pointers, shapes),
  * UNSUPPORTED (types, i32 among them, or more than PTORED_BLOCK_MAX_COLS
- * columns), INVALID_ARG (alignment), OVERLAP.  Zero rows or columns are no
- * error.  Results do not vary from run to run.
+ * columns), INVALID_ARG (the workspace, alignment), OVERLAP.  Buffers overlap
+ * where their spans do, from the first byte to the last with the gaps between
+ * rows: two column ranges of one matrix do.  Zero rows or columns are no error.
+ * Results do not vary from run to run.
  */
 #ifndef PTORED_BLOCK_H
 #define PTORED_BLOCK_H
@@ -152,9 +154,10 @@ int ptored_checkpoint_unpack(ptored_checkpoint kept, int64_t rows, int64_t cols,
 /*
  * ptored_checkpoint_wgrad -- a projection's weight gradient from its packed
  * input: dw[o, i] = sum_t dy[t, o] x[t, i] (+ dw[o, i] with accumulate),
- * products exact and sums in binary32, rounded once to dw_dtype.  dy is
- * rows x outs of `dtype`; x is rows x cols; dw is outs x cols of dw_dtype, F32
- * or `dtype`.  Zero rows give zeros (or leave dw, with accumulate).
+ * products exact and sums in binary32, rounded once to dw_dtype (of F32, a dy
+ * below 2^-110 is cut to a multiple of 2^-133 first).  dy is rows x outs of
+ * `dtype`; x is rows x cols; dw is outs x cols of dw_dtype, F32 or `dtype`.  Zero
+ * rows give zeros (or leave dw, with accumulate).
  */
 int ptored_checkpoint_wgrad(ptored_rows dy, ptored_checkpoint x, int64_t rows, int64_t outs,
                             int64_t cols, int dtype, ptored_rows dw, int dw_dtype,

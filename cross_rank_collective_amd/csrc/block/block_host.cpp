@@ -124,10 +124,11 @@ int status_of(int rc) { return rc == kOk ? PTORED_OK : PTORED_ERR_HIP; }
 // ones run alone and the partial rows that chunks leave (8 bytes a column,
 // written and read) grow.  A wave is 64 slots wide; its registers leave room
 // for 16 waves of 8-element slots on a compute unit and for 20 of 4.  But with
-// work for all compute units a chunk has 5 rows at least: with fewer the partial
-// rows weigh as much as the rows' own data (both kernels, bf16, packed: 4096 x
-// 1024 28 us without the rule, 24 with 3 rows, 21 with 5, 22 with 7; 1511 x 2520
-// 27, 23, 23, 22; 512 x 4096 22, 17 with 2 rows).
+// work for all compute units the rows are not cut below chunks of 5: with fewer
+// the partial rows weigh as much as the rows' own data (both kernels, bf16,
+// packed: 4096 x 1024 28 us without the rule, 24 with 3 rows, 21 with 5, 22 with
+// 7; 1511 x 2520 27, 23, 23, 22; 512 x 4096 22, 17 with 2 rows).  Where a gate
+// row is a little longer than that, its equal parts are shorter (6 rows: 3 and 3).
 GradSplit grad_split(int64_t rows, int64_t cols, int64_t gate_rows, int dtype,
                      bool in_order = false) {
     GradSplit s{};
@@ -177,10 +178,11 @@ struct WgradShape {
 // again by a second kernel: 4 us and the bytes at 2.6 TB/s.  So with few
 // tiles the best number of splits is near sqrt(walk / time of one dw), as
 // long as the tiles of all splits still run at once.
-// Measured, us, best splits of 128 x 128 tiles against 256 x 256: 1024 tokens
-// x 2048 x 2048 20 / 39, 4096 x 2048 x 2048 49 / 59, 16384 x 4096 x 512 94 /
-// 88, 8192 x 4096 x 4096 410 / 250; 32768 x 640 x 512 with 1, 6, 12 and 25
-// splits 267, 60, 41 and 49.
+// Measured, us, best splits of 128 x 128 tiles against 256 x 256, bf16: 1024
+// tokens x 2048 x 2048 19 / 39, 4096 x 2048 x 2048 48 / 57, 16384 x 4096 x 512 91
+// / 83, 8192 x 4096 x 4096 343 / 244; f16: 20 / 43, 50 / 62, 96 / 90, 369 / 280
+// (its kernel of 256 x 256 spills registers and still wins where tiles are many).
+// 32768 x 640 x 512 with 1, 6, 12 and 25 splits 267, 60, 41 and 49.
 struct WgradCost {
     int shape;
     int64_t tm, tn;

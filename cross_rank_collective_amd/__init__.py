@@ -5,7 +5,9 @@ over a valid rectangle of N equally shaped buffers; ``binding`` exposes its
 C ABI to Python and ``workloads`` draws seeded synthetic inputs.  ``block``
 holds what follows the reduction in a tensor-parallel model: the block
 boundary's norms, gate and residual with their gradients, and activations
-kept in 8 bits.
+kept in 8 bits.  ``step`` holds what runs next to it in a training or serving
+step: the boundary with layer norm, the gated feed-forward block and the
+clipping of gradients by their global norm.
 """
 
 from .binding import (  # noqa: F401
@@ -47,4 +49,25 @@ from .block import (  # noqa: F401
     ptored_checkpoint_unpack,
     ptored_checkpoint_wgrad,
     ptored_checkpoint_wgrad_workspace,
+)
+from .step import (  # noqa: F401
+    gated_ffn,
+    gated_ffn_backward,
+    gated_ffn_backward_workspace,
+    grad_clip,
+    grad_norm,
+    grad_scale,
+    layer_norm,
+    layer_norm_backward,
+    layer_norm_backward_workspace,
+    ptored_gated_ffn,
+    ptored_gated_ffn_backward,
+    ptored_gated_ffn_backward_workspace,
+    ptored_grad_clip,
+    ptored_grad_norm,
+    ptored_grad_norm_workspace,
+    ptored_grad_scale,
+    ptored_layer_norm,
+    ptored_layer_norm_backward,
+    ptored_layer_norm_backward_workspace,
 )

@@ -5,7 +5,7 @@ linked into ``cross_rank_collective_amd/libptored.so``: the host code, one
 unit per element type (copy and push-with-add kernels) and ``treduce_op.hip``
 once per (element type, operator) pair (reduction and ring kernels); and from
 csrc/block/ the block-boundary operators' kernels, once per floating type,
-with their host code.  Next to it, ``_torch_calls.so``: the block-boundary
+with their host code, and from csrc/step/ the step's.  Next to it, ``_torch_calls.so``: the block-boundary
 calls on torch tensors as an extension module (host code, g++).  Run as
 ``python -m cross_rank_collective_amd.build`` or through
 ``__graft_entry__.build()``.
@@ -41,6 +41,11 @@ UNITS += [("block/block_ops.hip", f"block_ops_{dt.lower()}",
            (f"-DPTORED_INST_DT=PTORED_{dt}", f"-DPTORED_INST_NAME={dt.lower()}"))
           for dt in ("BF16", "F16", "F32")]
 UNITS += [("block/block_host.cpp", "block_host", ())]
+# The step's operators likewise, and the kernels over lists of gradients.
+UNITS = [("step/step_ops.hip", f"step_ops_{dt.lower()}",
+          (f"-DPTORED_INST_DT=PTORED_{dt}", f"-DPTORED_INST_NAME={dt.lower()}"))
+         for dt in ("BF16", "F16", "F32")] + UNITS
+UNITS += [("step/step_host.cpp", "step_host", ()), ("step/grad_clip.hip", "grad_clip", ())]
 
 ARCH = "gfx950"
 CFLAGS = [

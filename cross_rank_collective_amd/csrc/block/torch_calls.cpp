@@ -1,12 +1,13 @@
-// torch_calls.cpp -- the tensor-level block-boundary calls, natively.
+// torch_calls.cpp -- the tensor-level calls of the block boundary and of the
+// step's operators, natively.
 //
 // The kernels of a single token take 4 us and less; reading a dozen tensors'
 // shapes, strides and pointers from Python and marshalling them takes 10.
 // This extension module reads them from the tensors themselves.  It takes only
 // calls whose tensors all fit as they are (types, shapes, devices, plain
 // strides, torch's current stream or a handle) and returns the library's
-// status; for anything else it returns None, and the Python code in block.py
-// looks again, makes the call or raises the error.
+// status; for anything else it returns None, and the Python code in block.py or
+// step.py looks again, makes the call or raises the error.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -15,8 +16,9 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
+#include <vector>
 
-#include "ptored_block.h"
+#include "ptored_step.h"
 
 namespace {
 
@@ -85,6 +87,26 @@ struct Group {
     ptored_rows mat(PyObject* o) const {
         if (o == Py_None) return {nullptr, 0};
         return rows_of(tensor(o), rows, cols, type);
+    }
+    // A matrix of the group's type and another shape, or None.
+    ptored_rows of(PyObject* o, int64_t r, int64_t c) const {
+        if (o == Py_None) return {nullptr, 0};
+        return rows_of(tensor(o), r, c, type);
+    }
+    // The ranks' partial outputs; returns how many.
+    int parts(PyObject* list, const void** to, int64_t& part_ld) const {
+        if (!PyList_Check(list) && !PyTuple_Check(list)) throw Misfit{};
+        const Py_ssize_t nranks = PySequence_Fast_GET_SIZE(list);
+        if (nranks > PTORED_MAX_RANKS) throw Misfit{};
+        part_ld = cols;
+        for (Py_ssize_t r = 0; r < nranks; ++r) {
+            const ptored_rows y = mat(PySequence_Fast_GET_ITEM(list, r));
+            if (r == 0) part_ld = y.ld;
+            // the pitch of a single row is any
+            if (y.data == nullptr || (rows > 1 && y.ld != part_ld)) throw Misfit{};
+            to[r] = y.data;
+        }
+        return (int)nranks;
     }
     void* vec(PyObject* o, int64_t n, at::ScalarType ty) const {
         if (o == Py_None) return nullptr;
@@ -183,18 +205,9 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
         want(n, 18);
         const Group g(tensor(a[1]));
-        if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) throw Misfit{};
-        const Py_ssize_t nranks = PySequence_Fast_GET_SIZE(a[0]);
-        if (nranks > PTORED_MAX_RANKS) throw Misfit{};
         const void* parts[PTORED_MAX_RANKS];
-        int64_t part_ld = g.cols;
-        for (Py_ssize_t r = 0; r < nranks; ++r) {
-            const ptored_rows y = g.mat(PySequence_Fast_GET_ITEM(a[0], r));
-            if (r == 0) part_ld = y.ld;
-            // the pitch of a single row is any
-            if (y.data == nullptr || (g.rows > 1 && y.ld != part_ld)) throw Misfit{};
-            parts[r] = y.data;
-        }
+        int64_t part_ld;
+        const int nranks = g.parts(a[0], parts, part_ld);
         at::ScalarType weights;
         const ptored_block_params p = g.params(a + 4, weights);
         ptored_block_io io{};
@@ -207,7 +220,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         io.h_kept = g.kept(a[14], g.cols);
         io.x_kept = g.kept(a[15], g.cols);
         io.z_kept = g.kept(a[16], g.cols);
-        return wrote(ptored_block_norm(parts, (int)nranks, part_ld, &p, &io, g.stream(a[17])),
+        return wrote(ptored_block_norm(parts, nranks, part_ld, &p, &io, g.stream(a[17])),
                      {a[2], a[3], a[11], a[12], a[13], a[14], a[15], a[16]});
     });
 }
@@ -305,10 +318,261 @@ PyObject* checkpoint_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// The type that weights (None among them) share; float32 without any.
+at::ScalarType weight_type(const Group& g, std::initializer_list<PyObject*> weights) {
+    for (PyObject* o : weights) {
+        if (o == Py_None) continue;
+        const at::ScalarType t = tensor(o).scalar_type();
+        if (t != g.type && t != at::kFloat) throw Misfit{};
+        return t;
+    }
+    return at::kFloat;
+}
+
+// parts, x, x_out, z, weight, bias, eps, mean, rstd, stream
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 10);
+        const Group g(tensor(a[1]));
+        const void* parts[PTORED_MAX_RANKS];
+        int64_t part_ld;
+        const int nranks = g.parts(a[0], parts, part_ld);
+        const at::ScalarType weights = weight_type(g, {a[4], a[5]});
+        ptored_layer_norm_params p{};
+        p.rows = g.rows;
+        p.cols = g.cols;
+        p.weight = g.vec(a[4], g.cols, weights);
+        p.bias = g.vec(a[5], g.cols, weights);
+        p.eps = number(a[6]);
+        p.dtype = g.code;
+        p.weight_dtype = code_of(weights);
+        return wrote(ptored_layer_norm(parts, nranks, part_ld, &p, g.mat(a[1]), g.mat(a[2]),
+                                       g.mat(a[3]),
+                                       static_cast<float*>(g.vec(a[7], g.rows, at::kFloat)),
+                                       static_cast<float*>(g.vec(a[8], g.rows, at::kFloat)),
+                                       g.stream(a[9])),
+                     {a[2], a[3], a[7], a[8]});
+    });
+}
+
+// dz, dx_out, x_out, mean, rstd, dx, weight, dweight, dbias, workspace, stream
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 11);
+        const Group g(tensor(a[0]));
+        if (a[2] == Py_None || a[3] == Py_None || a[4] == Py_None) throw Misfit{};
+        const at::ScalarType weights = weight_type(g, {a[6], a[7], a[8]});
+        ptored_layer_norm_params p{};
+        p.rows = g.rows;
+        p.cols = g.cols;
+        p.weight = g.vec(a[6], g.cols, weights);
+        p.dtype = g.code;
+        p.weight_dtype = code_of(weights);
+        void* const dw = g.vec(a[7], g.cols, weights);
+        void* const db = g.vec(a[8], g.cols, weights);
+        int64_t bytes = 0;
+        if ((dw || db) && ptored_layer_norm_backward_workspace(g.rows, g.cols, &bytes) != PTORED_OK)
+            throw Misfit{};
+        const ptored_rows dz = g.mat(a[0]), dxo = g.mat(a[1]), x = g.mat(a[2]), dx = g.mat(a[5]);
+        const void* const mean = g.vec(a[3], g.rows, at::kFloat);
+        const void* const rstd = g.vec(a[4], g.rows, at::kFloat);
+        const at::Tensor ws = g.workspace(a[9], a[10], bytes);
+        return wrote(ptored_layer_norm_backward(
+                         &p, dz, dxo, x, static_cast<const float*>(mean),
+                         static_cast<const float*>(rstd), dx, dw, db,
+                         ws.defined() ? ws.data_ptr() : nullptr,
+                         ws.defined() ? (int64_t)ws.nbytes() : 0, g.stream(a[10])),
+                     {a[5], a[7], a[8]});
+    });
+}
+
+int whole(PyObject* o) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Misfit{};
+    return (int)v;
+}
+
+// x, w_gate, w_up, y, activation, gate, up, stream
+PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 8);
+        const Group g(tensor(a[0]));
+        const at::Tensor& y = tensor(a[3]);
+        if (y.dim() != 2 || y.size(1) == 0) throw Misfit{};
+        const int64_t wide = y.size(1);
+        const ptored_ffn_params p{g.rows, g.cols, wide, g.code, whole(a[4])};
+        return wrote(ptored_gated_ffn(&p, g.mat(a[0]), g.of(a[1], wide, g.cols), g.of(a[2], wide, g.cols),
+                                      g.of(a[3], g.rows, wide), g.of(a[5], g.rows, wide),
+                                      g.of(a[6], g.rows, wide), g.stream(a[7])),
+                     {a[3], a[5], a[6]});
+    });
+}
+
+// dy, gate, up, dgate, dup, activation, x, w_gate, w_up, dx, dw_gate, dw_up, accumulate, workspace,
+// stream
+PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 15);
+        const Group g(tensor(a[0]));
+        for (int i = 1; i <= 4; ++i)
+            if (a[i] == Py_None) throw Misfit{};
+        const int64_t wide = g.cols;
+        int64_t cols = 0;
+        for (const int i : {6, 9, 7, 8}) {
+            if (a[i] == Py_None) continue;
+            const at::Tensor& t = tensor(a[i]);
+            if (t.dim() != 2 || t.size(1) == 0) throw Misfit{};
+            cols = t.size(1);
+            break;
+        }
+        const ptored_ffn_params p{g.rows, cols, wide, g.code, whole(a[5])};
+        ptored_ffn_grad_io io{};
+        io.dy = g.mat(a[0]);
+        io.gate = g.mat(a[1]);
+        io.up = g.mat(a[2]);
+        io.dgate = g.mat(a[3]);
+        io.dup = g.mat(a[4]);
+        io.x = g.of(a[6], g.rows, cols);
+        io.w_gate = g.of(a[7], wide, cols);
+        io.w_up = g.of(a[8], wide, cols);
+        io.dx = g.of(a[9], g.rows, cols);
+        at::ScalarType weights = g.type;
+        if (a[10] != Py_None || a[11] != Py_None)
+            weights = tensor(a[a[10] != Py_None ? 10 : 11]).scalar_type();
+        if (weights != g.type && weights != at::kFloat) throw Misfit{};
+        if (a[10] != Py_None) io.dw_gate = g.rows_of(tensor(a[10]), wide, cols, weights);
+        if (a[11] != Py_None) io.dw_up = g.rows_of(tensor(a[11]), wide, cols, weights);
+        if ((io.dx.data && !(io.w_gate.data && io.w_up.data)) ||
+            ((io.dw_gate.data || io.dw_up.data) && !io.x.data))
+            throw Misfit{};
+        io.dw_dtype = code_of(weights);
+        io.accumulate = PyObject_IsTrue(a[12]);
+        if (io.accumulate < 0) throw Misfit{};
+        int64_t bytes = 0;
+        if ((io.dx.data || io.dw_gate.data || io.dw_up.data) &&
+            ptored_gated_ffn_backward_workspace(g.rows, cols, wide, g.code, &bytes) != PTORED_OK)
+            throw Misfit{};
+        const at::Tensor ws = g.workspace(a[13], a[14], bytes);
+        if (ws.defined()) {
+            io.workspace = ws.data_ptr();
+            io.workspace_bytes = (int64_t)ws.nbytes();
+        }
+        return wrote(ptored_gated_ffn_backward(&p, &io, g.stream(a[14])),
+                     {a[3], a[4], a[9], a[10], a[11]});
+    });
+}
+
+// The gradients of a call that all lie as they are: filling a range of memory
+// in their order, or 2-D with unit column stride; outs alike.
+struct Gradients {
+    std::vector<ptored_grad> list;
+    const at::Tensor& norm;
+    PyObject* outs;
+    Group g;
+
+    Gradients(PyObject* grads, PyObject* norm_, PyObject* outs_)
+        : norm(tensor(norm_)), outs(outs_), g(on_device(norm)) {
+        if (!(PyList_Check(grads) || PyTuple_Check(grads))) throw Misfit{};
+        const bool into = outs != nullptr && outs != Py_None;
+        if (into && !(PyList_Check(outs) || PyTuple_Check(outs))) throw Misfit{};
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(grads);
+        if (into && PySequence_Fast_GET_SIZE(outs) != n) throw Misfit{};
+        list.resize((size_t)n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(grads, i));
+            const at::Tensor& o = into ? tensor(PySequence_Fast_GET_ITEM(outs, i)) : t;
+            ptored_grad& e = list[(size_t)i];
+            if (t.layout() != at::kStrided || o.layout() != at::kStrided || !t.is_cuda() ||
+                !o.is_cuda() || t.get_device() != g.device || o.get_device() != g.device)
+                throw Misfit{};
+            e.dtype = code_of(t.scalar_type());
+            e.out_dtype = code_of(o.scalar_type());
+            if (e.out_dtype != PTORED_F32 && e.out_dtype != e.dtype) throw Misfit{};
+            if (into && t.sizes() != o.sizes()) throw Misfit{};
+            const int64_t elems = t.numel();
+            if (elems == 0) throw Misfit{};
+            e.data = t.data_ptr();
+            e.out = o.data_ptr();
+            if (t.is_contiguous() && o.is_contiguous()) {
+                e.rows = 1;
+                e.cols = e.ld = e.out_ld = elems;
+                continue;
+            }
+            if (t.dim() != 2) throw Misfit{};
+            e.rows = t.size(0);
+            e.cols = t.size(1);
+            e.ld = t.stride(0);
+            e.out_ld = o.stride(0);
+            if (t.stride(1) != 1 || o.stride(1) != 1 || e.ld < e.cols || e.out_ld < e.cols)
+                throw Misfit{};
+        }
+    }
+    static Group on_device(const at::Tensor& norm) {
+        if (norm.numel() != 1 || norm.scalar_type() != at::kFloat) throw Misfit{};
+        return Group(norm.reshape({1, 1}));
+    }
+    at::Tensor workspace(PyObject* given, PyObject* stream) const {
+        int64_t bytes = 0;
+        if (ptored_grad_norm_workspace(list.data(), (int64_t)list.size(), &bytes) != PTORED_OK)
+            throw Misfit{};
+        return g.workspace(given, stream, bytes);
+    }
+    int wrote_outs(int status, PyObject* grads) const {
+        PyObject* o = outs == Py_None ? grads : outs;
+        for (Py_ssize_t i = 0; status == PTORED_OK && i < PySequence_Fast_GET_SIZE(o); ++i)
+            wrote(status, {PySequence_Fast_GET_ITEM(o, i)});
+        return status;
+    }
+};
+
+// grads, norm, workspace, stream
+PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 4);
+        const Gradients v(a[0], a[1], nullptr);
+        const at::Tensor ws = v.workspace(a[2], a[3]);
+        return wrote(ptored_grad_norm(v.list.data(), (int64_t)v.list.size(),
+                                      static_cast<float*>(v.norm.data_ptr()),
+                                      ws.defined() ? ws.data_ptr() : nullptr,
+                                      ws.defined() ? (int64_t)ws.nbytes() : 0, v.g.stream(a[3])),
+                     {a[1]});
+    });
+}
+
+// grads, norm, max_norm, outs, stream
+PyObject* grad_scale(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 5);
+        const Gradients v(a[0], a[1], a[3]);
+        return v.wrote_outs(ptored_grad_scale(v.list.data(), (int64_t)v.list.size(),
+                                              static_cast<const float*>(v.norm.data_ptr()),
+                                              number(a[2]), v.g.stream(a[4])),
+                            a[0]);
+    });
+}
+
+// grads, max_norm, norm, outs, workspace, stream
+PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        want(n, 6);
+        const Gradients v(a[0], a[2], a[3]);
+        const float most = number(a[1]);
+        const at::Tensor ws = v.workspace(a[4], a[5]);
+        const int status = ptored_grad_clip(v.list.data(), (int64_t)v.list.size(), most,
+                                            static_cast<float*>(v.norm.data_ptr()),
+                                            ws.defined() ? ws.data_ptr() : nullptr,
+                                            ws.defined() ? (int64_t)ws.nbytes() : 0, v.g.stream(a[5]));
+        return v.wrote_outs(wrote(status, {a[2]}), a[0]);
+    });
+}
+
 #define PTORED_CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     PTORED_CALL(block_norm),        PTORED_CALL(block_norm_backward), PTORED_CALL(checkpoint_pack),
-    PTORED_CALL(checkpoint_unpack), PTORED_CALL(checkpoint_wgrad),    {nullptr, nullptr, 0, nullptr},
+    PTORED_CALL(checkpoint_unpack), PTORED_CALL(checkpoint_wgrad),    PTORED_CALL(layer_norm),
+    PTORED_CALL(layer_norm_backward), PTORED_CALL(gated_ffn),         PTORED_CALL(gated_ffn_backward),
+    PTORED_CALL(grad_norm),         PTORED_CALL(grad_scale),          PTORED_CALL(grad_clip),
+    {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods,
                       nullptr,               nullptr,        nullptr, nullptr};

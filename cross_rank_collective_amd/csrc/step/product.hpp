@@ -1,0 +1,489 @@
+// product.hpp -- the matrix products of the gated feed-forward block.
+//
+//     kForward  g = x Wg^T, u = x Wu^T, y = f(g) u     sums over columns
+//     kInput    dx = dg Wg + du Wu                     over features, both pairs in turn
+//     kWeight   dWg = dg^T x, dWu = du^T x             over tokens
+//
+// An operand's sum index lies along its rows (kAlong) or across them (kAcross);
+// either way it is staged in the LDS as it comes from memory, kStepBytes of
+// each row along k (64 elements of 16 bits, 32 of 32) and as many rows across.
+// What differs is how fragments are read: along rows a lane's 16 bytes at once,
+// across them by transposing loads (16 bits: 16 lanes fetch 4 rows x 16
+// columns and receive 4 rows of one column each) or word by word (32 bits).
+// A lane's fragment is 16 bytes along k of one row of the product: elements
+// 0-7 of 16 for lanes 0-31 and 8-15 for the others (0-3 of 8 and 4-7 in 32
+// bits), in both layouts alike, so that any two operands match.
+//
+// The LDS has two buffers.  While a workgroup multiplies out of one, the loads
+// of the next step are on their way to the other.  One barrier a step, before
+// its last quarter, whose fragments are then in registers: behind it the next
+// step's buffer is whole and this step's is free, so the loads of the step
+// after next are asked for at once and the next step's first fragments are read
+// under the last quarter's products.
+//
+// kDirect loads go straight to the LDS (16 bytes a lane); they need rows that
+// start at multiples of 16 bytes and hold whole chunks.  Other matrices go
+// through registers, a chunk that would pass the end of a row loaded from the
+// row's last whole chunk and moved.
+#pragma once
+
+#include <type_traits>
+
+#include "gated.hpp"
+
+namespace ptored {
+namespace step {
+
+using namespace block;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer resource: reads as zeros
+
+// Address of LDS memory as the hardware takes it.
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+    return (uint32_t)(uintptr_t)(lds_char*)p;
+}
+
+// 16 bytes a lane from `off` behind the resource's base to the LDS at `to` (the
+// same for all lanes) + 16 x lane.  The compiler does not see the write:
+// barriers with a wait order it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is reserved, so every user sets it first
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t off, uint32_t to) {
+    asm volatile(
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %0, %1, 0 offen lds"
+        :
+        : "v"(off), "s"(rsrc), "s"(to)
+        : "m0");
+}
+#pragma clang diagnostic pop
+
+__device__ __forceinline__ u32x4 rsrc_words(const char* base) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xFFFFu)),
+                   0x7FFFFFFFu, 0x00020000u};
+}
+
+// Where rows of 128 bytes keep a chunk: rows of 8, and the even and the odd
+// ones of 16, keep the same chunk in different banks.
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ (row >> 3 & 1); }
+
+// A tile's share of one operand: EXT rows of the product, kStepBytes along k.
+// HALVES: the tile's upper half are a second matrix's rows of the same numbers.
+template <int DT, int LAYOUT, int EXT, int THREADS, bool DIRECT, bool HALVES>
+struct Side {
+    using E = Elem<DT>;
+    static constexpr int ES = E::kBytes, V = 16 / ES;
+    static constexpr int kDepth = kStepBytes / ES;  // k's a step
+    static constexpr int kRow = LAYOUT == kAlong ? kStepBytes : EXT * ES;
+    static constexpr int kBytes = EXT * kStepBytes;
+    static constexpr int kPerRow = kRow / 16;
+    static constexpr int kLoads = kBytes / 16 / THREADS;
+    static constexpr int kRows = THREADS / kPerRow;  // LDS rows that one load of all threads covers
+    static_assert(kRows % (LAYOUT == kAlong ? 16 : 4) == 0, "a thread's rows share their swizzle");
+    static_assert(!HALVES || (LAYOUT == kAlong && kLoads % 2 == 0), "halves are whole loads");
+
+    uint32_t off[kLoads];  // bytes from the operand's place, or kNowhere
+    int depth;             // kAlong: k of this thread's chunks in a step; kAcross: its first row's
+    int moved;             // kAcross: elements from where the chunks are loaded to where they belong
+    u32x4 held[DIRECT ? 1 : kLoads];
+
+    // The thread's chunks of the product's rows [first, first + EXT) of `total`.
+    __device__ __forceinline__ void init(int64_t first, int64_t total, int64_t ld) {
+        const int pos = (int)threadIdx.x % kPerRow, row0 = (int)threadIdx.x / kPerRow;
+        moved = 0;
+        if constexpr (LAYOUT == kAlong) {
+            const int c = pos ^ swizzle(row0);
+            depth = c * V;
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) {
+                const int row = row0 + (HALVES ? q % (kLoads / 2) : q) * kRows;
+                off[q] = first + row < total ? (uint32_t)(row * ld) + c * 16 : kNowhere;
+            }
+        } else {
+            const int c = ((pos >> 2 ^ (row0 & 3)) << 2) | (pos & 3);
+            depth = row0;
+            int64_t col = first + c * V;
+            const bool in = col < total;
+            if (!DIRECT && in && col + V > total) {
+                const int64_t from = total > V ? total - V : 0;
+                moved = (int)(col - from);
+                col = from;
+            }
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q)
+                // where moved, perhaps before the tile's first column
+                off[q] = in ? (uint32_t)((row0 + q * kRows) * ld + (col - first) * ES) : kNowhere;
+        }
+    }
+
+    // Whether chunk q lies past the `left` k's that remain.
+    __device__ __forceinline__ bool past(int q, int64_t left) const {
+        return (LAYOUT == kAlong ? depth : depth + q * kRows) >= left;
+    }
+    static __device__ __forceinline__ bool second(int q) { return HALVES && q >= kLoads / 2; }
+
+    __device__ __forceinline__ void load_direct(const char* p, const char* p2, int64_t left,
+                                                uint32_t to) const {
+        const u32x4 r = rsrc_words(p), r2 = HALVES ? rsrc_words(p2) : r;
+        const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            load_to_lds(second(q) ? r2 : r, past(q, left) ? kNowhere : off[q],
+                        to + q * (THREADS * 16) + wave * 1024);
+    }
+
+    // The same to registers.  `extent`: elements of the rows that chunks lie in.
+    __device__ __forceinline__ void load_held(const char* p, const char* p2, int64_t left,
+                                              int64_t extent) {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            held[q] = (u32x4)(0u);
+            if (off[q] == kNowhere || past(q, left)) continue;
+            const char* at = (second(q) ? p2 : p) + (int64_t)(int32_t)off[q];
+            if (extent < V) {  // the row's only chunk
+                uint32_t w[4] = {};
+#pragma unroll
+                for (int i = 0; i < V - 1; ++i) {
+                    if (i >= extent) continue;
+                    if constexpr (ES == 4)
+                        w[i] = reinterpret_cast<const uint32_t*>(at)[i];
+                    else
+                        w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(at)[i] << (16 * (i % 2));
+                }
+                held[q] = (u32x4){w[0], w[1], w[2], w[3]};
+            } else {
+                // of a chunk that the row's end cuts, what ends with the row
+                const int by = LAYOUT == kAlong && depth + V > left ? depth + V - (int)left : 0;
+                held[q] = *reinterpret_cast<const u32x4_any*>(at - by * ES);
+                if (LAYOUT == kAlong && by != 0) held[q] = shift_down(held[q], by * ES);
+            }
+        }
+    }
+    __device__ __forceinline__ void store_held(char* to) const {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            *reinterpret_cast<u32x4*>(to + (q * THREADS + (int)threadIdx.x) * 16) =
+                LAYOUT == kAcross && moved != 0 ? shift_down(held[q], moved * ES) : held[q];
+    }
+};
+
+// A lane's fragment of rows [32 block, 32 block + 32) in quarter `sub` of a step.
+template <int DT, int LAYOUT, int EXT>
+__device__ __forceinline__ u32x4 fragment(const char* buf, int sub, int block) {
+    constexpr int ES = Elem<DT>::kBytes, kRow = LAYOUT == kAlong ? kStepBytes : EXT * ES;
+    const int lane = (int)threadIdx.x & 63, hi = lane >> 5;
+    if constexpr (LAYOUT == kAlong) {
+        const int row = lane & 31;
+        return *reinterpret_cast<const u32x4*>(buf + block * (32 * kRow) + row * kRow +
+                                               ((2 * sub ^ (hi ^ swizzle(row))) << 4));
+    } else if constexpr (ES == 2) {
+        // rows hi 8 + 0-3 and + 4-7 of 16; 64-byte piece c of row t is at c ^ (t & 3)
+        const int t = (lane & 15) >> 2;
+        const char* at = buf + (sub * 16 + hi * 8 + t) * kRow + ((block ^ t) << 6) +
+                         (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
+        const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 4 * kRow));
+        return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = *reinterpret_cast<const uint32_t*>(buf + (sub * 8 + hi * 4 + j) * kRow +
+                                                      ((block * 2 + (lane >> 4 & 1) ^ j) << 6) +
+                                                      (lane & 15) * 4);
+        return v;
+    }
+}
+
+// acc += a b^T over a quarter's k's.
+template <int DT>
+__device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 acc) {
+    if constexpr (DT == PTORED_BF16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a),
+                                                       __builtin_bit_cast(b8, b), acc, 0, 0, 0);
+    } else if constexpr (DT == PTORED_F16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a),
+                                                      __builtin_bit_cast(h8, b), acc, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(as_f(a[j]), as_f(b[j]), acc, 0, 0, 0);
+        return acc;
+    }
+}
+
+// Waits for this wave's loads, then for the other waves.
+__device__ __forceinline__ void landed() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// WM x WN waves of TM x TN blocks of 32 x 32.
+template <int DT, int KIND, int WM, int WN, int TM, int TN, bool DIRECT>
+__global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
+    constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
+    constexpr bool kPair = KIND == kForward;  // block j of a wave belongs to weight j
+    static_assert(!kPair || TN == 2, "a gate's block and an up's");
+    constexpr int LA = KIND == kWeight ? kAcross : kAlong, LB = KIND == kForward ? kAlong : kAcross;
+    using A = Side<DT, LA, BM, kThreads, DIRECT, false>;
+    using B = Side<DT, LB, BN, kThreads, DIRECT, kPair>;
+    using E = Elem<DT>;
+    constexpr int kDepth = A::kDepth, kBytes = A::kBytes + B::kBytes;
+    constexpr int kCols = kPair ? BN / 2 : BN;  // of the output
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kBytes];
+
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = (int)(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    // Workgroups go to the 8 dies in turn: each die gets consecutive tiles of
+    // the order in which 4 rows of tiles advance together, so that its cache
+    // serves most reads of both operands.
+    const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.outs * a.splits;
+    int id = (int)blockIdx.x;
+    {
+        const int die = id % 8, each = total / 8, rest = total % 8;
+        id = die * each + (die < rest ? die : rest) + id / 8;
+    }
+    const int split = id / (tiles * a.outs), in_split = id % (tiles * a.outs);
+    const int which = in_split / tiles, tile = in_split % tiles;
+    const int band = tile / (4 * a.tiles_n), band_rows = min(4, a.tiles_m - band * 4);
+    const int in_band = tile - band * 4 * a.tiles_n;
+    const int64_t m0 = (int64_t)(band * 4 + in_band % band_rows) * BM;
+    const int64_t n0 = (int64_t)(in_band / band_rows) * kCols;
+
+    // Where the next load takes its step from.
+    const int64_t per_pair = a.k > kDepth ? (a.k + kDepth - 1) / kDepth : 1;
+    const int64_t all = KIND == kInput ? 2 * per_pair : per_pair;
+    const int64_t first = split * a.steps_per_split;
+    const int64_t steps = min(a.steps_per_split, all - first);
+    int pair = 0;
+    int64_t left;
+    const char *pa, *pb, *pb2;
+    auto begin = [&](int64_t step) {
+        pair = KIND == kInput ? (int)(step / per_pair) : KIND == kWeight ? which : 0;
+        const int64_t in = KIND == kInput ? step - pair * per_pair : step;
+        const int from = KIND == kWeight ? 0 : pair;
+        left = a.k - in * kDepth;
+        pa = a.a[pair] + (LA == kAlong ? m0 * a.a_ld[pair] + in * kStepBytes
+                                       : in * kDepth * a.a_ld[pair] + m0 * E::kBytes);
+        pb = a.b[from] + (LB == kAlong ? n0 * a.b_ld[from] + in * kStepBytes
+                                       : in * kDepth * a.b_ld[from] + n0 * E::kBytes);
+        pb2 = kPair ? a.b[1] + n0 * a.b_ld[1] + in * kStepBytes : pb;
+    };
+    A sa;
+    B sb;
+    auto places = [&] {
+        sa.init(m0, a.m, a.a_ld[pair]);
+        sb.init(n0, a.n, a.b_ld[KIND == kWeight ? 0 : pair]);
+    };
+    auto advance = [&] {
+        left -= kDepth;
+        if (KIND == kInput && left <= 0 && pair == 0) {
+            begin(per_pair);
+            places();
+            return;
+        }
+        pa += LA == kAlong ? kStepBytes : kDepth * a.a_ld[pair];
+        pb += LB == kAlong ? kStepBytes : kDepth * a.b_ld[KIND == kWeight ? 0 : pair];
+        pb2 += kStepBytes;
+    };
+    // extents of the rows that chunks lie in
+    const int64_t ea = LA == kAlong ? a.k : a.m, eb = LB == kAlong ? a.k : a.n;
+    auto hold = [&] {
+        sa.load_held(pa, pa, left, ea);
+        sb.load_held(pb, pb2, left, eb);
+        advance();
+    };
+    auto stage = [&](char* buf) {
+        if constexpr (DIRECT) {
+            sa.load_direct(pa, pa, left, lds_address(buf));
+            sb.load_direct(pb, pb2, left, lds_address(buf) + A::kBytes);
+            advance();
+        } else {
+            sa.store_held(buf);
+            sb.store_held(buf + A::kBytes);
+        }
+    };
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16)(0.0f);
+    struct Fragments {
+        u32x4 a[TM], b[TN];
+    };
+    auto read = [&](const char* buf, int sub, Fragments& f) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) f.a[i] = fragment<DT, LA, BM>(buf, sub, wm * TM + i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            f.b[j] = fragment<DT, LB, BN>(buf + A::kBytes, sub, kPair ? j * WN + wn : wn * TN + j);
+    };
+    auto products = [&](const Fragments& f) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = multiply<DT>(f.a[i], f.b[j], acc[i][j]);
+    };
+
+    char *cur = lds, *next = lds + kBytes;
+    begin(first);
+    places();
+    if (!DIRECT) hold();
+    stage(cur);
+    if (steps > 1) {
+        if (!DIRECT) hold();
+        stage(next);
+    }
+    if (!DIRECT && steps > 2) hold();
+    landed();
+    Fragments even, odd;
+    read(cur, 0, even);
+    for (int64_t s = 0; s < steps; ++s) {
+        read(cur, 1, odd);
+        products(even);
+        read(cur, 2, even);
+        products(odd);
+        read(cur, 3, odd);
+        products(even);
+        landed();
+        if (s + 2 < steps) {
+            stage(cur);
+            if (!DIRECT && s + 3 < steps) hold();
+        }
+        read(next, 0, even);  // past the last step: never used
+        products(odd);
+        char* t = cur;
+        cur = next;
+        next = t;
+    }
+
+    // Register r of a 32 x 32 block is row 8 (r / 4) + 4 (lane / 32) + r % 4,
+    // column lane % 32.
+    const int64_t row0 = m0 + wm * TM * 32 + 4 * (lane >> 5);
+    auto each = [&](auto f) {  // f(row, i, r) of the rows inside
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t row = row0 + i * 32 + 8 * (r / 4) + r % 4;
+                if (row < a.m) f(row, i, r);
+            }
+    };
+    if constexpr (kPair) {
+        const int64_t col = n0 + wn * 32 + (lane & 31);
+        if (col >= a.n) return;
+        each([&](int64_t row, int i, int r) {
+            const float g = acc[i][0][r], u = acc[i][1][r];
+            E::store1(a.out[0].p + row * a.out[0].ld + col * E::kBytes, activation(a.activation, g) * u);
+            if (a.gate.p) E::store1(a.gate.p + row * a.gate.ld + col * E::kBytes, g);
+            if (a.up.p) E::store1(a.up.p + row * a.up.ld + col * E::kBytes, u);
+        });
+    } else {
+        const Mat out = a.out[which];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t col = n0 + (wn * TN + j) * 32 + (lane & 31);
+            if (col >= a.n) continue;
+            each([&](int64_t row, int i, int r) {
+                float v = acc[i][j][r];
+                if (a.splits > 1) {
+                    a.ws[(((int64_t)split * a.outs + which) * a.m + row) * a.ws_ld + col] = v;
+                } else if (a.out_f32) {
+                    float* p = reinterpret_cast<float*>(out.p + row * out.ld) + col;
+                    *p = a.accumulate ? *p + v : v;
+                } else {
+                    char* p = out.p + row * out.ld + col * E::kBytes;
+                    if (a.accumulate) v += E::load1(p);
+                    E::store1(p, v);
+                }
+            });
+        }
+    }
+}
+
+// out (+)= the splits' sums.  A workgroup takes 64 times 4 columns of a row, 4
+// threads each for every fourth split, joined in the LDS in a fixed order.
+constexpr int kJoinLanes = 64, kJoinGroups = 4;
+template <int DT>
+__global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(const ProductArgs a) {
+    using E = Elem<DT>;
+    __shared__ f32x4 part[kJoinGroups][kJoinLanes];
+    const int lane = (int)threadIdx.x % kJoinLanes, group = (int)threadIdx.x / kJoinLanes;
+    const int64_t col = ((int64_t)blockIdx.x * kJoinLanes + lane) * 4;
+    const int64_t rows = a.m * a.outs, step = rows * a.ws_ld;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        f32x4 sum = (f32x4)(0.0f);
+        if (col < a.n) {
+            const float* ws = a.ws + row * a.ws_ld + col;
+#pragma unroll 4
+            for (int s = group; s < a.splits; s += kJoinGroups)
+                sum += *reinterpret_cast<const f32x4*>(ws + s * step);
+        }
+        part[group][lane] = sum;
+        __syncthreads();
+        if (group == 0 && col < a.n) {
+            const bool second = row >= a.m;
+            const Mat out = a.out[second];
+            char* at = out.p + (second ? row - a.m : row) * out.ld;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (col + i >= a.n) continue;
+                float v = (part[0][lane][i] + part[1][lane][i]) + (part[2][lane][i] + part[3][lane][i]);
+                if (a.out_f32) {
+                    float* p = reinterpret_cast<float*>(at) + col + i;
+                    *p = a.accumulate ? *p + v : v;
+                } else {
+                    char* p = at + (col + i) * E::kBytes;
+                    if (a.accumulate) v += E::load1(p);
+                    E::store1(p, v);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int DT, int KIND>
+int product_launch(const ProductArgs& a, hipStream_t stream) {
+    void* args[] = {const_cast<ProductArgs*>(&a)};
+    const void* k;
+    int threads = 256;
+    if (a.shape == kTile256) {
+        threads = 512;
+        if constexpr (DT == PTORED_F32) return kFailed;
+        else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, true>);
+    } else if (a.direct) {
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, true>);
+    } else {
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, false>);
+    }
+    const uint32_t grid = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)(a.outs * a.splits);
+    if (hipLaunchKernel(k, dim3(grid), dim3((uint32_t)threads), args, 0, stream) != hipSuccess)
+        return kFailed;
+    if constexpr (KIND != kForward) {
+        if (a.splits == 1) return kOk;
+        const int64_t rows = a.m * a.outs;
+        const dim3 joins((uint32_t)((a.n + 4 * kJoinLanes - 1) / (4 * kJoinLanes)),
+                         (uint32_t)(rows < 32768 ? rows : 32768));
+        if (hipLaunchKernel(reinterpret_cast<const void*>(product_join_kernel<DT>), joins,
+                            dim3(kJoinLanes * kJoinGroups), args, 0, stream) != hipSuccess)
+            return kFailed;
+    }
+    return kOk;
+}
+
+}  // namespace step
+}  // namespace ptored

@@ -1,0 +1,610 @@
+// step_host.cpp -- C ABI of the step's operators: argument checks, work
+// splits, launches.
+//
+// Every argument check runs before the first HIP call, so every error status
+// is reachable without a GPU.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <memory>
+#include <new>
+
+#include "block/block_checks.hpp"
+#include "step_plan.h"
+
+namespace ptored {
+namespace step {
+namespace {
+
+using namespace block;
+
+// ---------------------------------------------------------------- layer norm
+
+bool layer_valid(const ptored_layer_norm_params* p) {
+    return p != nullptr && shape_ok(p->rows, p->cols);
+}
+bool layer_supported(const ptored_layer_norm_params& p) {
+    return float_type(p.dtype) && (p.weight_dtype == PTORED_F32 || p.weight_dtype == p.dtype) &&
+           p.cols <= PTORED_BLOCK_MAX_COLS;
+}
+
+// Workgroups of the backward pass: as many as the chip holds at once, but with
+// work for all compute units none takes fewer than 5 rows, whose partial rows
+// (8 bytes a column) would weigh as much as the rows' own data.
+int64_t layer_chunks(int64_t rows, int64_t cols, int dtype) {
+    if (rows == 0 || cols == 0) return 0;
+    const int64_t slot = dtype == PTORED_F32 ? 4 : 8, room = dtype == PTORED_F32 ? 20 : 16;
+    const int64_t waves = std::min<int64_t>(16, (cols + 64 * slot - 1) / (64 * slot));
+    const int64_t target = 256 * (room / waves);
+    const int64_t per = std::max((rows + target - 1) / target,
+                                 std::min<int64_t>(5, (rows + 255) / 256));
+    return (rows + per - 1) / per;
+}
+// Columns of a partial row: whole vectors of 4.
+int64_t pitch_of(int64_t cols) { return (cols + 3) / 4 * 4; }
+int64_t layer_workspace(int64_t chunks, int64_t cols) { return chunks * 2 * pitch_of(cols) * 4; }
+
+// ---------------------------------------------------------------- feed-forward
+
+bool ffn_valid(const ptored_ffn_params* p) {
+    return p != nullptr && shape_ok(p->rows, p->cols) && shape_ok(p->rows, p->wide) &&
+           shape_ok(p->wide, p->cols);
+}
+bool ffn_supported(const ptored_ffn_params& p) {
+    return float_type(p.dtype) && p.activation >= PTORED_SILU && p.activation <= PTORED_GELU_TANH;
+}
+// A matrix whose tiles' offsets fit 32 bits.
+bool pitch_supported(const ptored_rows& r, int64_t rows, int es) {
+    return r.data == nullptr || rows <= 1 || r.ld <= PTORED_FFN_MAX_PITCH / es;
+}
+// Rows that start at multiples of 16 bytes and hold whole chunks of 16.
+bool direct_of(const ptored_rows& r, int64_t rows, int64_t cols, int es) {
+    return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && cols * es % 16 == 0 &&
+           (rows <= 1 || r.ld * es % 16 == 0);
+}
+
+struct ProductShape {
+    int64_t tiles_m, tiles_n, splits, steps_per_split;
+    int shape;
+};
+
+constexpr int64_t kMaxTiles = int64_t(1) << 22;
+
+// kInput: k of each of the two pairs.
+ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, int dtype,
+                           bool direct) {
+    ProductShape s{};
+    const int64_t depth = kStepBytes / esize_of(dtype);
+    const int64_t steps = std::max<int64_t>(1, (k + depth - 1) / depth) * (kind == kInput ? 2 : 1);
+    auto tiles = [&](int64_t tile) {
+        const int64_t cols = kind == kForward ? tile / 2 : tile;
+        s.tiles_m = (m + tile - 1) / tile;
+        s.tiles_n = (n + cols - 1) / cols;
+        return s.tiles_m * s.tiles_n * outs;
+    };
+    s.shape = kTile256;
+    if (dtype == PTORED_F32 || !direct || tiles(256) < 160) s.shape = kTile128;
+    const int64_t count = tiles(s.shape == kTile256 ? 256 : 128);
+    s.splits = 1;
+    if (kind != kForward && s.shape == kTile128 && count > 0 && count <= 256)
+        s.splits = std::max<int64_t>(1, std::min(512 / count, steps / 8));
+    s.steps_per_split = (steps + s.splits - 1) / s.splits;
+    s.splits = (steps + s.steps_per_split - 1) / s.steps_per_split;
+    return s;
+}
+int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs) {
+    return s.splits > 1 ? s.splits * outs * m * pitch_of(n) * 4 : 0;
+}
+bool launchable(const ProductShape& s, int outs) {
+    return s.tiles_m <= kMaxTiles && s.tiles_n <= kMaxTiles &&
+           s.tiles_m * s.tiles_n * outs * s.splits <= kMaxTiles;
+}
+void set_shape(ProductArgs& a, const ProductShape& s, bool direct) {
+    a.tiles_m = (int32_t)s.tiles_m;
+    a.tiles_n = (int32_t)s.tiles_n;
+    a.splits = (int32_t)s.splits;
+    a.steps_per_split = s.steps_per_split;
+    a.shape = s.shape;
+    a.direct = direct;
+}
+void set_a(ProductArgs& a, int i, const ptored_rows& r, int es) {
+    a.a[i] = static_cast<const char*>(r.data);
+    a.a_ld[i] = r.ld * es;
+}
+void set_b(ProductArgs& a, int i, const ptored_rows& r, int es) {
+    a.b[i] = static_cast<const char*>(r.data);
+    a.b_ld[i] = r.ld * es;
+}
+
+// ---------------------------------------------------------------- gradients
+
+constexpr int64_t kInt = 0x7FFFFFFF;
+
+bool grad_shape_ok(const ptored_grad& g, bool scaled) {
+    if (!shape_ok(g.rows, g.cols)) return false;
+    if (g.rows == 0 || g.cols == 0) return true;
+    if (g.data == nullptr || (scaled && g.out == nullptr)) return false;
+    return g.rows == 1 || (pitch_ok(g.rows, g.cols, g.ld) && (!scaled || pitch_ok(g.rows, g.cols, g.out_ld)));
+}
+bool grad_supported(const ptored_grad& g, bool scaled) {
+    if (!float_type(g.dtype)) return false;
+    if (scaled && g.out_dtype != PTORED_F32 && g.out_dtype != g.dtype) return false;
+    return g.rows <= 1 || (g.rows <= kInt && g.ld <= kInt && (!scaled || g.out_ld <= kInt));
+}
+int64_t span_of(const ptored_grad& g, int64_t ld, int es) {
+    return (g.rows == 1 ? g.cols : (g.rows - 1) * ld + g.cols) * es;
+}
+
+// Elements of a workgroup's chunk: 2048 workgroups, 8 a compute unit, for
+// gradients that fill the chip; smaller ones in chunks of 4096 elements.
+int64_t grad_chunk(const ptored_grad* grads, int64_t count) {
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) total += grads[i].rows * grads[i].cols;
+    return std::min<int64_t>(std::max<int64_t>(4096, ((total + 2047) / 2048 + 1023) / 1024 * 1024),
+                             int64_t(1) << 30);
+}
+// Workgroups of one gradient.
+int64_t grad_groups(const ptored_grad& g, int64_t chunk) {
+    if (g.rows == 0 || g.cols == 0) return 0;
+    if (g.rows == 1 || g.cols > chunk / 2) return g.rows * ((g.cols + chunk - 1) / chunk);
+    const int64_t group = chunk / g.cols;
+    return (g.rows + group - 1) / group;
+}
+int64_t all_groups(const ptored_grad* grads, int64_t count, int64_t chunk) {
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) n += grad_groups(grads[i], chunk);
+    return n;
+}
+
+struct Span {
+    uintptr_t begin, end;
+    bool out;
+};
+// Whether an output among the gradients (or `more`, 2 spans) overlaps another
+// buffer.  -1: no memory.
+int grads_overlap(const ptored_grad* grads, int64_t count, const Span* more) {
+    std::unique_ptr<Span[]> s(new (std::nothrow) Span[2 * (size_t)count + 2]);
+    if (!s) return -1;
+    size_t n = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const ptored_grad& g = grads[i];
+        if (g.rows == 0 || g.cols == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(g.data), q = reinterpret_cast<uintptr_t>(g.out);
+        const int64_t bytes = span_of(g, g.ld, esize_of(g.dtype));
+        const bool same = p == q && g.dtype == g.out_dtype && (g.rows == 1 || g.ld == g.out_ld);
+        s[n++] = {p, p + (uintptr_t)bytes, same};
+        if (!same) s[n++] = {q, q + (uintptr_t)span_of(g, g.out_ld, esize_of(g.out_dtype)), true};
+    }
+    for (int i = 0; i < 2; ++i)
+        if (more[i].end > more[i].begin) s[n++] = more[i];
+    std::sort(s.get(), s.get() + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    uintptr_t any = 0, outs = 0;  // how far buffers, and outputs among them, reach so far
+    for (size_t i = 0; i < n; ++i) {
+        if (s[i].begin < (s[i].out ? any : outs)) return 1;
+        any = std::max(any, s[i].end);
+        if (s[i].out) outs = std::max(outs, s[i].end);
+    }
+    return 0;
+}
+
+Span span(const void* p, int64_t bytes, bool out) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return {b, b + (uintptr_t)bytes, out};
+}
+
+// The checks of all three calls.  `sums`: the call needs a workspace.
+int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sums, const float* norm,
+                  const void* workspace, int64_t workspace_bytes) {
+    if (count < 0 || count > kInt || (count > 0 && grads == nullptr) || norm == nullptr)
+        return PTORED_ERR_INVALID_ARG;
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!grad_shape_ok(grads[i], scaled)) return PTORED_ERR_INVALID_ARG;
+        total += grads[i].rows * grads[i].cols;
+        if (total > kMaxElems) return PTORED_ERR_INVALID_ARG;
+    }
+    for (int64_t i = 0; i < count; ++i)
+        if (!grad_supported(grads[i], scaled)) return PTORED_ERR_UNSUPPORTED;
+    const int64_t groups = sums ? all_groups(grads, count, grad_chunk(grads, count)) : 0;
+    if (groups > kInt) return PTORED_ERR_UNSUPPORTED;
+    if (groups > 0 && (workspace == nullptr || workspace_bytes < groups * 8 ||
+                       reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+        return PTORED_ERR_INVALID_ARG;
+    bool aligned = reinterpret_cast<uintptr_t>(norm) % 4 == 0;
+    for (int64_t i = 0; i < count && aligned; ++i) {
+        const ptored_grad& g = grads[i];
+        if (g.rows == 0 || g.cols == 0) continue;
+        aligned = reinterpret_cast<uintptr_t>(g.data) % (uintptr_t)esize_of(g.dtype) == 0 &&
+                  (!scaled || reinterpret_cast<uintptr_t>(g.out) % (uintptr_t)esize_of(g.out_dtype) == 0);
+    }
+    if (!aligned) return PTORED_ERR_INVALID_ARG;
+    const Span more[2] = {span(norm, 4, sums), span(workspace, groups * 8, true)};
+    if (scaled) {
+        const int over = grads_overlap(grads, count, more);
+        return over < 0 ? PTORED_ERR_HIP : over > 0 ? PTORED_ERR_OVERLAP : PTORED_OK;
+    }
+    // only the norm and the workspace are written
+    if (more[0].begin < more[1].end && more[1].begin < more[0].end) return PTORED_ERR_OVERLAP;
+    for (int64_t i = 0; i < count; ++i) {
+        const ptored_grad& g = grads[i];
+        if (g.rows == 0 || g.cols == 0) continue;
+        const Span s = span(g.data, span_of(g, g.ld, esize_of(g.dtype)), false);
+        for (const Span& m : more)
+            if (s.begin < m.end && m.begin < s.end) return PTORED_ERR_OVERLAP;
+    }
+    return PTORED_OK;
+}
+
+// Cuts the gradients into launches and calls f(list) for each.  Returns a
+// launch's code.
+template <typename F>
+int each_launch(const ptored_grad* grads, int64_t count, int64_t chunk, GradList& a, F f) {
+    a.count = a.groups = 0;
+    a.chunk = chunk;
+    for (int64_t i = 0; i < count; ++i) {
+        const ptored_grad& g = grads[i];
+        const int64_t groups = grad_groups(g, chunk);
+        if (groups == 0) continue;
+        GradEntry& e = a.e[a.count++];
+        e.data = static_cast<const char*>(g.data);
+        e.out = static_cast<char*>(g.out);
+        e.cols = g.cols;
+        e.rows = (int32_t)g.rows;
+        e.ld = g.rows == 1 ? 0 : (int32_t)g.ld;
+        e.out_ld = g.rows == 1 ? 0 : (int32_t)g.out_ld;
+        e.first = a.groups;
+        e.type = g.dtype | g.out_dtype << 8;
+        e.chunks = g.rows == 1 || g.cols > chunk / 2 ? (int32_t)((g.cols + chunk - 1) / chunk) : 0;
+        a.groups += (int32_t)groups;
+        if (a.count == kGradEntries) {
+            const int rc = f(a);
+            if (rc != kOk) return rc;
+            a.count = a.groups = 0;
+        }
+    }
+    return a.count > 0 ? f(a) : kOk;
+}
+
+int run_sums(const ptored_grad* grads, int64_t count, int64_t chunk, GradList& a, double* sums,
+             hipStream_t stream) {
+    int64_t done = 0;
+    const int rc = each_launch(grads, count, chunk, a, [&](GradList& l) {
+        l.sums = sums + done;
+        done += l.groups;
+        return grad_sums(l, stream);
+    });
+    a.all = sums;
+    a.all_count = (int32_t)done;
+    return rc;
+}
+
+}  // namespace
+}  // namespace step
+}  // namespace ptored
+
+using namespace ptored::step;
+using ptored::block::Buffers;
+using ptored::block::esize_of;
+using ptored::block::float_type;
+using ptored::block::mat;
+using ptored::block::shape_ok;
+using ptored::block::status_of;
+
+extern "C" int ptored_layer_norm(const void* const* parts, int nranks, int64_t part_ld,
+                                 const ptored_layer_norm_params* params, ptored_rows x,
+                                 ptored_rows x_out, ptored_rows z, float* mean, float* rstd,
+                                 hipStream_t stream) {
+    if (nranks < 0 || nranks > PTORED_MAX_RANKS || (nranks > 0 && parts == nullptr))
+        return PTORED_ERR_INVALID_ARG;
+    if (!layer_valid(params) || x.data == nullptr || !(params->eps >= 0.0f))
+        return PTORED_ERR_INVALID_ARG;
+    const ptored_layer_norm_params& p = *params;
+    const int es = esize_of(p.dtype), ws = esize_of(p.weight_dtype);
+    Buffers b;
+    bool ok = b.rows(x.data, p.rows, p.cols, x.ld, es, false);
+    for (int r = 0; r < nranks && ok; ++r)
+        ok = parts[r] != nullptr && b.rows(parts[r], p.rows, p.cols, part_ld, es, false);
+    ok = ok && b.rows(x_out.data, p.rows, p.cols, x_out.ld, es, true) &&
+         b.rows(z.data, p.rows, p.cols, z.ld, es, true);
+    if (!ok) return PTORED_ERR_INVALID_ARG;
+    if (!layer_supported(p)) return PTORED_ERR_UNSUPPORTED;
+    b.vec(p.weight, p.cols * ws, ws, false);
+    b.vec(p.bias, p.cols * ws, ws, false);
+    b.vec(mean, p.rows * 4, 4, true);
+    b.vec(rstd, p.rows * 4, 4, true);
+    if (!b.aligned()) return PTORED_ERR_INVALID_ARG;
+    if (!b.disjoint()) return PTORED_ERR_OVERLAP;
+    if (p.rows == 0 || p.cols == 0) return PTORED_OK;
+
+    LayerNormArgs a{};
+    for (int r = 0; r < nranks; ++r) a.part[r] = static_cast<const char*>(parts[r]);
+    a.part_ld = part_ld * es;
+    a.nranks = nranks;
+    a.rows = p.rows;
+    a.cols = (int32_t)p.cols;
+    a.x = mat(x, es);
+    a.x_out = mat(x_out, es);
+    a.z = mat(z, es);
+    a.w = static_cast<const char*>(p.weight);
+    a.b = static_cast<const char*>(p.bias);
+    a.mean = mean;
+    a.rstd = rstd;
+    a.w_f32 = p.weight_dtype == PTORED_F32;
+    a.eps = p.eps;
+    a.inv_cols = 1.0f / (float)p.cols;
+    return status_of(PTORED_BY_TYPE(layer_norm, p.dtype, a, stream));
+}
+
+extern "C" int ptored_layer_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+    if (bytes == nullptr || !shape_ok(rows, cols)) return PTORED_ERR_INVALID_ARG;
+    if (cols > PTORED_BLOCK_MAX_COLS) return PTORED_ERR_UNSUPPORTED;
+    // of any type
+    *bytes = layer_workspace(std::max(layer_chunks(rows, cols, PTORED_F32),
+                                      layer_chunks(rows, cols, PTORED_BF16)), cols);
+    return PTORED_OK;
+}
+
+extern "C" int ptored_layer_norm_backward(const ptored_layer_norm_params* params, ptored_rows dz,
+                                          ptored_rows dx_out, ptored_rows x_out, const float* mean,
+                                          const float* rstd, ptored_rows dx, void* dweight,
+                                          void* dbias, void* workspace, int64_t workspace_bytes,
+                                          hipStream_t stream) {
+    if (!layer_valid(params) || dz.data == nullptr || x_out.data == nullptr || mean == nullptr ||
+        rstd == nullptr)
+        return PTORED_ERR_INVALID_ARG;
+    const ptored_layer_norm_params& p = *params;
+    const int es = esize_of(p.dtype), ws = esize_of(p.weight_dtype);
+    Buffers b;
+    if (!b.rows(dz.data, p.rows, p.cols, dz.ld, es, false) ||
+        !b.rows(dx_out.data, p.rows, p.cols, dx_out.ld, es, false) ||
+        !b.rows(x_out.data, p.rows, p.cols, x_out.ld, es, false) ||
+        !b.rows(dx.data, p.rows, p.cols, dx.ld, es, true))
+        return PTORED_ERR_INVALID_ARG;
+    if (!layer_supported(p)) return PTORED_ERR_UNSUPPORTED;
+    b.vec(p.weight, p.cols * ws, ws, false);
+    b.vec(mean, p.rows * 4, 4, false);
+    b.vec(rstd, p.rows * 4, 4, false);
+    b.vec(dweight, p.cols * ws, ws, true);
+    b.vec(dbias, p.cols * ws, ws, true);
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    const int64_t chunks = layer_chunks(p.rows, p.cols, p.dtype);
+    const int64_t need = sums ? layer_workspace(chunks, p.cols) : 0;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PTORED_ERR_INVALID_ARG;
+    if (need > 0) b.vec(workspace, need, 16, true);
+    if (!b.aligned()) return PTORED_ERR_INVALID_ARG;
+    if (!b.disjoint()) return PTORED_ERR_OVERLAP;
+    if (p.cols == 0 || (dx.data == nullptr && !sums)) return PTORED_OK;
+
+    LayerGradArgs a{};
+    a.rows = p.rows;
+    a.cols = (int32_t)p.cols;
+    a.dz = mat(dz, es);
+    a.dxo = mat(dx_out, es);
+    a.x = mat(x_out, es);
+    a.dx = mat(dx, es);
+    a.w = static_cast<const char*>(p.weight);
+    a.mean = mean;
+    a.rstd = rstd;
+    a.ws = sums ? static_cast<float*>(workspace) : nullptr;
+    a.dw = static_cast<char*>(dweight);
+    a.db = static_cast<char*>(dbias);
+    a.chunks = chunks;
+    a.ws_pitch = pitch_of(p.cols);
+    a.w_f32 = p.weight_dtype == PTORED_F32;
+    a.inv_cols = 1.0f / (float)p.cols;
+    return status_of(PTORED_BY_TYPE(layer_grad, p.dtype, a, stream));
+}
+
+extern "C" int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, ptored_rows w_gate,
+                                ptored_rows w_up, ptored_rows y, ptored_rows gate, ptored_rows up,
+                                hipStream_t stream) {
+    if (!ffn_valid(params) || x.data == nullptr || w_gate.data == nullptr || w_up.data == nullptr ||
+        y.data == nullptr)
+        return PTORED_ERR_INVALID_ARG;
+    const ptored_ffn_params& p = *params;
+    const int es = esize_of(p.dtype);
+    Buffers b;
+    if (!b.rows(x.data, p.rows, p.cols, x.ld, es, false, false) ||
+        !b.rows(w_gate.data, p.wide, p.cols, w_gate.ld, es, false, false) ||
+        !b.rows(w_up.data, p.wide, p.cols, w_up.ld, es, false, false) ||
+        !b.rows(y.data, p.rows, p.wide, y.ld, es, true, false) ||
+        !b.rows(gate.data, p.rows, p.wide, gate.ld, es, true, false) ||
+        !b.rows(up.data, p.rows, p.wide, up.ld, es, true, false))
+        return PTORED_ERR_INVALID_ARG;
+    if (!ffn_supported(p) || !pitch_supported(x, p.rows, es) || !pitch_supported(w_gate, p.wide, es) ||
+        !pitch_supported(w_up, p.wide, es))
+        return PTORED_ERR_UNSUPPORTED;
+    const bool direct = direct_of(x, p.rows, p.cols, es) && direct_of(w_gate, p.wide, p.cols, es) &&
+                        direct_of(w_up, p.wide, p.cols, es);
+    const ProductShape s = product_shape(kForward, p.rows, p.wide, p.cols, 1, p.dtype, direct);
+    if (!launchable(s, 1)) return PTORED_ERR_UNSUPPORTED;
+    if (!b.aligned()) return PTORED_ERR_INVALID_ARG;
+    if (!b.disjoint()) return PTORED_ERR_OVERLAP;
+    if (p.rows == 0 || p.wide == 0) return PTORED_OK;
+
+    ProductArgs a{};
+    set_a(a, 0, x, es);
+    set_b(a, 0, w_gate, es);
+    set_b(a, 1, w_up, es);
+    a.m = p.rows;
+    a.n = p.wide;
+    a.k = p.cols;
+    a.out[0] = mat(y, es);
+    a.gate = mat(gate, es);
+    a.up = mat(up, es);
+    a.outs = 1;
+    a.activation = p.activation;
+    set_shape(a, s, direct);
+    return status_of(PTORED_BY_TYPE(product_forward, p.dtype, a, stream));
+}
+
+extern "C" int ptored_gated_ffn_backward_workspace(int64_t rows, int64_t cols, int64_t wide,
+                                                   int dtype, int64_t* bytes) {
+    if (bytes == nullptr || !shape_ok(rows, cols) || !shape_ok(rows, wide) || !shape_ok(wide, cols))
+        return PTORED_ERR_INVALID_ARG;
+    if (!float_type(dtype)) return PTORED_ERR_UNSUPPORTED;
+    int64_t most = 0;  // of any alignment and any choice of gradients; products take turns
+    for (const bool direct : {false, true}) {
+        most = std::max(most, product_workspace(product_shape(kInput, rows, cols, wide, 1, dtype, direct),
+                                                rows, cols, 1));
+        for (const int outs : {1, 2})
+            most = std::max(most, product_workspace(product_shape(kWeight, wide, cols, rows, outs, dtype,
+                                                                  direct), wide, cols, outs));
+    }
+    *bytes = most;
+    return PTORED_OK;
+}
+
+extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
+                                         const ptored_ffn_grad_io* io, hipStream_t stream) {
+    if (!ffn_valid(params) || io == nullptr || io->dy.data == nullptr || io->gate.data == nullptr ||
+        io->up.data == nullptr || io->dgate.data == nullptr || io->dup.data == nullptr)
+        return PTORED_ERR_INVALID_ARG;
+    const ptored_ffn_params& p = *params;
+    const bool input = io->dx.data != nullptr;
+    const int outs = (io->dw_gate.data != nullptr) + (io->dw_up.data != nullptr);
+    if ((outs > 0 && io->x.data == nullptr) ||
+        (input && (io->w_gate.data == nullptr || io->w_up.data == nullptr)))
+        return PTORED_ERR_INVALID_ARG;
+    const int es = esize_of(p.dtype), ws = esize_of(io->dw_dtype);
+    // what no product reads is not looked at
+    const ptored_rows none{nullptr, 0};
+    const ptored_rows x = outs > 0 ? io->x : none;
+    const ptored_rows wg = input ? io->w_gate : none, wu = input ? io->w_up : none;
+    Buffers b;
+    if (!b.rows(io->dy.data, p.rows, p.wide, io->dy.ld, es, false) ||
+        !b.rows(io->gate.data, p.rows, p.wide, io->gate.ld, es, false) ||
+        !b.rows(io->up.data, p.rows, p.wide, io->up.ld, es, false) ||
+        !b.rows(io->dgate.data, p.rows, p.wide, io->dgate.ld, es, true) ||
+        !b.rows(io->dup.data, p.rows, p.wide, io->dup.ld, es, true) ||
+        !b.rows(x.data, p.rows, p.cols, x.ld, es, false, false) ||
+        !b.rows(wg.data, p.wide, p.cols, wg.ld, es, false, false) ||
+        !b.rows(wu.data, p.wide, p.cols, wu.ld, es, false, false) ||
+        !b.rows(io->dx.data, p.rows, p.cols, io->dx.ld, es, true, false) ||
+        !b.rows(io->dw_gate.data, p.wide, p.cols, io->dw_gate.ld, ws, true, false) ||
+        !b.rows(io->dw_up.data, p.wide, p.cols, io->dw_up.ld, ws, true, false))
+        return PTORED_ERR_INVALID_ARG;
+    if (!ffn_supported(p) || (outs > 0 && io->dw_dtype != PTORED_F32 && io->dw_dtype != p.dtype))
+        return PTORED_ERR_UNSUPPORTED;
+    if (!pitch_supported(io->dgate, p.rows, es) || !pitch_supported(io->dup, p.rows, es) ||
+        !pitch_supported(x, p.rows, es) || !pitch_supported(wg, p.wide, es) ||
+        !pitch_supported(wu, p.wide, es))
+        return PTORED_ERR_UNSUPPORTED;
+    const bool whole = direct_of(io->dgate, p.rows, p.wide, es) && direct_of(io->dup, p.rows, p.wide, es);
+    const bool direct_in = whole && direct_of(wg, p.wide, p.cols, es) && direct_of(wu, p.wide, p.cols, es);
+    const bool direct_w = whole && direct_of(x, p.rows, p.cols, es);
+    const ProductShape si = product_shape(kInput, p.rows, p.cols, p.wide, 1, p.dtype, direct_in);
+    const ProductShape sw =
+        product_shape(kWeight, p.wide, p.cols, p.rows, std::max(outs, 1), p.dtype, direct_w);
+    if ((input && !launchable(si, 1)) || (outs > 0 && !launchable(sw, outs)))
+        return PTORED_ERR_UNSUPPORTED;
+    const int64_t need = std::max(input ? product_workspace(si, p.rows, p.cols, 1) : 0,
+                                  outs > 0 ? product_workspace(sw, p.wide, p.cols, outs) : 0);
+    if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
+        return PTORED_ERR_INVALID_ARG;
+    if (need > 0) b.vec(io->workspace, need, 16, true);
+    if (!b.aligned()) return PTORED_ERR_INVALID_ARG;
+    if (!b.disjoint()) return PTORED_ERR_OVERLAP;
+
+    if (p.rows > 0 && p.wide > 0) {
+        const SlopeArgs a{mat(io->dy, es), mat(io->gate, es), mat(io->up, es), mat(io->dgate, es),
+                          mat(io->dup, es), p.rows, p.wide, p.activation};
+        const int rc = PTORED_BY_TYPE(product_slope, p.dtype, a, stream);
+        if (rc != ptored::block::kOk) return status_of(rc);
+    }
+    if (input && p.rows > 0 && p.cols > 0) {
+        ProductArgs a{};
+        set_a(a, 0, io->dgate, es);
+        set_a(a, 1, io->dup, es);
+        set_b(a, 0, wg, es);
+        set_b(a, 1, wu, es);
+        a.m = p.rows;
+        a.n = p.cols;
+        a.k = p.wide;
+        a.out[0] = mat(io->dx, es);
+        a.outs = 1;
+        a.out_f32 = p.dtype == PTORED_F32;
+        a.ws = static_cast<float*>(io->workspace);
+        a.ws_ld = pitch_of(p.cols);
+        set_shape(a, si, direct_in);
+        const int rc = PTORED_BY_TYPE(product_input, p.dtype, a, stream);
+        if (rc != ptored::block::kOk) return status_of(rc);
+    }
+    if (outs > 0 && p.wide > 0 && p.cols > 0 && !(p.rows == 0 && io->accumulate)) {
+        ProductArgs a{};
+        int n = 0;
+        for (int i = 0; i < 2; ++i) {
+            const ptored_rows& dw = i == 0 ? io->dw_gate : io->dw_up;
+            if (dw.data == nullptr) continue;
+            set_a(a, n, i == 0 ? io->dgate : io->dup, es);
+            a.out[n++] = mat(dw, ws);
+        }
+        set_b(a, 0, x, es);
+        a.m = p.wide;
+        a.n = p.cols;
+        a.k = p.rows;
+        a.outs = outs;
+        a.out_f32 = io->dw_dtype == PTORED_F32;
+        a.accumulate = io->accumulate != 0;
+        a.ws = static_cast<float*>(io->workspace);
+        a.ws_ld = pitch_of(p.cols);
+        set_shape(a, sw, direct_w);
+        const int rc = PTORED_BY_TYPE(product_weight, p.dtype, a, stream);
+        if (rc != ptored::block::kOk) return status_of(rc);
+    }
+    return PTORED_OK;
+}
+
+extern "C" int ptored_grad_norm_workspace(const ptored_grad* grads, int64_t count, int64_t* bytes) {
+    if (bytes == nullptr || count < 0 || (count > 0 && grads == nullptr)) return PTORED_ERR_INVALID_ARG;
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!shape_ok(grads[i].rows, grads[i].cols)) return PTORED_ERR_INVALID_ARG;
+        total += grads[i].rows * grads[i].cols;
+        if (total > ptored::block::kMaxElems) return PTORED_ERR_INVALID_ARG;
+    }
+    *bytes = all_groups(grads, count, grad_chunk(grads, count)) * 8;
+    return PTORED_OK;
+}
+
+extern "C" int ptored_grad_norm(const ptored_grad* grads, int64_t count, float* norm, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream) {
+    const int st = grads_checked(grads, count, false, true, norm, workspace, workspace_bytes);
+    if (st != PTORED_OK) return st;
+    GradList a{};
+    int rc = run_sums(grads, count, grad_chunk(grads, count), a, static_cast<double*>(workspace), stream);
+    if (rc != ptored::block::kOk) return status_of(rc);
+    a.norm = norm;
+    return status_of(grad_join(a, stream));
+}
+
+extern "C" int ptored_grad_scale(const ptored_grad* grads, int64_t count, const float* norm,
+                                 float max_norm, hipStream_t stream) {
+    if (!(max_norm >= 0.0f)) return PTORED_ERR_INVALID_ARG;
+    const int st = grads_checked(grads, count, true, false, norm, nullptr, 0);
+    if (st != PTORED_OK) return st;
+    GradList a{};
+    a.norm = const_cast<float*>(norm);  // read only: no sums are given
+    a.max_norm = max_norm;
+    return status_of(each_launch(grads, count, grad_chunk(grads, count), a,
+                                 [&](GradList& l) { return grad_scale(l, stream); }));
+}
+
+extern "C" int ptored_grad_clip(const ptored_grad* grads, int64_t count, float max_norm, float* norm,
+                                void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!(max_norm >= 0.0f)) return PTORED_ERR_INVALID_ARG;
+    const int st = grads_checked(grads, count, true, true, norm, workspace, workspace_bytes);
+    if (st != PTORED_OK) return st;
+    const int64_t chunk = grad_chunk(grads, count);
+    GradList a{};
+    int rc = run_sums(grads, count, chunk, a, static_cast<double*>(workspace), stream);
+    if (rc != ptored::block::kOk) return status_of(rc);
+    a.norm = norm;
+    a.max_norm = max_norm;
+    rc = grad_join(a, stream);
+    if (rc != ptored::block::kOk) return status_of(rc);
+    a.all = nullptr;
+    return status_of(each_launch(grads, count, chunk, a, [&](GradList& l) { return grad_scale(l, stream); }));
+}

@@ -1,0 +1,123 @@
+// step_plan.h -- what the host code hands to the kernels of the step's
+// operators, and the launch functions (one per element type where they depend
+// on one, each in a unit of its own, step_ops.hip).
+#pragma once
+
+#include "block/block_plan.h"
+#include "ptored_step.h"
+
+namespace ptored {
+namespace step {
+
+using block::kFailed;
+using block::kOk;
+using block::Mat;
+
+struct LayerNormArgs {
+    const char* part[PTORED_MAX_RANKS];
+    int64_t part_ld;  // bytes
+    int64_t rows;
+    Mat x, x_out, z;
+    const char *w, *b;
+    float *mean, *rstd;
+    int32_t nranks, cols, w_f32;
+    float eps, inv_cols;
+};
+
+struct LayerGradArgs {
+    int64_t rows;
+    Mat dz, dxo, x, dx;
+    const char* w;
+    const float *mean, *rstd;
+    float* ws;         // partial sums: [chunk][dw, db][ws_pitch]
+    char *dw, *db;
+    int64_t chunks;    // workgroups; chunk c takes rows c, c + chunks, ...
+    int64_t ws_pitch;  // the columns, rounded up to whole vectors of 4
+    int32_t cols, w_f32;
+    float inv_cols;
+};
+
+// Layouts of a product's operands: the sum's index along rows (k consecutive)
+// or across them (k is the row).
+enum : int { kAlong = 0, kAcross = 1 };
+
+// The products of the feed-forward block.
+enum : int {
+    kForward = 0,  // f(x Wg^T) (x Wu^T): both operands along
+    kInput = 1,    // dg Wg + du Wu: dg along, weights across
+    kWeight = 2    // dg^T x and du^T x: both across
+};
+
+struct ProductArgs {
+    // kForward: x; Wg, Wu.  kInput: dg, du; Wg, Wu.  kWeight: dg, du; x.
+    const char *a[2], *b[2];
+    int64_t a_ld[2], b_ld[2];  // bytes
+    int64_t m, n, k;           // kForward: n features of each weight; kInput: k of each pair
+    Mat out[2];                // kForward: y; kInput: dx; kWeight: dWg, dWu
+    Mat gate, up;              // kForward: what is kept
+    float* ws;                 // [split][out][m][ws_ld] partial sums when splits > 1
+    int64_t ws_ld;             // n, rounded up to whole vectors of 4
+    int64_t steps_per_split;
+    int32_t tiles_m, tiles_n, splits;
+    int32_t outs;        // kWeight: products, 1 or 2
+    int32_t out_f32, accumulate, activation;
+    int32_t shape;       // a tile of kShapes
+    int32_t direct;      // every row and column range is whole aligned chunks
+};
+
+// Tiles of the products.
+enum : int {
+    kTile128 = 0,  // 128 x 128, 4 waves
+    kTile256 = 1   // 256 x 256, 8 waves; 16-bit types, aligned
+};
+constexpr int kStepBytes = 128;  // of each row along k that a step takes
+
+struct SlopeArgs {  // dg and du
+    Mat dy, gate, up, dgate, dup;
+    int64_t rows, cols;
+    int32_t activation;
+};
+
+// Gradients of one launch.  An entry is rows x cols elements, cut into chunks
+// of `chunk` elements: of a row, or of whole rows where several fit.
+constexpr int kGradEntries = 72;
+struct GradEntry {
+    const char* data;
+    char* out;
+    int64_t cols;
+    int32_t rows;
+    int32_t ld, out_ld;  // elements
+    int32_t first;       // the entry's first workgroup in this launch
+    int32_t type;        // dtype | out_dtype << 8
+    int32_t chunks;      // along a row, or 0: `group` whole rows a chunk
+};
+struct GradList {
+    GradEntry e[kGradEntries];
+    int32_t count, groups;  // entries, workgroups
+    int64_t chunk;
+    double* sums;           // this launch's place among the partial sums
+    const double* all;      // every partial sum, or null: `norm` is given
+    int32_t all_count;
+    float* norm;
+    float max_norm;
+};
+
+int grad_sums(const GradList&, hipStream_t);
+int grad_join(const GradList&, hipStream_t);
+int grad_scale(const GradList&, hipStream_t);
+
+// T = f32, bf16, f16
+#define PTORED_STEP_LAUNCHES(T)                              \
+    int layer_norm_##T(const LayerNormArgs&, hipStream_t);   \
+    int layer_grad_##T(const LayerGradArgs&, hipStream_t);   \
+    int product_forward_##T(const ProductArgs&, hipStream_t);\
+    int product_input_##T(const ProductArgs&, hipStream_t);  \
+    int product_weight_##T(const ProductArgs&, hipStream_t); \
+    int product_slope_##T(const SlopeArgs&, hipStream_t);
+PTORED_STEP_LAUNCHES(f32)
+PTORED_STEP_LAUNCHES(bf16)
+PTORED_STEP_LAUNCHES(f16)
+#undef PTORED_STEP_LAUNCHES
+
+}  // namespace step
+}  // namespace ptored

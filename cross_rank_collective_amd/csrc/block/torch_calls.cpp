@@ -539,14 +539,18 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// grads, norm, max_norm, outs, stream
+// grads, norm, max_norm, outs, workspace, stream
 PyObject* grad_scale(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        want(n, 5);
+        want(n, 6);
         const Gradients v(a[0], a[1], a[3]);
+        const float most = number(a[2]);
+        const at::Tensor ws = v.workspace(a[4], a[5]);
         return v.wrote_outs(ptored_grad_scale(v.list.data(), (int64_t)v.list.size(),
-                                              static_cast<const float*>(v.norm.data_ptr()),
-                                              number(a[2]), v.g.stream(a[4])),
+                                              static_cast<const float*>(v.norm.data_ptr()), most,
+                                              ws.defined() ? ws.data_ptr() : nullptr,
+                                              ws.defined() ? (int64_t)ws.nbytes() : 0,
+                                              v.g.stream(a[5])),
                             a[0]);
     });
 }

@@ -131,32 +131,33 @@ bool grad_shape_ok(const ptored_grad& g, bool scaled) {
 bool grad_supported(const ptored_grad& g, bool scaled) {
     if (!float_type(g.dtype)) return false;
     if (scaled && g.out_dtype != PTORED_F32 && g.out_dtype != g.dtype) return false;
-    return g.rows <= 1 || (g.rows <= kInt && g.ld <= kInt && (!scaled || g.out_ld <= kInt));
+    if (g.rows == 0 || g.cols == 0) return true;
+    if (g.rows == 1) return g.cols < kGradMost;
+    return g.rows <= kInt && g.ld <= kGradPitch && (!scaled || g.out_ld <= kGradPitch);
 }
 int64_t span_of(const ptored_grad& g, int64_t ld, int es) {
     return (g.rows == 1 ? g.cols : (g.rows - 1) * ld + g.cols) * es;
 }
 
-// Elements of a workgroup's chunk: 2048 workgroups, 8 a compute unit, for
-// gradients that fill the chip; smaller ones in chunks of 4096 elements.
-int64_t grad_chunk(const ptored_grad* grads, int64_t count) {
-    int64_t total = 0;
-    for (int64_t i = 0; i < count; ++i) total += grads[i].rows * grads[i].cols;
-    return std::min<int64_t>(std::max<int64_t>(4096, ((total + 2047) / 2048 + 1023) / 1024 * 1024),
-                             int64_t(1) << 30);
+int64_t chunks_of(const ptored_grad& g) {
+    return g.rows == 0 || g.cols == 0 ? 0 : grad_chunks(g.rows, g.cols, g.dtype);
 }
-// Workgroups of one gradient.
-int64_t grad_groups(const ptored_grad& g, int64_t chunk) {
-    if (g.rows == 0 || g.cols == 0) return 0;
-    if (g.rows == 1 || g.cols > chunk / 2) return g.rows * ((g.cols + chunk - 1) / chunk);
-    const int64_t group = chunk / g.cols;
-    return (g.rows + group - 1) / group;
-}
-int64_t all_groups(const ptored_grad* grads, int64_t count, int64_t chunk) {
+int64_t all_chunks(const ptored_grad* grads, int64_t count) {
     int64_t n = 0;
-    for (int64_t i = 0; i < count; ++i) n += grad_groups(grads[i], chunk);
+    // (one of an unknown type is refused before its chunks matter)
+    for (int64_t i = 0; i < count; ++i) n += chunks_of(grads[i]);
     return n;
 }
+
+// The workspace: the table of more gradients than a launch's arguments hold,
+// then the partial sums.
+int64_t grad_table_bytes(const ptored_grad* grads, int64_t count) {
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) n += grads[i].rows > 0 && grads[i].cols > 0;
+    return n > kGradEntries ? n * (int64_t)sizeof(GradEntry) : 0;
+}
+
+int64_t groups_of(int64_t chunks) { return std::min<int64_t>(chunks, kGradGroups); }
 
 struct Span {
     uintptr_t begin, end;
@@ -194,7 +195,7 @@ Span span(const void* p, int64_t bytes, bool out) {
     return {b, b + (uintptr_t)bytes, out};
 }
 
-// The checks of all three calls.  `sums`: the call needs a workspace.
+// The checks of all three calls.  `sums`: the norm is taken.
 int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sums, const float* norm,
                   const void* workspace, int64_t workspace_bytes) {
     if (count < 0 || count > kInt || (count > 0 && grads == nullptr) || norm == nullptr)
@@ -207,10 +208,11 @@ int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sum
     }
     for (int64_t i = 0; i < count; ++i)
         if (!grad_supported(grads[i], scaled)) return PTORED_ERR_UNSUPPORTED;
-    const int64_t groups = sums ? all_groups(grads, count, grad_chunk(grads, count)) : 0;
-    if (groups > kInt) return PTORED_ERR_UNSUPPORTED;
-    if (groups > 0 && (workspace == nullptr || workspace_bytes < groups * 8 ||
-                       reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+    const int64_t chunks = all_chunks(grads, count);
+    if (chunks > kInt) return PTORED_ERR_UNSUPPORTED;
+    const int64_t need = grad_table_bytes(grads, count) + (sums ? groups_of(chunks) * 8 : 0);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
+                     reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
         return PTORED_ERR_INVALID_ARG;
     bool aligned = reinterpret_cast<uintptr_t>(norm) % 4 == 0;
     for (int64_t i = 0; i < count && aligned; ++i) {
@@ -220,7 +222,7 @@ int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sum
                   (!scaled || reinterpret_cast<uintptr_t>(g.out) % (uintptr_t)esize_of(g.out_dtype) == 0);
     }
     if (!aligned) return PTORED_ERR_INVALID_ARG;
-    const Span more[2] = {span(norm, 4, sums), span(workspace, groups * 8, true)};
+    const Span more[2] = {span(norm, 4, sums), span(workspace, need, true)};
     if (scaled) {
         const int over = grads_overlap(grads, count, more);
         return over < 0 ? PTORED_ERR_HIP : over > 0 ? PTORED_ERR_OVERLAP : PTORED_OK;
@@ -237,46 +239,76 @@ int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sum
     return PTORED_OK;
 }
 
-// Cuts the gradients into launches and calls f(list) for each.  Returns a
-// launch's code.
-template <typename F>
-int each_launch(const ptored_grad* grads, int64_t count, int64_t chunk, GradList& a, F f) {
-    a.count = a.groups = 0;
-    a.chunk = chunk;
-    for (int64_t i = 0; i < count; ++i) {
-        const ptored_grad& g = grads[i];
-        const int64_t groups = grad_groups(g, chunk);
-        if (groups == 0) continue;
-        GradEntry& e = a.e[a.count++];
-        e.data = static_cast<const char*>(g.data);
-        e.out = static_cast<char*>(g.out);
-        e.cols = g.cols;
-        e.rows = (int32_t)g.rows;
-        e.ld = g.rows == 1 ? 0 : (int32_t)g.ld;
-        e.out_ld = g.rows == 1 ? 0 : (int32_t)g.out_ld;
-        e.first = a.groups;
-        e.type = g.dtype | g.out_dtype << 8;
-        e.chunks = g.rows == 1 || g.cols > chunk / 2 ? (int32_t)((g.cols + chunk - 1) / chunk) : 0;
-        a.groups += (int32_t)groups;
-        if (a.count == kGradEntries) {
-            const int rc = f(a);
-            if (rc != kOk) return rc;
-            a.count = a.groups = 0;
-        }
+// An entry's slots in a pack; 0 where they do not fit.
+int packed(const ptored_grad& g, GradPack& p) {
+    const int slots = g.rows == 1 ? 1 : 2, at = p.slots;
+    if (at + slots > kGradSlots) return 0;
+    const uint64_t type = (uint64_t)(g.dtype == g.out_dtype ? g.dtype : g.dtype + 3);
+    p.heads[at / 32] |= 1u << at % 32;
+    p.data[at] = reinterpret_cast<uint64_t>(g.data) | (uint64_t)(g.cols >> 32) << 48 | type << 56 |
+                 (uint64_t)(slots - 1) << 59;
+    p.out[at] = reinterpret_cast<uint64_t>(g.out);
+    p.cols[at] = (uint32_t)g.cols;
+    if (slots == 2) {
+        p.data[at + 1] = (uint64_t)g.rows | (uint64_t)g.ld << 32;
+        p.out[at + 1] = (uint64_t)g.out_ld;
+        p.cols[at + 1] = 0;
     }
-    return a.count > 0 ? f(a) : kOk;
+    p.slots += slots;
+    return slots;
 }
 
-int run_sums(const ptored_grad* grads, int64_t count, int64_t chunk, GradList& a, double* sums,
+// The list of a call, in the arguments or put together in the workspace.
+int list_of(const ptored_grad* grads, int64_t count, void* workspace, GradList& a, hipStream_t stream) {
+    const int64_t bytes = grad_table_bytes(grads, count);
+    GradPack p{};
+    GradEntry* to = p.table = static_cast<GradEntry*>(workspace);
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const ptored_grad& g = grads[i];
+        if (g.rows == 0 || g.cols == 0) continue;
+        if (bytes > 0) {
+            if (packed(g, p) == 0) {
+                const int rc = grad_table(p, stream);
+                if (rc != kOk) return rc;
+                p = GradPack{};
+                p.table = to;
+                p.first = (int32_t)chunks;
+                packed(g, p);
+            }
+            ++to;
+        } else {
+            GradEntry& e = a.e[a.count];
+            e.data = static_cast<const char*>(g.data);
+            e.out = static_cast<char*>(g.out);
+            e.cols = g.cols;
+            e.rows = (int32_t)g.rows;
+            e.ld = g.rows == 1 ? 0 : (int32_t)g.ld;
+            e.out_ld = g.rows == 1 ? 0 : (int32_t)g.out_ld;
+            e.first = (int32_t)chunks;
+            e.type = g.dtype | g.out_dtype << 8;
+        }
+        ++a.count;
+        chunks += chunks_of(g);
+    }
+    if (bytes > 0) {
+        const int rc = grad_table(p, stream);
+        if (rc != kOk) return rc;
+        a.table = static_cast<const GradEntry*>(workspace);
+    }
+    a.chunks = (int32_t)chunks;
+    a.groups = (int32_t)groups_of(chunks);
+    a.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + bytes);
+    return kOk;
+}
+
+// The list and its partial sums.
+int run_sums(const ptored_grad* grads, int64_t count, void* workspace, GradList& a,
              hipStream_t stream) {
-    int64_t done = 0;
-    const int rc = each_launch(grads, count, chunk, a, [&](GradList& l) {
-        l.sums = sums + done;
-        done += l.groups;
-        return grad_sums(l, stream);
-    });
-    a.all = sums;
-    a.all_count = (int32_t)done;
+    int rc = list_of(grads, count, workspace, a, stream);
+    if (rc == kOk && a.groups > 0) rc = grad_sums(a, stream);
+    a.all = a.sums;
+    a.all_count = a.groups;
     return rc;
 }
 
@@ -565,7 +597,7 @@ extern "C" int ptored_grad_norm_workspace(const ptored_grad* grads, int64_t coun
         total += grads[i].rows * grads[i].cols;
         if (total > ptored::block::kMaxElems) return PTORED_ERR_INVALID_ARG;
     }
-    *bytes = all_groups(grads, count, grad_chunk(grads, count)) * 8;
+    *bytes = grad_table_bytes(grads, count) + groups_of(all_chunks(grads, count)) * 8;
     return PTORED_OK;
 }
 
@@ -574,22 +606,24 @@ extern "C" int ptored_grad_norm(const ptored_grad* grads, int64_t count, float* 
     const int st = grads_checked(grads, count, false, true, norm, workspace, workspace_bytes);
     if (st != PTORED_OK) return st;
     GradList a{};
-    int rc = run_sums(grads, count, grad_chunk(grads, count), a, static_cast<double*>(workspace), stream);
+    const int rc = run_sums(grads, count, workspace, a, stream);
     if (rc != ptored::block::kOk) return status_of(rc);
     a.norm = norm;
     return status_of(grad_join(a, stream));
 }
 
 extern "C" int ptored_grad_scale(const ptored_grad* grads, int64_t count, const float* norm,
-                                 float max_norm, hipStream_t stream) {
+                                 float max_norm, void* workspace, int64_t workspace_bytes,
+                                 hipStream_t stream) {
     if (!(max_norm >= 0.0f)) return PTORED_ERR_INVALID_ARG;
-    const int st = grads_checked(grads, count, true, false, norm, nullptr, 0);
+    const int st = grads_checked(grads, count, true, false, norm, workspace, workspace_bytes);
     if (st != PTORED_OK) return st;
     GradList a{};
+    const int rc = list_of(grads, count, workspace, a, stream);
+    if (rc != ptored::block::kOk || a.groups == 0) return status_of(rc);
     a.norm = const_cast<float*>(norm);  // read only: no sums are given
     a.max_norm = max_norm;
-    return status_of(each_launch(grads, count, grad_chunk(grads, count), a,
-                                 [&](GradList& l) { return grad_scale(l, stream); }));
+    return status_of(grad_scale(a, stream));
 }
 
 extern "C" int ptored_grad_clip(const ptored_grad* grads, int64_t count, float max_norm, float* norm,
@@ -597,14 +631,10 @@ extern "C" int ptored_grad_clip(const ptored_grad* grads, int64_t count, float m
     if (!(max_norm >= 0.0f)) return PTORED_ERR_INVALID_ARG;
     const int st = grads_checked(grads, count, true, true, norm, workspace, workspace_bytes);
     if (st != PTORED_OK) return st;
-    const int64_t chunk = grad_chunk(grads, count);
     GradList a{};
-    int rc = run_sums(grads, count, chunk, a, static_cast<double*>(workspace), stream);
+    const int rc = run_sums(grads, count, workspace, a, stream);
     if (rc != ptored::block::kOk) return status_of(rc);
     a.norm = norm;
     a.max_norm = max_norm;
-    rc = grad_join(a, stream);
-    if (rc != ptored::block::kOk) return status_of(rc);
-    a.all = nullptr;
-    return status_of(each_launch(grads, count, chunk, a, [&](GradList& l) { return grad_scale(l, stream); }));
+    return status_of(a.groups > 0 ? grad_scale(a, stream) : grad_join(a, stream));
 }

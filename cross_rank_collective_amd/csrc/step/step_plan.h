@@ -78,30 +78,59 @@ struct SlopeArgs {  // dg and du
     int32_t activation;
 };
 
-// Gradients of one launch.  An entry is rows x cols elements, cut into chunks
-// of `chunk` elements: of a row, or of whole rows where several fit.
-constexpr int kGradEntries = 72;
+// Gradients of a call.  An entry is rows x cols elements, cut into chunks of
+// kGradChunk elements, or of as many slots of 16 bytes where there are several
+// rows (each with its last slot perhaps partly filled).
+constexpr int kGradChunk = 2048;
+constexpr int kGradPerUnit = 8;                   // workgroups at once on a compute unit
+constexpr int kGradGroups = 256 * kGradPerUnit;   // and on the chip
+constexpr int kGradEntries = 72;                  // that a launch's arguments hold
+constexpr int64_t kGradMost = int64_t(1) << 40;   // elements of a gradient of one row
+constexpr int64_t kGradPitch = int64_t(1) << 27;  // and from one row to the next of several
+inline __host__ __device__ int64_t grad_chunks(int64_t rows, int64_t cols, int dtype) {
+    if (rows == 1) return (cols + kGradChunk - 1) / kGradChunk;
+    const int64_t slot = dtype == PTORED_F32 ? 4 : 8, chunk = kGradChunk / slot;
+    return (rows * ((cols + slot - 1) / slot) + chunk - 1) / chunk;
+}
 struct GradEntry {
     const char* data;
     char* out;
     int64_t cols;
     int32_t rows;
     int32_t ld, out_ld;  // elements
-    int32_t first;       // the entry's first workgroup in this launch
+    int32_t first;       // the entry's first chunk
     int32_t type;        // dtype | out_dtype << 8
-    int32_t chunks;      // along a row, or 0: `group` whole rows a chunk
+    int32_t unused;
 };
 struct GradList {
     GradEntry e[kGradEntries];
-    int32_t count, groups;  // entries, workgroups
-    int64_t chunk;
-    double* sums;           // this launch's place among the partial sums
-    const double* all;      // every partial sum, or null: `norm` is given
+    const GradEntry* table;  // all entries in the workspace where they are more, or null
+    int32_t count, chunks;   // entries and chunks of all
+    int32_t groups;          // workgroups
+    double* sums;            // partial sums, one for each workgroup
+    const double* all;       // those to be joined, or null: `norm` is given
     int32_t all_count;
     float* norm;
     float max_norm;
 };
 
+// More entries than that on their way to a table in the workspace, packed: one
+// slot of a single run, two of rows with gaps.
+constexpr int kGradSlots = 192;
+struct GradPack {
+    GradEntry* table;               // where this launch's entries go
+    int32_t first;                  // their first chunk
+    int32_t slots;
+    uint32_t heads[kGradSlots / 32];  // slots that begin an entry
+    // an entry's first slot: address | elements of a row >> 32 << 48 | type << 56
+    // (3 bits, type = dtype + 3 where the output is wider) | 1 << 59 with a
+    // second slot; the second: rows | pitch << 32
+    uint64_t data[kGradSlots];
+    uint64_t out[kGradSlots];   // address; the output's pitch
+    uint32_t cols[kGradSlots];  // elements of a row, low half
+};
+
+int grad_table(const GradPack&, hipStream_t);
 int grad_sums(const GradList&, hipStream_t);
 int grad_join(const GradList&, hipStream_t);
 int grad_scale(const GradList&, hipStream_t);

@@ -68,7 +68,7 @@ def _load() -> ctypes.CDLL:
         lib.ptored_gated_ffn_backward.argtypes = [P(ptored_ffn_params), P(ptored_ffn_grad_io), _vp]
         lib.ptored_gated_ffn_backward_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, P(_i64)]
         lib.ptored_grad_norm.argtypes = [P(ptored_grad), _i64, _vp, _vp, _i64, _vp]
-        lib.ptored_grad_scale.argtypes = [P(ptored_grad), _i64, _vp, _f32, _vp]
+        lib.ptored_grad_scale.argtypes = [P(ptored_grad), _i64, _vp, _f32, _vp, _i64, _vp]
         lib.ptored_grad_clip.argtypes = [P(ptored_grad), _i64, _f32, _vp, _vp, _i64, _vp]
         lib.ptored_grad_norm_workspace.argtypes = [P(ptored_grad), _i64, P(_i64)]
         for name in ("ptored_layer_norm", "ptored_layer_norm_backward",
@@ -122,8 +122,9 @@ def ptored_grad_norm(grads, count: int, norm, workspace, workspace_bytes: int, s
     return _load().ptored_grad_norm(grads, count, norm, workspace, workspace_bytes, stream)
 
 
-def ptored_grad_scale(grads, count: int, norm, max_norm: float, stream: int) -> int:
-    return _load().ptored_grad_scale(grads, count, norm, max_norm, stream)
+def ptored_grad_scale(grads, count: int, norm, max_norm: float, workspace, workspace_bytes: int,
+                      stream: int) -> int:
+    return _load().ptored_grad_scale(grads, count, norm, max_norm, workspace, workspace_bytes, stream)
 
 
 def ptored_grad_clip(grads, count: int, max_norm: float, norm, workspace, workspace_bytes: int,
@@ -465,17 +466,18 @@ def grad_norm(grads, norm, workspace=None, stream=None) -> None:
     K._wrote(norm)
 
 
-def grad_scale(grads, norm, max_norm: float, outs=None, stream=None) -> None:
+def grad_scale(grads, norm, max_norm: float, outs=None, workspace=None, stream=None) -> None:
     """Scales every gradient by c = max_norm / norm where norm > max_norm, 1
     where it is not and NaN where it is NaN, into ``outs`` (of the gradients'
     shapes, each of its gradient's type or float32; default: in place).
 
     ``norm`` is read on the GPU when the kernels run: the gradients' norm, or
     that of all shards after an all-reduce."""
-    if K._native_call("grad_scale", stream, grads, norm, max_norm, outs):
+    if K._native_call("grad_scale", stream, grads, norm, max_norm, outs, workspace):
         return
     g = _Grads(grads, norm, outs)
-    g.run(stream, ptored_grad_scale, g.table, g.count, norm.data_ptr(), max_norm)
+    keep, ptr, nbytes = g.workspace(workspace, stream)
+    g.run(stream, ptored_grad_scale, g.table, g.count, norm.data_ptr(), max_norm, ptr, nbytes)
     K._wrote(*g.outs)
 
 

@@ -159,16 +159,15 @@ int ptored_grad_norm(const ptored_grad* grads, int64_t count, float* norm, void*
  * data exactly (type and pitch too) or overlaps no gradient's data or out.
  */
 int ptored_grad_scale(const ptored_grad* grads, int64_t count, const float* norm, float max_norm,
-                      hipStream_t stream);
+                      void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /* ptored_grad_clip -- both: the norm into norm[0], and the gradients scaled by
  * it as ptored_grad_scale scales them. */
 int ptored_grad_clip(const ptored_grad* grads, int64_t count, float max_norm, float* norm,
                      void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace (16-byte aligned) of ptored_grad_norm and
- * ptored_grad_clip for these gradients (no HIP call; only shapes and types are
- * read). */
+/* Bytes of workspace (16-byte aligned) of each of the three calls for these
+ * gradients (no HIP call; only shapes and types are read). */
 int ptored_grad_norm_workspace(const ptored_grad* grads, int64_t count, int64_t* bytes);
 
 #ifdef __cplusplus

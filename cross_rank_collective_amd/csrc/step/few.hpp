@@ -1,0 +1,212 @@
+// few.hpp -- the gated feed-forward block of few tokens (decoding).
+//
+//     g = x Wg^T,  u = x Wu^T,  y = f(g) u
+//
+// Bound by memory: both weights are read once.  They go from memory straight
+// into the matrix instructions' registers: a lane's 16 bytes of one feature's
+// row are its operand, and the tokens, padded to blocks of 16, are the other
+// one, so that nothing passes through the LDS on the way.  A workgroup takes 16
+// FB features; its W waves take the columns in turn, units of U steps of 64
+// bytes, the next unit's loads in flight while one is multiplied, and add their
+// sums in the LDS at the end, in a fixed order.
+#pragma once
+
+#include "gated.hpp"
+
+namespace ptored {
+namespace step {
+
+using namespace block;
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+// 16 rows of a times 16 rows of b, 64 bytes of each: lane l has 16 bytes of row
+// l % 16 from k = V (l / 16) on.
+template <int DT>
+__device__ __forceinline__ f32x4 multiply16(u32x4 a, u32x4 b, f32x4 acc) {
+    if constexpr (DT == PTORED_BF16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a),
+                                                       __builtin_bit_cast(b8, b), acc, 0, 0, 0);
+    } else if constexpr (DT == PTORED_F16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
+                                                      __builtin_bit_cast(h8, b), acc, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(a[j]), as_f(b[j]), acc, 0, 0, 0);
+        return acc;
+    }
+}
+
+// Tokens in TB blocks of 16.  The columns fill at least one lane's 16 bytes.
+template <int DT, int W, int FB, int TB, int U>
+__global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
+    using E = Elem<DT>;
+    constexpr int ES = E::kBytes, V = E::V, kStep = 64 / ES, kUnit = U * kStep;
+    __shared__ f32x4 part[W][FB * 2 * TB][64];
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t f0 = (int64_t)blockIdx.x * (16 * FB);
+    const int features = (int)min(a.n - f0, (int64_t)(16 * FB)), tokens = (int)a.m, k = (int)a.k;
+    // resources that end with the last row; rows past it are nowhere
+    constexpr int kNone = (int)0x80000000u;
+    const char *pg = a.b[0] + f0 * a.b_ld[0], *pu = a.b[1] + f0 * a.b_ld[1], *px = a.a[0];
+    const int ng = (int)((features - 1) * a.b_ld[0] + k * ES);
+    const int nu = (int)((features - 1) * a.b_ld[1] + k * ES);
+    const int nx = (int)((tokens - 1) * a.a_ld[0] + k * ES);
+    const int col = (lane >> 4) * 16;  // bytes
+    int og[FB], ou[FB], ox[TB];
+#pragma unroll
+    for (int i = 0; i < FB; ++i) {
+        const int row = i * 16 + (lane & 15);
+        og[i] = row < features ? row * (int)a.b_ld[0] + col : kNone;
+        ou[i] = row < features ? row * (int)a.b_ld[1] + col : kNone;
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+        const int row = i * 16 + (lane & 15);
+        ox[i] = row < tokens ? row * (int)a.a_ld[0] + col : kNone;
+    }
+    struct Unit {
+        u32x4 g[U][FB], u[U][FB], x[U][TB];
+    };
+    Unit one, two;
+    const int whole = k / kUnit;  // units without an end in them
+    // Each workgroup begins at a unit of its own: the rows of all of them are a
+    // pitch apart, and at one column they would ask the same memory channels.
+    const int turn = whole > 0 ? (int)((uint32_t)blockIdx.x * W % (uint32_t)whole) : 0;
+    // Past the last unit the resources are empty: zeros without a branch, which
+    // would have every wait count on the way without loads.
+    auto load = [&](Unit& to, int unit) {
+        const bool in = unit < whole;
+        const int from = (unit + turn < whole ? unit + turn : unit + turn - whole) * (U * 64);
+        const rsrc_t rg = row_rsrc(pg, in ? ng : 0), ru = row_rsrc(pu, in ? nu : 0);
+        const rsrc_t rx = row_rsrc(px, in ? nx : 0);
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+#pragma unroll
+            for (int i = 0; i < FB; ++i) {
+                to.g[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rg, og[i], from + s * 64, kPolicyKeep);
+                to.u[s][i] = __builtin_amdgcn_raw_buffer_load_b128(ru, ou[i], from + s * 64, kPolicyKeep);
+            }
+#pragma unroll
+            for (int i = 0; i < TB; ++i)
+                to.x[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, ox[i], from + s * 64, kPolicyKeep);
+        }
+    };
+    f32x4 ag[FB][TB], au[FB][TB];
+#pragma unroll
+    for (int i = 0; i < FB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) ag[i][j] = au[i][j] = (f32x4)(0.0f);
+    auto multiply = [&](const Unit& v) {
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+            for (int i = 0; i < FB; ++i)
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    ag[i][j] = multiply16<DT>(v.g[s][i], v.x[s][j], ag[i][j]);
+                    au[i][j] = multiply16<DT>(v.u[s][i], v.x[s][j], au[i][j]);
+                }
+    };
+    // What the units leave, at most U steps, is taken first, a step by each of the
+    // first waves.  A chunk that the rows' end cuts is loaded so that it ends with
+    // them, and moved.
+    static_assert(U <= W, "a wave for each step that is left");
+    const int rest = whole * kUnit + wave * kStep;
+    u32x4 tg[FB], tu[FB], tx[TB];
+    int by = 0;
+    if (rest < k) {
+        const int at = rest + (lane >> 4) * V;
+        by = at < k ? max(at + V - k, 0) : 0;
+        auto ending = [&](const char* p, int bytes, int off) {
+            return __builtin_amdgcn_raw_buffer_load_b128(
+                row_rsrc(p, bytes), at < k && off != kNone ? off + (rest - by) * ES : kNone, 0, 0);
+        };
+#pragma unroll
+        for (int i = 0; i < FB; ++i) {
+            tg[i] = ending(pg, ng, og[i]);
+            tu[i] = ending(pu, nu, ou[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < TB; ++j) tx[j] = ending(px, nx, ox[j]);
+    }
+    load(one, wave);
+    if (rest < k) {
+#pragma unroll
+        for (int j = 0; j < TB; ++j) tx[j] = shift_down(tx[j], by * ES);
+#pragma unroll
+        for (int i = 0; i < FB; ++i) {
+            tg[i] = shift_down(tg[i], by * ES);
+            tu[i] = shift_down(tu[i], by * ES);
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+                ag[i][j] = multiply16<DT>(tg[i], tx[j], ag[i][j]);
+                au[i][j] = multiply16<DT>(tu[i], tx[j], au[i][j]);
+            }
+        }
+    }
+    for (int unit = wave; unit < whole; unit += 2 * W) {
+        load(two, unit + W);
+        __builtin_amdgcn_sched_barrier(0);  // or the products are moved before the loads
+        multiply(one);
+        __builtin_amdgcn_sched_barrier(0);
+        load(one, unit + 2 * W);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(two);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < FB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+            part[wave][(i * TB + j) * 2][lane] = ag[i][j];
+            part[wave][(i * TB + j) * 2 + 1][lane] = au[i][j];
+        }
+    __syncthreads();
+    // Register r of a lane's sum: feature 4 (lane / 16) + r, token lane % 16.
+    // Consecutive threads take consecutive features.
+    for (int o = (int)threadIdx.x; o < FB * TB * 256; o += W * 64) {
+        const int f = o % (16 * FB), t = o / (16 * FB);
+        const int block = (f / 16 * TB + t / 16) * 2, from = (f % 16 / 4) * 16 + t % 16, r = f % 4;
+        if (f >= features || t >= tokens) continue;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            g += part[w][block][from][r];
+            u += part[w][block + 1][from][r];
+        }
+        const int64_t at = (f0 + f) * ES;
+        E::store1(a.out[0].p + t * a.out[0].ld + at, activation(a.activation, g) * u);
+        if (a.gate.p) E::store1(a.gate.p + t * a.gate.ld + at, g);
+        if (a.up.p) E::store1(a.up.p + t * a.up.ld + at, u);
+    }
+}
+
+template <int DT, int FB, int TB, int U>
+static const void* few_pick(int waves, int& threads) {
+    threads = waves * 64;
+    if constexpr (FB == 1 && TB == 1) {
+        if (waves == 16) return reinterpret_cast<const void*>(few_kernel<DT, 16, FB, TB, U>);
+    }
+    if (waves == 8) return reinterpret_cast<const void*>(few_kernel<DT, 8, FB, TB, U>);
+    return reinterpret_cast<const void*>(few_kernel<DT, 4, FB, TB, U>);
+}
+
+template <int DT>
+int few_launch(const ProductArgs& a, hipStream_t stream) {
+    int threads = 0;
+    const void* k = a.shape == kFew16   ? few_pick<DT, 1, 1, 4>(a.splits, threads)
+                    : a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a.splits, threads)
+                                        : few_pick<DT, 2, 4, 2>(a.splits, threads);
+    void* args[] = {const_cast<ProductArgs*>(&a)};
+    return hipLaunchKernel(k, dim3((uint32_t)a.tiles_n), dim3((uint32_t)threads), args, 0, stream) ==
+                   hipSuccess
+               ? kOk
+               : kFailed;
+}
+
+}  // namespace step
+}  // namespace ptored

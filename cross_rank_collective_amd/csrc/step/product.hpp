@@ -29,7 +29,7 @@
 
 #include <type_traits>
 
-#include "gated.hpp"
+#include "few.hpp"
 
 namespace ptored {
 namespace step {
@@ -38,8 +38,6 @@ using namespace block;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
@@ -222,29 +220,70 @@ __device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 acc) {
     }
 }
 
-// Waits for this wave's loads, then for the other waves.
+// Waits until at most LEFT of this wave's loads are under way and its LDS
+// accesses are done, then for the other waves.
+template <int LEFT>
 __device__ __forceinline__ void landed() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// WM x WN waves of TM x TN blocks of 32 x 32.
-template <int DT, int KIND, int WM, int WN, int TM, int TN, bool DIRECT>
+// Swaps x's upper 32 lanes with y's lower ones.
+__device__ __forceinline__ void swap_halves(float& x, float& y) {
+    const auto v = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(y), false, false);
+    x = as_f(v[0]);
+    y = as_f(v[1]);
+}
+
+// 8 elements to or from `n` (at most 8 count) of a row.
+template <int DT>
+__device__ __forceinline__ void store8(char* p, const float* v, int64_t n) {
+    using E = Elem<DT>;
+    if (n >= 8) {
+        *reinterpret_cast<u32x4_any*>(p) = E::narrow(v);
+        if constexpr (E::V == 4) *reinterpret_cast<u32x4_any*>(p + 16) = E::narrow(v + 4);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) E::store1(p + i * E::kBytes, v[i]);
+}
+template <int DT>
+__device__ __forceinline__ void add8(const char* p, float* v, int64_t n) {
+    using E = Elem<DT>;
+    if (n >= 8) {
+        float w[8];
+        E::widen(*reinterpret_cast<const u32x4_any*>(p), w);
+        if constexpr (E::V == 4) E::widen(*reinterpret_cast<const u32x4_any*>(p + 16), w + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += w[i];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) v[i] += E::load1(p + i * E::kBytes);
+}
+
+// WM x WN waves of TM x TN blocks of 32 x 32; NS buffers in the LDS.
+template <int DT, int KIND, int WM, int WN, int TM, int TN, int NS, bool DIRECT>
 __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
     constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
     constexpr bool kPair = KIND == kForward;  // block j of a wave belongs to weight j
     static_assert(!kPair || TN == 2, "a gate's block and an up's");
+    static_assert(DIRECT || NS == 2, "registers hold one step");
     constexpr int LA = KIND == kWeight ? kAcross : kAlong, LB = KIND == kForward ? kAlong : kAcross;
     using A = Side<DT, LA, BM, kThreads, DIRECT, false>;
     using B = Side<DT, LB, BN, kThreads, DIRECT, kPair>;
     using E = Elem<DT>;
     constexpr int kDepth = A::kDepth, kBytes = A::kBytes + B::kBytes;
+    constexpr int kLoads = DIRECT ? A::kLoads + B::kLoads : 0;  // of a step that barriers wait for
+    static_assert((NS - 1) * kLoads <= 63, "as far as the hardware counts");
     constexpr int kCols = kPair ? BN / 2 : BN;  // of the output
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kBytes];
+    __shared__ __attribute__((aligned(1024))) char lds[NS * kBytes];
 
     const int lane = (int)threadIdx.x & 63;
-    const int wave = (int)(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     // Workgroups go to the 8 dies in turn: each die gets consecutive tiles of
     // the order in which 4 rows of tiles advance together, so that its cache
@@ -266,8 +305,8 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     const int64_t per_pair = a.k > kDepth ? (a.k + kDepth - 1) / kDepth : 1;
     const int64_t all = KIND == kInput ? 2 * per_pair : per_pair;
     const int64_t first = split * a.steps_per_split;
-    const int64_t steps = min(a.steps_per_split, all - first);
-    int pair = 0;
+    const int steps = (int)min(a.steps_per_split, all - first);
+    int pair = 0, loaded = 0;  // the operands' pair; steps asked for
     int64_t left;
     const char *pa, *pb, *pb2;
     auto begin = [&](int64_t step) {
@@ -288,6 +327,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
         sb.init(n0, a.n, a.b_ld[KIND == kWeight ? 0 : pair]);
     };
     auto advance = [&] {
+        ++loaded;
         left -= kDepth;
         if (KIND == kInput && left <= 0 && pair == 0) {
             begin(per_pair);
@@ -301,18 +341,23 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     // extents of the rows that chunks lie in
     const int64_t ea = LA == kAlong ? a.k : a.m, eb = LB == kAlong ? a.k : a.n;
     auto hold = [&] {
+        if (loaded >= steps) return;
         sa.load_held(pa, pa, left, ea);
         sb.load_held(pb, pb2, left, eb);
         advance();
     };
+    // The next step to a buffer.  Past the last one zeros, from nowhere, so that
+    // the loads under way stay countable.
     auto stage = [&](char* buf) {
         if constexpr (DIRECT) {
-            sa.load_direct(pa, pa, left, lds_address(buf));
-            sb.load_direct(pb, pb2, left, lds_address(buf) + A::kBytes);
+            const int64_t n = loaded < steps ? left : 0;
+            sa.load_direct(pa, pa, n, lds_address(buf));
+            sb.load_direct(pb, pb2, n, lds_address(buf) + A::kBytes);
             advance();
         } else {
             sa.store_held(buf);
             sb.store_held(buf + A::kBytes);
+            hold();
         }
     };
 
@@ -331,85 +376,94 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
         for (int j = 0; j < TN; ++j)
             f.b[j] = fragment<DT, LB, BN>(buf + A::kBytes, sub, kPair ? j * WN + wn : wn * TN + j);
     };
+    // transposed: a lane's sums belong to one row of the output
     auto products = [&](const Fragments& f) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = multiply<DT>(f.a[i], f.b[j], acc[i][j]);
+            for (int j = 0; j < TN; ++j) acc[i][j] = multiply<DT>(f.b[j], f.a[i], acc[i][j]);
     };
 
-    char *cur = lds, *next = lds + kBytes;
     begin(first);
     places();
     if (!DIRECT) hold();
-    stage(cur);
-    if (steps > 1) {
-        if (!DIRECT) hold();
-        stage(next);
-    }
-    if (!DIRECT && steps > 2) hold();
-    landed();
+#pragma unroll
+    for (int b = 0; b < NS; ++b) stage(lds + b * kBytes);
+    landed<(NS - 1) * kLoads>();
+    char* cur = lds;
     Fragments even, odd;
     read(cur, 0, even);
-    for (int64_t s = 0; s < steps; ++s) {
+    for (int s = 0; s < steps; ++s) {
         read(cur, 1, odd);
         products(even);
         read(cur, 2, even);
         products(odd);
         read(cur, 3, odd);
         products(even);
-        landed();
-        if (s + 2 < steps) {
-            stage(cur);
-            if (!DIRECT && s + 3 < steps) hold();
-        }
-        read(next, 0, even);  // past the last step: never used
+        landed<(NS - 2) * kLoads>();
+        stage(cur);
+        cur = cur == lds + (NS - 1) * kBytes ? lds : cur + kBytes;
+        read(cur, 0, even);  // past the last step: zeros, never used
         products(odd);
-        char* t = cur;
-        cur = next;
-        next = t;
     }
+    landed<0>();  // the LDS may be another workgroup's after this
 
-    // Register r of a 32 x 32 block is row 8 (r / 4) + 4 (lane / 32) + r % 4,
-    // column lane % 32.
-    const int64_t row0 = m0 + wm * TM * 32 + 4 * (lane >> 5);
-    auto each = [&](auto f) {  // f(row, i, r) of the rows inside
+    // Register r of a block is column 8 (r / 4) + 4 (lane / 32) + r % 4 of row lane
+    // % 32.  With halves swapped a lane has 8 consecutive ones for each of two
+    // half blocks.
+    auto half = [&](f32x16& v, int h, float* to) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t row = row0 + i * 32 + 8 * (r / 4) + r % 4;
-                if (row < a.m) f(row, i, r);
-            }
+        for (int r = 0; r < 4; ++r) {
+            to[r] = v[8 * h + r];
+            to[4 + r] = v[8 * h + 4 + r];
+            swap_halves(to[r], to[4 + r]);
+        }
     };
-    if constexpr (kPair) {
-        const int64_t col = n0 + wn * 32 + (lane & 31);
-        if (col >= a.n) return;
-        each([&](int64_t row, int i, int r) {
-            const float g = acc[i][0][r], u = acc[i][1][r];
-            E::store1(a.out[0].p + row * a.out[0].ld + col * E::kBytes, activation(a.activation, g) * u);
-            if (a.gate.p) E::store1(a.gate.p + row * a.gate.ld + col * E::kBytes, g);
-            if (a.up.p) E::store1(a.up.p + row * a.up.ld + col * E::kBytes, u);
-        });
-    } else {
-        const Mat out = a.out[which];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t col = n0 + (wn * TN + j) * 32 + (lane & 31);
-            if (col >= a.n) continue;
-            each([&](int64_t row, int i, int r) {
-                float v = acc[i][j][r];
-                if (a.splits > 1) {
-                    a.ws[(((int64_t)split * a.outs + which) * a.m + row) * a.ws_ld + col] = v;
-                } else if (a.out_f32) {
-                    float* p = reinterpret_cast<float*>(out.p + row * out.ld) + col;
-                    *p = a.accumulate ? *p + v : v;
-                } else {
-                    char* p = out.p + row * out.ld + col * E::kBytes;
-                    if (a.accumulate) v += E::load1(p);
-                    E::store1(p, v);
+    for (int i = 0; i < TM; ++i) {
+        const int64_t row = m0 + (wm * TM + i) * 32 + (lane & 31);
+        // every lane takes part in the swaps
+        if constexpr (kPair) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t col = n0 + wn * 32 + h * 16 + (lane >> 5) * 8;
+                float g[8], u[8], y[8];
+                half(acc[i][0], h, g);
+                half(acc[i][1], h, u);
+                const int64_t n = row < a.m ? a.n - col : 0;
+                if (n <= 0) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = activation(a.activation, g[e]) * u[e];
+                store8<DT>(a.out[0].p + row * a.out[0].ld + col * E::kBytes, y, n);
+                if (a.gate.p) store8<DT>(a.gate.p + row * a.gate.ld + col * E::kBytes, g, n);
+                if (a.up.p) store8<DT>(a.up.p + row * a.up.ld + col * E::kBytes, u, n);
+            }
+        } else {
+            const Mat out = a.out[which];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t col = n0 + (wn * TN + j) * 32 + h * 16 + (lane >> 5) * 8;
+                    float v[8];
+                    half(acc[i][j], h, v);
+                    const int64_t n = row < a.m ? a.n - col : 0;
+                    if (n <= 0) continue;
+                    if (a.splits > 1) {
+                        // ws_ld holds whole vectors of 4, which the join reads
+                        float* p = a.ws + (((int64_t)split * a.outs + which) * a.m + row) * a.ws_ld + col;
+                        *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
+                        if (n > 4) *reinterpret_cast<f32x4*>(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+                    } else if (a.out_f32) {
+                        char* p = out.p + row * out.ld + col * 4;
+                        if (a.accumulate) add8<PTORED_F32>(p, v, n);
+                        store8<PTORED_F32>(p, v, n);
+                    } else {
+                        char* p = out.p + row * out.ld + col * E::kBytes;
+                        if (a.accumulate) add8<DT>(p, v, n);
+                        store8<DT>(p, v, n);
+                    }
                 }
-            });
         }
     }
 }
@@ -461,14 +515,25 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
     void* args[] = {const_cast<ProductArgs*>(&a)};
     const void* k;
     int threads = 256;
+    if constexpr (KIND == kForward) {
+        if (a.shape >= kFew16) return few_launch<DT>(a, stream);
+    }
     if (a.shape == kTile256) {
         threads = 512;
         if constexpr (DT == PTORED_F32) return kFailed;
-        else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, true>);
-    } else if (a.direct) {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, true>);
+        else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 2, true>);
+    } else if (!a.direct) {
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 2, false>);
     } else {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, false>);
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 2, true>);
+        if constexpr (KIND == kForward) {
+            if (a.shape == kTile64) {
+                threads = 128;
+                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 8, true>);
+            } else if (a.shape == kTile128x32) {
+                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 6, true>);
+            }
+        }
     }
     const uint32_t grid = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)(a.outs * a.splits);
     if (hipLaunchKernel(k, dim3(grid), dim3((uint32_t)threads), args, 0, stream) != hipSuccess)

@@ -72,6 +72,9 @@ struct ProductShape {
 
 constexpr int64_t kMaxTiles = int64_t(1) << 22;
 
+// Tokens of the forward pass that the kernels for few take.
+constexpr int64_t kFewTokens = 64;
+
 // kInput: k of each of the two pairs.
 ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, int dtype,
                            bool direct) {
@@ -84,6 +87,23 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         s.tiles_n = (n + cols - 1) / cols;
         return s.tiles_m * s.tiles_n * outs;
     };
+    if (kind == kForward && direct && m > 16 && m <= 128) {
+        s.shape = m <= 64 ? kTile64 : kTile128x32;
+        s.tiles_m = 1;
+        s.tiles_n = (n + 31) / 32;
+        s.splits = 1;
+        s.steps_per_split = steps;
+        return s;
+    }
+    if (kind == kForward && m <= kFewTokens && k >= 16 / esize_of(dtype)) {
+        s.shape = m <= 16 ? kFew16 : m <= 32 ? kFew32 : kFew64;
+        s.tiles_m = 1;
+        s.tiles_n = s.shape == kFew64 ? (n + 31) / 32 : (n + 15) / 16;
+        const int64_t most = s.shape == kFew16 ? 16 : 8;
+        s.splits = 8;
+        while (s.splits < most && s.splits * s.tiles_n < 2048) s.splits *= 2;
+        return s;
+    }
     s.shape = kTile256;
     if (dtype == PTORED_F32 || !direct || tiles(256) < 160) s.shape = kTile128;
     const int64_t count = tiles(s.shape == kTile256 ? 256 : 128);

@@ -68,7 +68,12 @@ struct ProductArgs {
 // Tiles of the products.
 enum : int {
     kTile128 = 0,  // 128 x 128, 4 waves
-    kTile256 = 1   // 256 x 256, 8 waves; 16-bit types, aligned
+    kTile256 = 1,  // 256 x 256, 8 waves; 16-bit types, aligned
+    kTile64 = 2,   // kForward: 64 tokens x 32 features, 2 waves
+    kTile128x32 = 3,  // kForward: 128 tokens x 32 features, 4 waves
+    kFew16 = 4,    // kForward of up to 16 tokens; `splits` counts a workgroup's waves
+    kFew32 = 5,    // 32 tokens
+    kFew64 = 6     // 64 tokens
 };
 constexpr int kStepBytes = 128;  // of each row along k that a step takes
 

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
             u += part[w][block + 1][from][r];
         }
         const int64_t at = (f0 + f) * ES;
-        E::store1(a.out[0].p + t * a.out[0].ld + at, activation(a.activation, g) * u);
+        E::store1(a.out[0].p + t * a.out[0].ld + at, activation<DT>(a.activation, g) * u);
         if (a.gate.p) E::store1(a.gate.p + t * a.gate.ld + at, g);
         if (a.up.p) E::store1(a.up.p + t * a.up.ld + at, u);
     }

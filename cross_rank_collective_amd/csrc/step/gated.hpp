@@ -19,21 +19,33 @@ using namespace block;
 // f(g) = g s(g) for all three: s is the logistic function, the normal
 // distribution's, or the logistic function of 2 sqrt(2/pi) (g + 0.044715 g^3),
 // since (1 + tanh(t)) / 2 is that of 2t.
-__device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
+//
+// For 16-bit types the logistic function is the hardware's 2^v and reciprocal:
+// off by some (4 + 2 |v|) 2^-24, where the type rounds by 2^-9 or 2^-12, and 3%
+// off the whole forward pass of 2048 tokens (235 -> 226 us).
+template <int DT>
+__device__ __forceinline__ float logistic(float v) {
+    if constexpr (DT == PTORED_F32)
+        return 1.0f / (1.0f + expf(-v));
+    else
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
 __device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(g * -0.70710678f); }
 constexpr float kTanhScale = 1.59576912f;  // 2 sqrt(2/pi)
+template <int DT>
 __device__ __forceinline__ float activation(int which, float g) {
     switch (which) {
-        case PTORED_SILU: return g * logistic(g);
+        case PTORED_SILU: return g * logistic<DT>(g);
         case PTORED_GELU: return g * normal_cdf(g);
-        default: return g * logistic(kTanhScale * (g + 0.044715f * g * g * g));
+        default: return g * logistic<DT>(kTanhScale * (g + 0.044715f * g * g * g));
     }
 }
 // f(g) and f'(g).
+template <int DT>
 __device__ __forceinline__ void with_slope(int which, float g, float& f, float& slope) {
     switch (which) {
         case PTORED_SILU: {
-            const float s = logistic(g);
+            const float s = logistic<DT>(g);
             f = g * s;
             slope = s * (1.0f + g * (1.0f - s));
             break;
@@ -45,7 +57,7 @@ __device__ __forceinline__ void with_slope(int which, float g, float& f, float& 
             break;
         }
         default: {
-            const float s = logistic(kTanhScale * (g + 0.044715f * g * g * g));
+            const float s = logistic<DT>(kTanhScale * (g + 0.044715f * g * g * g));
             const float q = s * (1.0f - s);
             f = g * s;
             // where the logistic function is flat, g^2 may be infinite
@@ -93,7 +105,7 @@ __global__ __launch_bounds__(kSlopeThreads) void slope_kernel(const SlopeArgs a)
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             float f, slope;
-            with_slope(a.activation, g[k], f, slope);
+            with_slope<DT>(a.activation, g[k], f, slope);
             g[k] = dy[k] * u[k] * slope;
             u[k] = dy[k] * f;
         }

@@ -71,19 +71,22 @@ __device__ __forceinline__ u32x4 rsrc_words(const char* base) {
                    0x7FFFFFFFu, 0x00020000u};
 }
 
-// Where rows of 128 bytes keep a chunk: rows of 8, and the even and the odd
-// ones of 16, keep the same chunk in different banks.
-__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ (row >> 3 & 1); }
+// Where rows of STEP bytes keep a chunk: any 8 rows that begin at a multiple of 8,
+// and any 16 at one of 16, keep the same chunk in different banks.
+template <int STEP>
+__device__ __forceinline__ int swizzle(int row) {
+    return (STEP == 128 ? row & 7 : row >> 1 & 3) ^ (row >> 3 & 1);
+}
 
-// A tile's share of one operand: EXT rows of the product, kStepBytes along k.
+// A tile's share of one operand: EXT rows of the product, STEP bytes along k.
 // HALVES: the tile's upper half are a second matrix's rows of the same numbers.
-template <int DT, int LAYOUT, int EXT, int THREADS, bool DIRECT, bool HALVES>
+template <int DT, int LAYOUT, int EXT, int STEP, int THREADS, bool DIRECT, bool HALVES>
 struct Side {
     using E = Elem<DT>;
     static constexpr int ES = E::kBytes, V = 16 / ES;
-    static constexpr int kDepth = kStepBytes / ES;  // k's a step
-    static constexpr int kRow = LAYOUT == kAlong ? kStepBytes : EXT * ES;
-    static constexpr int kBytes = EXT * kStepBytes;
+    static constexpr int kDepth = STEP / ES;  // k's a step
+    static constexpr int kRow = LAYOUT == kAlong ? STEP : EXT * ES;
+    static constexpr int kBytes = EXT * STEP;
     static constexpr int kPerRow = kRow / 16;
     static constexpr int kLoads = kBytes / 16 / THREADS;
     static constexpr int kRows = THREADS / kPerRow;  // LDS rows that one load of all threads covers
@@ -100,7 +103,7 @@ struct Side {
         const int pos = (int)threadIdx.x % kPerRow, row0 = (int)threadIdx.x / kPerRow;
         moved = 0;
         if constexpr (LAYOUT == kAlong) {
-            const int c = pos ^ swizzle(row0);
+            const int c = pos ^ swizzle<STEP>(row0);
             depth = c * V;
 #pragma unroll
             for (int q = 0; q < kLoads; ++q) {
@@ -175,15 +178,15 @@ struct Side {
     }
 };
 
-// A lane's fragment of rows [32 block, 32 block + 32) in quarter `sub` of a step.
-template <int DT, int LAYOUT, int EXT>
+// A lane's fragment of rows [32 block, 32 block + 32) in the `sub`th 32 bytes of a step.
+template <int DT, int LAYOUT, int EXT, int STEP>
 __device__ __forceinline__ u32x4 fragment(const char* buf, int sub, int block) {
-    constexpr int ES = Elem<DT>::kBytes, kRow = LAYOUT == kAlong ? kStepBytes : EXT * ES;
+    constexpr int ES = Elem<DT>::kBytes, kRow = LAYOUT == kAlong ? STEP : EXT * ES;
     const int lane = (int)threadIdx.x & 63, hi = lane >> 5;
     if constexpr (LAYOUT == kAlong) {
         const int row = lane & 31;
         return *reinterpret_cast<const u32x4*>(buf + block * (32 * kRow) + row * kRow +
-                                               ((2 * sub ^ (hi ^ swizzle(row))) << 4));
+                                               ((2 * sub ^ (hi ^ swizzle<STEP>(row))) << 4));
     } else if constexpr (ES == 2) {
         // rows hi 8 + 0-3 and + 4-7 of 16; 64-byte piece c of row t is at c ^ (t & 3)
         const int t = (lane & 15) >> 2;
@@ -265,16 +268,17 @@ __device__ __forceinline__ void add8(const char* p, float* v, int64_t n) {
         if (i < n) v[i] += E::load1(p + i * E::kBytes);
 }
 
-// WM x WN waves of TM x TN blocks of 32 x 32; NS buffers in the LDS.
-template <int DT, int KIND, int WM, int WN, int TM, int TN, int NS, bool DIRECT>
+// WM x WN waves of TM x TN blocks of 32 x 32; NS buffers of STEP bytes along k in
+// the LDS.
+template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, bool DIRECT>
 __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
     constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
-    constexpr bool kPair = KIND == kForward;  // block j of a wave belongs to weight j
-    static_assert(!kPair || TN == 2, "a gate's block and an up's");
+    constexpr bool kPair = KIND == kForward;  // a wave's lower blocks are the gate's, its upper ones the up's
+    static_assert(!kPair || TN % 2 == 0, "as many gate's blocks as up's");
     static_assert(DIRECT || NS == 2, "registers hold one step");
     constexpr int LA = KIND == kWeight ? kAcross : kAlong, LB = KIND == kForward ? kAlong : kAcross;
-    using A = Side<DT, LA, BM, kThreads, DIRECT, false>;
-    using B = Side<DT, LB, BN, kThreads, DIRECT, kPair>;
+    using A = Side<DT, LA, BM, STEP, kThreads, DIRECT, false>;
+    using B = Side<DT, LB, BN, STEP, kThreads, DIRECT, kPair>;
     using E = Elem<DT>;
     constexpr int kDepth = A::kDepth, kBytes = A::kBytes + B::kBytes;
     constexpr int kLoads = DIRECT ? A::kLoads + B::kLoads : 0;  // of a step that barriers wait for
@@ -306,6 +310,10 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     const int64_t all = KIND == kInput ? 2 * per_pair : per_pair;
     const int64_t first = split * a.steps_per_split;
     const int steps = (int)min(a.steps_per_split, all - first);
+    // Tiles of few rows, whose time is that of the weights' way, begin at steps of
+    // their own: rows are a pitch apart, and at one column all tiles would ask the
+    // same memory channels.
+    const int turn = KIND == kForward && BN == 64 ? (int)((uint32_t)id * 5 % (uint32_t)steps) : 0;
     int pair = 0, loaded = 0;  // the operands' pair; steps asked for
     int64_t left;
     const char *pa, *pb, *pb2;
@@ -314,11 +322,11 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
         const int64_t in = KIND == kInput ? step - pair * per_pair : step;
         const int from = KIND == kWeight ? 0 : pair;
         left = a.k - in * kDepth;
-        pa = a.a[pair] + (LA == kAlong ? m0 * a.a_ld[pair] + in * kStepBytes
+        pa = a.a[pair] + (LA == kAlong ? m0 * a.a_ld[pair] + in * STEP
                                        : in * kDepth * a.a_ld[pair] + m0 * E::kBytes);
-        pb = a.b[from] + (LB == kAlong ? n0 * a.b_ld[from] + in * kStepBytes
+        pb = a.b[from] + (LB == kAlong ? n0 * a.b_ld[from] + in * STEP
                                        : in * kDepth * a.b_ld[from] + n0 * E::kBytes);
-        pb2 = kPair ? a.b[1] + n0 * a.b_ld[1] + in * kStepBytes : pb;
+        pb2 = kPair ? a.b[1] + n0 * a.b_ld[1] + in * STEP : pb;
     };
     A sa;
     B sb;
@@ -334,9 +342,13 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
             places();
             return;
         }
-        pa += LA == kAlong ? kStepBytes : kDepth * a.a_ld[pair];
-        pb += LB == kAlong ? kStepBytes : kDepth * a.b_ld[KIND == kWeight ? 0 : pair];
-        pb2 += kStepBytes;
+        if (KIND == kForward && BN == 64 && loaded == steps - turn) {
+            begin(0);
+            return;
+        }
+        pa += LA == kAlong ? STEP : kDepth * a.a_ld[pair];
+        pb += LB == kAlong ? STEP : kDepth * a.b_ld[KIND == kWeight ? 0 : pair];
+        pb2 += STEP;
     };
     // extents of the rows that chunks lie in
     const int64_t ea = LA == kAlong ? a.k : a.m, eb = LB == kAlong ? a.k : a.n;
@@ -346,16 +358,19 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
         sb.load_held(pb, pb2, left, eb);
         advance();
     };
-    // The next step to a buffer.  Past the last one zeros, from nowhere, so that
-    // the loads under way stay countable.
-    auto stage = [&](char* buf) {
+    // The next step to a buffer, in two halves.  Past the last one zeros, from
+    // nowhere, so that the loads under way stay countable.
+    auto stage_a = [&](char* buf) {
+        if constexpr (DIRECT)
+            sa.load_direct(pa, pa, loaded < steps ? left : 0, lds_address(buf));
+        else
+            sa.store_held(buf);
+    };
+    auto stage_b = [&](char* buf) {
         if constexpr (DIRECT) {
-            const int64_t n = loaded < steps ? left : 0;
-            sa.load_direct(pa, pa, n, lds_address(buf));
-            sb.load_direct(pb, pb2, n, lds_address(buf) + A::kBytes);
+            sb.load_direct(pb, pb2, loaded < steps ? left : 0, lds_address(buf) + A::kBytes);
             advance();
         } else {
-            sa.store_held(buf);
             sb.store_held(buf + A::kBytes);
             hold();
         }
@@ -371,10 +386,11 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     };
     auto read = [&](const char* buf, int sub, Fragments& f) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) f.a[i] = fragment<DT, LA, BM>(buf, sub, wm * TM + i);
+        for (int i = 0; i < TM; ++i) f.a[i] = fragment<DT, LA, BM, STEP>(buf, sub, wm * TM + i);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            f.b[j] = fragment<DT, LB, BN>(buf + A::kBytes, sub, kPair ? j * WN + wn : wn * TN + j);
+            f.b[j] = fragment<DT, LB, BN, STEP>(buf + A::kBytes, sub, kPair ? j / (TN / 2) * (WN * TN / 2) + wn * (TN / 2) + j % (TN / 2)
+                                                                : wn * TN + j);
     };
     // transposed: a lane's sums belong to one row of the output
     auto products = [&](const Fragments& f) {
@@ -384,27 +400,58 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
             for (int j = 0; j < TN; ++j) acc[i][j] = multiply<DT>(f.b[j], f.a[i], acc[i][j]);
     };
 
-    begin(first);
+    // The instructions of 32 bytes along k: the next fragments' reads between the first
+    // products.  Left to itself the compiler puts each read right before its use.
+    constexpr int kReadsA = LA == kAlong ? 1 : (E::kBytes == 2 ? 2 : 4);
+    constexpr int kReadsB = LB == kAlong ? 1 : (E::kBytes == 2 ? 2 : 4);
+    constexpr int kProducts = TM * TN * (DT == PTORED_F32 ? 4 : 1);
+    constexpr int kBetween = (TM * kReadsA + TN * kReadsB + kProducts - 1) / kProducts;
+    auto order = [] {
+#pragma unroll
+        for (int i = 0; i < kProducts; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);         // matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x100, kBetween, 0);  // LDS reads
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    begin(first + turn);
     places();
     if (!DIRECT) hold();
 #pragma unroll
-    for (int b = 0; b < NS; ++b) stage(lds + b * kBytes);
+    for (int b = 0; b < NS; ++b) {
+        stage_a(lds + b * kBytes);
+        stage_b(lds + b * kBytes);
+    }
     landed<(NS - 1) * kLoads>();
-    char* cur = lds;
+    char *cur = lds, *last = lds;
     Fragments even, odd;
     read(cur, 0, even);
     for (int s = 0; s < steps; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        // b's half of what the last step began: with a's, the loads of all waves at
+        // once keep the matrix cores waiting (3%)
+        if (DIRECT && s > 0) stage_b(last);
         read(cur, 1, odd);
         products(even);
-        read(cur, 2, even);
-        products(odd);
-        read(cur, 3, odd);
-        products(even);
+        order();
+        if constexpr (STEP == 128) {
+            read(cur, 2, even);
+            products(odd);
+            order();
+            read(cur, 3, odd);
+            products(even);
+            order();
+        }
         landed<(NS - 2) * kLoads>();
-        stage(cur);
+        __builtin_amdgcn_sched_barrier(0);
+        stage_a(cur);
+        if (!DIRECT) stage_b(cur);
+        last = cur;
         cur = cur == lds + (NS - 1) * kBytes ? lds : cur + kBytes;
         read(cur, 0, even);  // past the last step: zeros, never used
         products(odd);
+        order();
     }
     landed<0>();  // the LDS may be another workgroup's after this
 
@@ -425,19 +472,21 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
         // every lane takes part in the swaps
         if constexpr (kPair) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t col = n0 + wn * 32 + h * 16 + (lane >> 5) * 8;
-                float g[8], u[8], y[8];
-                half(acc[i][0], h, g);
-                half(acc[i][1], h, u);
-                const int64_t n = row < a.m ? a.n - col : 0;
-                if (n <= 0) continue;
+            for (int j = 0; j < TN / 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = activation(a.activation, g[e]) * u[e];
-                store8<DT>(a.out[0].p + row * a.out[0].ld + col * E::kBytes, y, n);
-                if (a.gate.p) store8<DT>(a.gate.p + row * a.gate.ld + col * E::kBytes, g, n);
-                if (a.up.p) store8<DT>(a.up.p + row * a.up.ld + col * E::kBytes, u, n);
-            }
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t col = n0 + (wn * (TN / 2) + j) * 32 + h * 16 + (lane >> 5) * 8;
+                    float g[8], u[8], y[8];
+                    half(acc[i][j], h, g);
+                    half(acc[i][TN / 2 + j], h, u);
+                    const int64_t n = row < a.m ? a.n - col : 0;
+                    if (n <= 0) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = activation<DT>(a.activation, g[e]) * u[e];
+                    store8<DT>(a.out[0].p + row * a.out[0].ld + col * E::kBytes, y, n);
+                    if (a.gate.p) store8<DT>(a.gate.p + row * a.gate.ld + col * E::kBytes, g, n);
+                    if (a.up.p) store8<DT>(a.up.p + row * a.up.ld + col * E::kBytes, u, n);
+                }
         } else {
             const Mat out = a.out[which];
 #pragma unroll
@@ -518,22 +567,23 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
     if constexpr (KIND == kForward) {
         if (a.shape >= kFew16) return few_launch<DT>(a, stream);
     }
-    if (a.shape == kTile256) {
+    if (!a.direct) {
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, false>);
+    } else if (a.shape == kTile128) {
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, true>);
+    } else if (a.shape == kTile128Deep) {
+        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 4, true>);
+    } else if (a.shape == kTile256) {
         threads = 512;
         if constexpr (DT == PTORED_F32) return kFailed;
-        else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 2, true>);
-    } else if (!a.direct) {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 2, false>);
+        else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, true>);
+    } else if constexpr (KIND == kForward) {
+        if (a.shape == kTile64) threads = 128;
+        k = a.shape == kTile64
+                ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, true>)
+                : reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, true>);
     } else {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 2, true>);
-        if constexpr (KIND == kForward) {
-            if (a.shape == kTile64) {
-                threads = 128;
-                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 8, true>);
-            } else if (a.shape == kTile128x32) {
-                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 6, true>);
-            }
-        }
+        return kFailed;
     }
     const uint32_t grid = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)(a.outs * a.splits);
     if (hipLaunchKernel(k, dim3(grid), dim3((uint32_t)threads), args, 0, stream) != hipSuccess)

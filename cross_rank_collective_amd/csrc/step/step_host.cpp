@@ -72,46 +72,80 @@ struct ProductShape {
 
 constexpr int64_t kMaxTiles = int64_t(1) << 22;
 
-// Tokens of the forward pass that the kernels for few take.
-constexpr int64_t kFewTokens = 64;
+// A tile's time: base + step us for each of its steps, `slots` tiles at once
+// (fits to 16 to 8192 tokens, 512 to 4096 columns and 640 to 16384 features).
+struct TileCost {
+    int shape;
+    int64_t tile, slots;
+    double base, step;
+};
 
-// kInput: k of each of the two pairs.
+// Tiles and splits of a product; for kInput k is that of each of the two pairs.
+// Splits share a tile's steps among several workgroups, each of which writes
+// its sums in 32 bits, which are read again by a second kernel: 4 us and the
+// bytes at 4 TB/s.  The forward pass has none (the activation needs whole sums).
+//
+// Few tokens, forward (16-bit types; D = 4096, F = 8192, us): 1 token 25 with
+// kFew16, 60 in tiles of 128; 32 tokens 33 with kTile64, 37 with kFew32; 64: 35,
+// 41; 128: 38 with kTile128x32, 68 in tiles of 128.  In 32 bits kTile64's two
+// waves are not enough for its products (64 tokens 149, kFew64 80).
+// Beyond, with tiles of 128, the same with loads further ahead, and 256: 192
+// tokens 70, 48, 103; 512: 85, 103, 107; 1024: 159, 181, 122.
 ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, int dtype,
                            bool direct) {
-    ProductShape s{};
-    const int64_t depth = kStepBytes / esize_of(dtype);
+    static constexpr TileCost k16[] = {{kTile128, 128, 512, 5, 1.1},
+                                       {kTile128Deep, 128, 256, 4, 0.85},
+                                       {kTile256, 256, 256, 8, 1.7}};
+    static constexpr TileCost k32[] = {{kTile128, 128, 512, 5, 3.9}, {kTile128Deep, 128, 256, 4, 2.0}};
+    const int es = esize_of(dtype);
+    const int64_t depth = kStepBytes / es;
     const int64_t steps = std::max<int64_t>(1, (k + depth - 1) / depth) * (kind == kInput ? 2 : 1);
-    auto tiles = [&](int64_t tile) {
-        const int64_t cols = kind == kForward ? tile / 2 : tile;
-        s.tiles_m = (m + tile - 1) / tile;
-        s.tiles_n = (n + cols - 1) / cols;
-        return s.tiles_m * s.tiles_n * outs;
-    };
-    if (kind == kForward && direct && m > 16 && m <= 128) {
+    ProductShape s{};
+    s.splits = 1;
+    s.steps_per_split = steps;
+    if (m == 0 || n == 0) return s;
+    const bool skinny = direct && m > 16 && m <= 128 && (dtype != PTORED_F32 || m > 64);
+    if (kind == kForward && skinny) {
         s.shape = m <= 64 ? kTile64 : kTile128x32;
         s.tiles_m = 1;
         s.tiles_n = (n + 31) / 32;
-        s.splits = 1;
-        s.steps_per_split = steps;
         return s;
     }
-    if (kind == kForward && m <= kFewTokens && k >= 16 / esize_of(dtype)) {
+    if (kind == kForward && m <= 64 && k * es >= 16) {
         s.shape = m <= 16 ? kFew16 : m <= 32 ? kFew32 : kFew64;
         s.tiles_m = 1;
         s.tiles_n = s.shape == kFew64 ? (n + 31) / 32 : (n + 15) / 16;
+        // waves to share the columns: 2048 fill the chip
         const int64_t most = s.shape == kFew16 ? 16 : 8;
         s.splits = 8;
         while (s.splits < most && s.splits * s.tiles_n < 2048) s.splits *= 2;
         return s;
     }
-    s.shape = kTile256;
-    if (dtype == PTORED_F32 || !direct || tiles(256) < 160) s.shape = kTile128;
-    const int64_t count = tiles(s.shape == kTile256 ? 256 : 128);
-    s.splits = 1;
-    if (kind != kForward && s.shape == kTile128 && count > 0 && count <= 256)
-        s.splits = std::max<int64_t>(1, std::min(512 / count, steps / 8));
-    s.steps_per_split = (steps + s.splits - 1) / s.splits;
-    s.splits = (steps + s.steps_per_split - 1) / s.steps_per_split;
+    const TileCost* costs = dtype == PTORED_F32 ? k32 : k16;
+    const int count = !direct ? 1 : dtype == PTORED_F32 ? 2 : 3;
+    const double join = (double)outs * (double)m * (double)n * 8 / 4e6;
+    double best = -1;
+    for (int i = 0; i < count; ++i) {
+        const TileCost& c = costs[i];
+        const int64_t wide = kind == kForward ? c.tile / 2 : c.tile;
+        const int64_t tm = (m + c.tile - 1) / c.tile, tn = (n + wide - 1) / wide, tiles = tm * tn * outs;
+        // more splits than make 2 rounds never pay
+        const int64_t most = kind == kForward ? 1 : std::min((2 * c.slots + tiles - 1) / tiles, (steps + 3) / 4);
+        for (int64_t splits = 1; splits <= std::max<int64_t>(most, 1); ++splits) {
+            const int64_t per = (steps + splits - 1) / splits;
+            if (splits > 1 && (steps + per - 1) / per != splits) continue;  // a split would be empty
+            const double rounds = (double)((tiles * splits + c.slots - 1) / c.slots);
+            const double us = rounds * (c.base + c.step * (double)per) +
+                              (splits > 1 ? 4.0 + join * (double)splits : 0.0);
+            if (best >= 0 && us >= best) continue;
+            best = us;
+            s.shape = c.shape;
+            s.tiles_m = tm;
+            s.tiles_n = tn;
+            s.splits = splits;
+            s.steps_per_split = per;
+        }
+    }
     return s;
 }
 int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs) {

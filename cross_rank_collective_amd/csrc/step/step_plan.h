@@ -67,13 +67,14 @@ struct ProductArgs {
 
 // Tiles of the products.
 enum : int {
-    kTile128 = 0,  // 128 x 128, 4 waves
-    kTile256 = 1,  // 256 x 256, 8 waves; 16-bit types, aligned
-    kTile64 = 2,   // kForward: 64 tokens x 32 features, 2 waves
-    kTile128x32 = 3,  // kForward: 128 tokens x 32 features, 4 waves
-    kFew16 = 4,    // kForward of up to 16 tokens; `splits` counts a workgroup's waves
-    kFew32 = 5,    // 32 tokens
-    kFew64 = 6     // 64 tokens
+    kTile128 = 0,      // 128 x 128, 4 waves, two workgroups a compute unit
+    kTile128Deep = 1,  // the same with loads three steps ahead, one a compute unit; aligned
+    kTile256 = 2,      // 256 x 256, 8 waves; 16-bit types, aligned
+    kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; aligned
+    kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned
+    kFew16 = 5,        // kForward of up to 16 tokens; `splits` counts a workgroup's waves
+    kFew32 = 6,        // 32 tokens
+    kFew64 = 7         // 64 tokens
 };
 constexpr int kStepBytes = 128;  // of each row along k that a step takes
 

@@ -191,16 +191,20 @@ static const void* few_pick(int waves, int& threads) {
     if constexpr (FB == 1 && TB == 1) {
         if (waves == 16) return reinterpret_cast<const void*>(few_kernel<DT, 16, FB, TB, U>);
     }
-    if (waves == 8) return reinterpret_cast<const void*>(few_kernel<DT, 8, FB, TB, U>);
-    return reinterpret_cast<const void*>(few_kernel<DT, 4, FB, TB, U>);
+    return reinterpret_cast<const void*>(few_kernel<DT, 8, FB, TB, U>);
 }
 
 template <int DT>
 int few_launch(const ProductArgs& a, hipStream_t stream) {
     int threads = 0;
-    const void* k = a.shape == kFew16   ? few_pick<DT, 1, 1, 4>(a.splits, threads)
-                    : a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a.splits, threads)
-                                        : few_pick<DT, 2, 4, 2>(a.splits, threads);
+    const void* k;
+    if (a.shape == kFew16)
+        k = few_pick<DT, 1, 1, 4>(a.splits, threads);
+    else if constexpr (DT != PTORED_F32)
+        return kFailed;
+    else
+        k = a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a.splits, threads)
+                              : few_pick<DT, 2, 4, 2>(a.splits, threads);
     void* args[] = {const_cast<ProductArgs*>(&a)};
     return hipLaunchKernel(k, dim3((uint32_t)a.tiles_n), dim3((uint32_t)threads), args, 0, stream) ==
                    hipSuccess

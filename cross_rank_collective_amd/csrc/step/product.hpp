@@ -91,12 +91,21 @@ struct Side {
     static constexpr int kLoads = kBytes / 16 / THREADS;
     static constexpr int kRows = THREADS / kPerRow;  // LDS rows that one load of all threads covers
     static_assert(kRows % (LAYOUT == kAlong ? 16 : 4) == 0, "a thread's rows share their swizzle");
+    // Chunks that end with a row are loaded from up to a chunk before their place.
+    static constexpr int kBack = DIRECT ? 0 : 16;
     static_assert(!HALVES || (LAYOUT == kAlong && kLoads % 2 == 0), "halves are whole loads");
 
     uint32_t off[kLoads];  // bytes from the operand's place, or kNowhere
     int depth;             // kAlong: k of this thread's chunks in a step; kAcross: its first row's
     int moved;             // kAcross: elements from where the chunks are loaded to where they belong
-    u32x4 held[DIRECT ? 1 : kLoads];
+    bool edge;             // some lane of the wave has moved chunks
+
+    // A step's chunks in registers.
+    struct Held {
+        u32x4 w[kLoads];
+        int by;    // kAlong: elements from where the chunks were loaded to where they belong
+        bool cut;  // some lane has such
+    };
 
     // The thread's chunks of the product's rows [first, first + EXT) of `total`.
     __device__ __forceinline__ void init(int64_t first, int64_t total, int64_t ld) {
@@ -108,7 +117,7 @@ struct Side {
 #pragma unroll
             for (int q = 0; q < kLoads; ++q) {
                 const int row = row0 + (HALVES ? q % (kLoads / 2) : q) * kRows;
-                off[q] = first + row < total ? (uint32_t)(row * ld) + c * 16 : kNowhere;
+                off[q] = first + row < total ? (uint32_t)(row * ld) + c * 16 + kBack : kNowhere;
             }
         } else {
             const int c = ((pos >> 2 ^ (row0 & 3)) << 2) | (pos & 3);
@@ -122,59 +131,87 @@ struct Side {
             }
 #pragma unroll
             for (int q = 0; q < kLoads; ++q)
-                // where moved, perhaps before the tile's first column
-                off[q] = in ? (uint32_t)((row0 + q * kRows) * ld + (col - first) * ES) : kNowhere;
+                // (the base lies kBack before the tile's first column, for moved ones)
+                off[q] = in ? (uint32_t)((row0 + q * kRows) * ld + (col - first) * ES + kBack) : kNowhere;
         }
+        edge = __ballot(moved != 0) != 0;
     }
 
-    // Whether chunk q lies past the `left` k's that remain.
-    __device__ __forceinline__ bool past(int q, int64_t left) const {
-        return (LAYOUT == kAlong ? depth : depth + q * kRows) >= left;
+    // Where chunk q of a step is loaded from; `left` k's remain, fewer than a step
+    // takes only in a row's last one.
+    template <bool LAST>
+    __device__ __forceinline__ uint32_t place(int q, int left) const {
+        if (!LAST) return off[q];
+        return (LAYOUT == kAlong ? depth : depth + q * kRows) >= left ? kNowhere : off[q];
     }
     static __device__ __forceinline__ bool second(int q) { return HALVES && q >= kLoads / 2; }
 
-    __device__ __forceinline__ void load_direct(const char* p, const char* p2, int64_t left,
-                                                uint32_t to) const {
+    __device__ __forceinline__ void load_direct(const char* p, const char* p2, int left, uint32_t to) const {
         const u32x4 r = rsrc_words(p), r2 = HALVES ? rsrc_words(p2) : r;
         const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        auto each = [&](auto last) {
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q)
-            load_to_lds(second(q) ? r2 : r, past(q, left) ? kNowhere : off[q],
-                        to + q * (THREADS * 16) + wave * 1024);
+            for (int q = 0; q < kLoads; ++q)
+                load_to_lds(second(q) ? r2 : r, place<decltype(last)::value>(q, left),
+                            to + q * (THREADS * 16) + wave * 1024);
+        };
+        if (left >= kDepth)
+            each(std::false_type{});
+        else
+            each(std::true_type{});
     }
 
     // The same to registers.  `extent`: elements of the rows that chunks lie in.
-    __device__ __forceinline__ void load_held(const char* p, const char* p2, int64_t left,
-                                              int64_t extent) {
+    __device__ __forceinline__ void load_held(Held& h, const char* p, const char* p2, int left,
+                                              int64_t extent) const {
+        const rsrc_t r = row_rsrc(p - kBack, 0x7FFFFFFF), r2 = HALVES ? row_rsrc(p2 - kBack, 0x7FFFFFFF) : r;
+        h.by = 0;
+        h.cut = false;
+        if (__builtin_expect(left >= kDepth && extent >= V, 1)) {
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) {
-            held[q] = (u32x4)(0u);
-            if (off[q] == kNowhere || past(q, left)) continue;
-            const char* at = (second(q) ? p2 : p) + (int64_t)(int32_t)off[q];
-            if (extent < V) {  // the row's only chunk
+            for (int q = 0; q < kLoads; ++q)
+                h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(second(q) ? r2 : r, (int)off[q], 0, 0);
+        } else if (extent >= V) {
+            // of a chunk that the row's end cuts, what ends with the row
+            if (LAYOUT == kAlong && depth < left) h.by = max(depth + V - left, 0);
+            h.cut = LAYOUT == kAlong;
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) {
+                const uint32_t at = place<true>(q, left);
+                h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(
+                    second(q) ? r2 : r, (int)(at == kNowhere ? at : at - h.by * ES), 0, 0);
+            }
+        } else {
+            // the rows' only chunks, element by element
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) {
+                const uint32_t from = place<true>(q, left);
                 uint32_t w[4] = {};
 #pragma unroll
                 for (int i = 0; i < V - 1; ++i) {
-                    if (i >= extent) continue;
+                    const int at = (int)(i >= extent || from == kNowhere ? kNowhere : from + i * ES);
                     if constexpr (ES == 4)
-                        w[i] = reinterpret_cast<const uint32_t*>(at)[i];
+                        w[i] = __builtin_amdgcn_raw_buffer_load_b32(second(q) ? r2 : r, at, 0, 0);
                     else
-                        w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(at)[i] << (16 * (i % 2));
+                        w[i / 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(second(q) ? r2 : r, at, 0, 0)
+                                    << (16 * (i % 2));
                 }
-                held[q] = (u32x4){w[0], w[1], w[2], w[3]};
-            } else {
-                // of a chunk that the row's end cuts, what ends with the row
-                const int by = LAYOUT == kAlong && depth + V > left ? depth + V - (int)left : 0;
-                held[q] = *reinterpret_cast<const u32x4_any*>(at - by * ES);
-                if (LAYOUT == kAlong && by != 0) held[q] = shift_down(held[q], by * ES);
+                h.w[q] = (u32x4){w[0], w[1], w[2], w[3]};
             }
         }
     }
-    __device__ __forceinline__ void store_held(char* to) const {
+    __device__ __forceinline__ void store_held(const Held& h, char* to) const {
+        auto each = [&](auto any) {
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q)
-            *reinterpret_cast<u32x4*>(to + (q * THREADS + (int)threadIdx.x) * 16) =
-                LAYOUT == kAcross && moved != 0 ? shift_down(held[q], moved * ES) : held[q];
+            for (int q = 0; q < kLoads; ++q)
+                *reinterpret_cast<u32x4*>(to + (q * THREADS + (int)threadIdx.x) * 16) =
+                    decltype(any)::value ? shift_down(h.w[q], (LAYOUT == kAlong ? h.by : moved) * ES)
+                                         : h.w[q];
+        };
+        if (__builtin_expect(LAYOUT == kAlong ? h.cut : edge, 0))
+            each(std::true_type{});
+        else
+            each(std::false_type{});
     }
 };
 
@@ -225,9 +262,13 @@ __device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 acc) {
 
 // Waits until at most LEFT of this wave's loads are under way and its LDS
 // accesses are done, then for the other waves.
+// LEFT < 0: loads to registers, which the compiler waits for itself.
 template <int LEFT>
 __device__ __forceinline__ void landed() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
+    if constexpr (LEFT >= 0)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
+    else
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -275,7 +316,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
     constexpr bool kPair = KIND == kForward;  // a wave's lower blocks are the gate's, its upper ones the up's
     static_assert(!kPair || TN % 2 == 0, "as many gate's blocks as up's");
-    static_assert(DIRECT || NS == 2, "registers hold one step");
+    static_assert(DIRECT || NS == 2, "registers hold the steps after the next");
     constexpr int LA = KIND == kWeight ? kAcross : kAlong, LB = KIND == kForward ? kAlong : kAcross;
     using A = Side<DT, LA, BM, STEP, kThreads, DIRECT, false>;
     using B = Side<DT, LB, BN, STEP, kThreads, DIRECT, kPair>;
@@ -305,6 +346,8 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     const int64_t m0 = (int64_t)(band * 4 + in_band % band_rows) * BM;
     const int64_t n0 = (int64_t)(in_band / band_rows) * kCols;
 
+    // k's that a load looks at.
+    auto remain = [&](int64_t left, bool any) { return any ? (int)min(left, (int64_t)1 << 20) : 0; };
     // Where the next load takes its step from.
     const int64_t per_pair = a.k > kDepth ? (a.k + kDepth - 1) / kDepth : 1;
     const int64_t all = KIND == kInput ? 2 * per_pair : per_pair;
@@ -352,29 +395,35 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     };
     // extents of the rows that chunks lie in
     const int64_t ea = LA == kAlong ? a.k : a.m, eb = LB == kAlong ? a.k : a.n;
-    auto hold = [&] {
-        if (loaded >= steps) return;
-        sa.load_held(pa, pa, left, ea);
-        sb.load_held(pb, pb2, left, eb);
+    // Registers: the steps after those in the LDS, two where they fit.
+    constexpr int kSets = DIRECT ? 1 : TM * TN > 4 ? 1 : 2;
+    typename A::Held ha[kSets];
+    typename B::Held hb[kSets];
+    auto hold = [&](auto which_set) {
+        constexpr int set = decltype(which_set)::value;
+        // past the last step the rows are over: zeros from nowhere
+        const int n = remain(left, loaded < steps);
+        sa.load_held(ha[set], pa, pa, n, ea);
+        sb.load_held(hb[set], pb, pb2, n, eb);
         advance();
     };
     // The next step to a buffer, in two halves.  Past the last one zeros, from
     // nowhere, so that the loads under way stay countable.
     auto stage_a = [&](char* buf) {
-        if constexpr (DIRECT)
-            sa.load_direct(pa, pa, loaded < steps ? left : 0, lds_address(buf));
-        else
-            sa.store_held(buf);
+        sa.load_direct(pa, pa, remain(left, loaded < steps), lds_address(buf));
     };
     auto stage_b = [&](char* buf) {
-        if constexpr (DIRECT) {
-            sb.load_direct(pb, pb2, loaded < steps ? left : 0, lds_address(buf) + A::kBytes);
-            advance();
-        } else {
-            sb.store_held(buf + A::kBytes);
-            hold();
-        }
+        sb.load_direct(pb, pb2, remain(left, loaded < steps), lds_address(buf) + A::kBytes);
+        advance();
     };
+    auto stage_held = [&](char* buf, auto which_set) {
+        constexpr int set = decltype(which_set)::value;
+        sa.store_held(ha[set], buf);
+        sb.store_held(hb[set], buf + A::kBytes);
+        hold(which_set);
+    };
+    using Set0 = std::integral_constant<int, 0>;
+    using Set1 = std::integral_constant<int, kSets - 1>;
 
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -417,17 +466,23 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
 
     begin(first + turn);
     places();
-    if (!DIRECT) hold();
+    if constexpr (DIRECT) {
 #pragma unroll
-    for (int b = 0; b < NS; ++b) {
-        stage_a(lds + b * kBytes);
-        stage_b(lds + b * kBytes);
+        for (int b = 0; b < NS; ++b) {
+            stage_a(lds + b * kBytes);
+            stage_b(lds + b * kBytes);
+        }
+    } else {
+        hold(Set0{});
+        if constexpr (kSets == 2) hold(Set1{});
+        stage_held(lds, Set0{});
+        stage_held(lds + kBytes, Set1{});
     }
-    landed<(NS - 1) * kLoads>();
+    landed<DIRECT ? (NS - 1) * kLoads : -1>();
     char *cur = lds, *last = lds;
     Fragments even, odd;
     read(cur, 0, even);
-    for (int s = 0; s < steps; ++s) {
+    auto step = [&](int s, auto set) {
         __builtin_amdgcn_sched_barrier(0);
         // b's half of what the last step began: with a's, the loads of all waves at
         // once keep the matrix cores waiting (3%)
@@ -443,15 +498,25 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
             products(even);
             order();
         }
-        landed<(NS - 2) * kLoads>();
+        landed<DIRECT ? (NS - 2) * kLoads : -1>();
         __builtin_amdgcn_sched_barrier(0);
-        stage_a(cur);
-        if (!DIRECT) stage_b(cur);
+        if constexpr (DIRECT)
+            stage_a(cur);
+        else
+            stage_held(cur, set);
         last = cur;
         cur = cur == lds + (NS - 1) * kBytes ? lds : cur + kBytes;
         read(cur, 0, even);  // past the last step: zeros, never used
         products(odd);
         order();
+    };
+    if constexpr (kSets == 2) {
+        for (int s = 0; s < steps; s += 2) {
+            step(s, Set0{});
+            if (s + 1 < steps) step(s + 1, Set1{});
+        }
+    } else {
+        for (int s = 0; s < steps; ++s) step(s, Set0{});
     }
     landed<0>();  // the LDS may be another workgroup's after this
 
@@ -569,6 +634,12 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
     }
     if (!a.direct) {
         k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, false>);
+        if constexpr (DT != PTORED_F32) {
+            if (a.shape == kTile256) {
+                threads = 512;
+                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, false>);
+            }
+        }
     } else if (a.shape == kTile128) {
         k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, true>);
     } else if (a.shape == kTile128Deep) {

@@ -86,9 +86,11 @@ struct TileCost {
 // bytes at 4 TB/s.  The forward pass has none (the activation needs whole sums).
 //
 // Few tokens, forward (16-bit types; D = 4096, F = 8192, us): 1 token 25 with
-// kFew16, 60 in tiles of 128; 32 tokens 33 with kTile64, 37 with kFew32; 64: 35,
-// 41; 128: 38 with kTile128x32, 68 in tiles of 128.  In 32 bits kTile64's two
-// waves are not enough for its products (64 tokens 149, kFew64 80).
+// kFew16, 60 in tiles of 128; 32 tokens 32 with kTile64, 37 with kFew32; 64: 34,
+// 41; 128: 37 with kTile128x32, 68 in tiles of 128.  Rows that do not start at
+// multiples of 16 bytes (D = 4095, F = 8193): 64 tokens 80 in tiles of 128, 157
+// with kFew64.  In 32 bits kTile64's two waves are not enough for its products (64
+// tokens 149, kFew64 80).
 // Beyond, with tiles of 128, the same with loads further ahead, and 256: 192
 // tokens 70, 48, 103; 512: 85, 103, 107; 1024: 159, 181, 122.
 ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, int dtype,
@@ -111,7 +113,7 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         s.tiles_n = (n + 31) / 32;
         return s;
     }
-    if (kind == kForward && m <= 64 && k * es >= 16) {
+    if (kind == kForward && (m <= 16 || (dtype == PTORED_F32 && m <= 64)) && k * es >= 16) {
         s.shape = m <= 16 ? kFew16 : m <= 32 ? kFew32 : kFew64;
         s.tiles_m = 1;
         s.tiles_n = s.shape == kFew64 ? (n + 31) / 32 : (n + 15) / 16;
@@ -121,8 +123,9 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         while (s.splits < most && s.splits * s.tiles_n < 2048) s.splits *= 2;
         return s;
     }
-    const TileCost* costs = dtype == PTORED_F32 ? k32 : k16;
-    const int count = !direct ? 1 : dtype == PTORED_F32 ? 2 : 3;
+    static constexpr TileCost kHeld16[] = {{kTile128, 128, 512, 5, 1.35}, {kTile256, 256, 256, 8, 2.1}};
+    const TileCost* costs = dtype == PTORED_F32 ? k32 : direct ? k16 : kHeld16;
+    const int count = dtype == PTORED_F32 ? (direct ? 2 : 1) : direct ? 3 : 2;
     const double join = (double)outs * (double)m * (double)n * 8 / 4e6;
     double best = -1;
     for (int i = 0; i < count; ++i) {

@@ -73,8 +73,8 @@ enum : int {
     kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; aligned
     kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned
     kFew16 = 5,        // kForward of up to 16 tokens; `splits` counts a workgroup's waves
-    kFew32 = 6,        // 32 tokens
-    kFew64 = 7         // 64 tokens
+    kFew32 = 6,        // 32 tokens; F32
+    kFew64 = 7         // 64 tokens; F32
 };
 constexpr int kStepBytes = 128;  // of each row along k that a step takes
 

@@ -54,6 +54,7 @@ from .step import (  # noqa: F401
     gated_ffn,
     gated_ffn_backward,
     gated_ffn_backward_workspace,
+    gated_ffn_workspace,
     grad_clip,
     grad_norm,
     grad_scale,
@@ -63,6 +64,7 @@ from .step import (  # noqa: F401
     ptored_gated_ffn,
     ptored_gated_ffn_backward,
     ptored_gated_ffn_backward_workspace,
+    ptored_gated_ffn_workspace,
     ptored_grad_clip,
     ptored_grad_norm,
     ptored_grad_norm_workspace,

@@ -392,18 +392,23 @@ int whole(PyObject* o) {
     return (int)v;
 }
 
-// x, w_gate, w_up, y, activation, gate, up, stream
+// x, w_gate, w_up, y, activation, gate, up, workspace, stream
 PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        want(n, 8);
+        want(n, 9);
         const Group g(tensor(a[0]));
-        const at::Tensor& y = tensor(a[3]);
-        if (y.dim() != 2 || y.size(1) == 0) throw Misfit{};
-        const int64_t wide = y.size(1);
+        const at::Tensor& out = tensor(a[3]);
+        if (out.dim() != 2 || out.size(1) == 0) throw Misfit{};
+        const int64_t wide = out.size(1);
         const ptored_ffn_params p{g.rows, g.cols, wide, g.code, whole(a[4])};
-        return wrote(ptored_gated_ffn(&p, g.mat(a[0]), g.of(a[1], wide, g.cols), g.of(a[2], wide, g.cols),
-                                      g.of(a[3], g.rows, wide), g.of(a[5], g.rows, wide),
-                                      g.of(a[6], g.rows, wide), g.stream(a[7])),
+        const ptored_rows x = g.mat(a[0]), wg = g.of(a[1], wide, g.cols), wu = g.of(a[2], wide, g.cols);
+        const ptored_rows y = g.of(a[3], g.rows, wide), gate = g.of(a[5], g.rows, wide);
+        const ptored_rows up = g.of(a[6], g.rows, wide);
+        int64_t bytes = 0;
+        if (ptored_gated_ffn_workspace(g.rows, g.cols, wide, g.code, &bytes) != PTORED_OK) throw Misfit{};
+        const at::Tensor ws = g.workspace(a[7], a[8], bytes);
+        return wrote(ptored_gated_ffn(&p, x, wg, wu, y, gate, up, ws.defined() ? ws.data_ptr() : nullptr,
+                                      ws.defined() ? (int64_t)ws.nbytes() : 0, g.stream(a[8])),
                      {a[3], a[5], a[6]});
     });
 }

@@ -8,7 +8,8 @@
 // one, so that nothing passes through the LDS on the way.  A workgroup takes 16
 // FB features; its W waves take the columns in turn, units of U steps of 64
 // bytes, the next unit's loads in flight while one is multiplied, and add their
-// sums in the LDS at the end, in a fixed order.
+// sums in the LDS at the end, in a fixed order.  Where few features leave compute
+// units idle, several workgroups share the columns and a second kernel joins them.
 #pragma once
 
 #include "gated.hpp"
@@ -72,7 +73,10 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
         u32x4 g[U][FB], u[U][FB], x[U][TB];
     };
     Unit one, two;
-    const int whole = k / kUnit;  // units without an end in them
+    // units without an end in them; this split's among them
+    const int split = (int)blockIdx.y, units = k / kUnit;
+    const int first = (int)((int64_t)units * split / a.splits);
+    const int whole = (int)((int64_t)units * (split + 1) / a.splits) - first;
     // Each workgroup begins at a unit of its own: the rows of all of them are a
     // pitch apart, and at one column they would ask the same memory channels.
     const int turn = whole > 0 ? (int)((uint32_t)blockIdx.x * W % (uint32_t)whole) : 0;
@@ -80,7 +84,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
     // would have every wait count on the way without loads.
     auto load = [&](Unit& to, int unit) {
         const bool in = unit < whole;
-        const int from = (unit + turn < whole ? unit + turn : unit + turn - whole) * (U * 64);
+        const int from = (first + (unit + turn < whole ? unit + turn : unit + turn - whole)) * (U * 64);
         const rsrc_t rg = row_rsrc(pg, in ? ng : 0), ru = row_rsrc(pu, in ? nu : 0);
         const rsrc_t rx = row_rsrc(px, in ? nx : 0);
 #pragma unroll
@@ -115,7 +119,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
     // first waves.  A chunk that the rows' end cuts is loaded so that it ends with
     // them, and moved.
     static_assert(U <= W, "a wave for each step that is left");
-    const int rest = whole * kUnit + wave * kStep;
+    const int rest = split + 1 == a.splits ? units * kUnit + wave * kStep : k;
     u32x4 tg[FB], tu[FB], tx[TB];
     int by = 0;
     if (rest < k) {
@@ -178,6 +182,12 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
             g += part[w][block][from][r];
             u += part[w][block + 1][from][r];
         }
+        if (a.splits > 1) {
+            float* to = a.ws + ((int64_t)split * 2 * tokens + t) * a.ws_ld + f0 + f;
+            to[0] = g;
+            to[tokens * a.ws_ld] = u;
+            continue;
+        }
         const int64_t at = (f0 + f) * ES;
         E::store1(a.out[0].p + t * a.out[0].ld + at, activation<DT>(a.activation, g) * u);
         if (a.gate.p) E::store1(a.gate.p + t * a.gate.ld + at, g);
@@ -199,15 +209,15 @@ int few_launch(const ProductArgs& a, hipStream_t stream) {
     int threads = 0;
     const void* k;
     if (a.shape == kFew16)
-        k = few_pick<DT, 1, 1, 4>(a.splits, threads);
+        k = few_pick<DT, 1, 1, 4>(a.waves, threads);
     else if constexpr (DT != PTORED_F32)
         return kFailed;
     else
-        k = a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a.splits, threads)
-                              : few_pick<DT, 2, 4, 2>(a.splits, threads);
+        k = a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a.waves, threads)
+                              : few_pick<DT, 2, 4, 2>(a.waves, threads);
     void* args[] = {const_cast<ProductArgs*>(&a)};
-    return hipLaunchKernel(k, dim3((uint32_t)a.tiles_n), dim3((uint32_t)threads), args, 0, stream) ==
-                   hipSuccess
+    return hipLaunchKernel(k, dim3((uint32_t)a.tiles_n, (uint32_t)a.splits), dim3((uint32_t)threads), args, 0,
+                           stream) == hipSuccess
                ? kOk
                : kFailed;
 }

@@ -309,6 +309,12 @@ __device__ __forceinline__ void add8(const char* p, float* v, int64_t n) {
         if (i < n) v[i] += E::load1(p + i * E::kBytes);
 }
 
+// 8 partial sums, `n` of them inside a row of whole vectors of 4.
+__device__ __forceinline__ void store_sums(float* p, const float* v, int64_t n) {
+    *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
+    if (n > 4) *reinterpret_cast<f32x4*>(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+}
+
 // WM x WN waves of TM x TN blocks of 32 x 32; NS buffers of STEP bytes along k in
 // the LDS.
 template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, bool DIRECT>
@@ -386,7 +392,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
             return;
         }
         if (KIND == kForward && BN == 64 && loaded == steps - turn) {
-            begin(0);
+            begin(first);
             return;
         }
         pa += LA == kAlong ? STEP : kDepth * a.a_ld[pair];
@@ -546,6 +552,11 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
                     half(acc[i][TN / 2 + j], h, u);
                     const int64_t n = row < a.m ? a.n - col : 0;
                     if (n <= 0) continue;
+                    if (a.splits > 1) {
+                        store_sums(a.ws + ((int64_t)split * 2 * a.m + row) * a.ws_ld + col, g, n);
+                        store_sums(a.ws + (((int64_t)split * 2 + 1) * a.m + row) * a.ws_ld + col, u, n);
+                        continue;
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = activation<DT>(a.activation, g[e]) * u[e];
                     store8<DT>(a.out[0].p + row * a.out[0].ld + col * E::kBytes, y, n);
@@ -564,10 +575,8 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
                     const int64_t n = row < a.m ? a.n - col : 0;
                     if (n <= 0) continue;
                     if (a.splits > 1) {
-                        // ws_ld holds whole vectors of 4, which the join reads
-                        float* p = a.ws + (((int64_t)split * a.outs + which) * a.m + row) * a.ws_ld + col;
-                        *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
-                        if (n > 4) *reinterpret_cast<f32x4*>(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+                        store_sums(a.ws + (((int64_t)split * a.outs + which) * a.m + row) * a.ws_ld + col,
+                                   v, n);
                     } else if (a.out_f32) {
                         char* p = out.p + row * out.ld + col * 4;
                         if (a.accumulate) add8<PTORED_F32>(p, v, n);
@@ -582,41 +591,55 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     }
 }
 
-// out (+)= the splits' sums.  A workgroup takes 64 times 4 columns of a row, 4
-// threads each for every fourth split, joined in the LDS in a fixed order.
+// out (+)= the splits' sums, or the forward pass's outputs from them.  A workgroup
+// takes 64 times 4 columns of a row, 4 threads each for every fourth split,
+// joined in the LDS in a fixed order.
 constexpr int kJoinLanes = 64, kJoinGroups = 4;
-template <int DT>
+template <int DT, int KIND>
 __global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(const ProductArgs a) {
     using E = Elem<DT>;
-    __shared__ f32x4 part[kJoinGroups][kJoinLanes];
+    constexpr int kSums = KIND == kForward ? 2 : 1;  // g and u
+    __shared__ f32x4 part[kSums][kJoinGroups][kJoinLanes];
     const int lane = (int)threadIdx.x % kJoinLanes, group = (int)threadIdx.x / kJoinLanes;
     const int64_t col = ((int64_t)blockIdx.x * kJoinLanes + lane) * 4;
-    const int64_t rows = a.m * a.outs, step = rows * a.ws_ld;
+    const int64_t rows = a.m * (KIND == kForward ? 1 : a.outs), step = rows * kSums * a.ws_ld;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-        f32x4 sum = (f32x4)(0.0f);
+        f32x4 sum[kSums] = {};
         if (col < a.n) {
             const float* ws = a.ws + row * a.ws_ld + col;
 #pragma unroll 4
             for (int s = group; s < a.splits; s += kJoinGroups)
-                sum += *reinterpret_cast<const f32x4*>(ws + s * step);
+#pragma unroll
+                for (int k = 0; k < kSums; ++k)
+                    sum[k] += *reinterpret_cast<const f32x4*>(ws + s * step + k * rows * a.ws_ld);
         }
-        part[group][lane] = sum;
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) part[k][group][lane] = sum[k];
         __syncthreads();
         if (group == 0 && col < a.n) {
-            const bool second = row >= a.m;
+            const bool second = KIND != kForward && row >= a.m;
+            const int64_t r = second ? row - a.m : row;
             const Mat out = a.out[second];
-            char* at = out.p + (second ? row - a.m : row) * out.ld;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (col + i >= a.n) continue;
-                float v = (part[0][lane][i] + part[1][lane][i]) + (part[2][lane][i] + part[3][lane][i]);
-                if (a.out_f32) {
-                    float* p = reinterpret_cast<float*>(at) + col + i;
-                    *p = a.accumulate ? *p + v : v;
+                float v[kSums];
+#pragma unroll
+                for (int k = 0; k < kSums; ++k)
+                    v[k] = (part[k][0][lane][i] + part[k][1][lane][i]) +
+                           (part[k][2][lane][i] + part[k][3][lane][i]);
+                if constexpr (KIND == kForward) {
+                    const int64_t at = (col + i) * E::kBytes;
+                    E::store1(out.p + r * out.ld + at, activation<DT>(a.activation, v[0]) * v[1]);
+                    if (a.gate.p) E::store1(a.gate.p + r * a.gate.ld + at, v[0]);
+                    if (a.up.p) E::store1(a.up.p + r * a.up.ld + at, v[1]);
+                } else if (a.out_f32) {
+                    float* p = reinterpret_cast<float*>(out.p + r * out.ld) + col + i;
+                    *p = a.accumulate ? *p + v[0] : v[0];
                 } else {
-                    char* p = at + (col + i) * E::kBytes;
-                    if (a.accumulate) v += E::load1(p);
-                    E::store1(p, v);
+                    char* p = out.p + r * out.ld + (col + i) * E::kBytes;
+                    if (a.accumulate) v[0] += E::load1(p);
+                    E::store1(p, v[0]);
                 }
             }
         }
@@ -627,48 +650,53 @@ __global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(c
 template <int DT, int KIND>
 int product_launch(const ProductArgs& a, hipStream_t stream) {
     void* args[] = {const_cast<ProductArgs*>(&a)};
-    const void* k;
+    const void* k = nullptr;
     int threads = 256;
-    if constexpr (KIND == kForward) {
-        if (a.shape >= kFew16) return few_launch<DT>(a, stream);
-    }
-    if (!a.direct) {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, false>);
-        if constexpr (DT != PTORED_F32) {
-            if (a.shape == kTile256) {
-                threads = 512;
-                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, false>);
-            }
-        }
-    } else if (a.shape == kTile128) {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, true>);
-    } else if (a.shape == kTile128Deep) {
-        k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 4, true>);
-    } else if (a.shape == kTile256) {
-        threads = 512;
-        if constexpr (DT == PTORED_F32) return kFailed;
-        else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, true>);
-    } else if constexpr (KIND == kForward) {
-        if (a.shape == kTile64) threads = 128;
-        k = a.shape == kTile64
-                ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, true>)
-                : reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, true>);
+    if (a.shape >= kFew16) {
+        if constexpr (KIND != kForward) return kFailed;
+        const int rc = few_launch<DT>(a, stream);
+        if (rc != kOk) return rc;
     } else {
-        return kFailed;
-    }
-    const uint32_t grid = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)(a.outs * a.splits);
-    if (hipLaunchKernel(k, dim3(grid), dim3((uint32_t)threads), args, 0, stream) != hipSuccess)
-        return kFailed;
-    if constexpr (KIND != kForward) {
-        if (a.splits == 1) return kOk;
-        const int64_t rows = a.m * a.outs;
-        const dim3 joins((uint32_t)((a.n + 4 * kJoinLanes - 1) / (4 * kJoinLanes)),
-                         (uint32_t)(rows < 32768 ? rows : 32768));
-        if (hipLaunchKernel(reinterpret_cast<const void*>(product_join_kernel<DT>), joins,
-                            dim3(kJoinLanes * kJoinGroups), args, 0, stream) != hipSuccess)
+        if (a.shape == kTile32x128) {
+            if constexpr (KIND != kInput) return kFailed;
+            else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 4, true>)
+                              : reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 2, false>);
+        } else if (!a.direct) {
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, false>);
+            if constexpr (DT != PTORED_F32) {
+                if (a.shape == kTile256) {
+                    threads = 512;
+                    k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, false>);
+                }
+            }
+        } else if (a.shape == kTile128) {
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, true>);
+        } else if (a.shape == kTile128Deep) {
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 4, true>);
+        } else if (a.shape == kTile256) {
+            threads = 512;
+            if constexpr (DT == PTORED_F32) return kFailed;
+            else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, true>);
+        } else if constexpr (KIND == kForward) {
+            if (a.shape == kTile64) threads = 128;
+            k = a.shape == kTile64
+                    ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, true>)
+                    : reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, true>);
+        } else {
+            return kFailed;
+        }
+        const uint32_t grid = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)(a.outs * a.splits);
+        if (hipLaunchKernel(k, dim3(grid), dim3((uint32_t)threads), args, 0, stream) != hipSuccess)
             return kFailed;
     }
-    return kOk;
+    if (a.splits == 1) return kOk;
+    const int64_t rows = a.m * (KIND == kForward ? 1 : a.outs);
+    const dim3 joins((uint32_t)((a.n + 4 * kJoinLanes - 1) / (4 * kJoinLanes)),
+                     (uint32_t)(rows < 32768 ? rows : 32768));
+    return hipLaunchKernel(reinterpret_cast<const void*>(product_join_kernel<DT, KIND>), joins,
+                           dim3(kJoinLanes * kJoinGroups), args, 0, stream) == hipSuccess
+               ? kOk
+               : kFailed;
 }
 
 }  // namespace step

@@ -67,38 +67,36 @@ bool direct_of(const ptored_rows& r, int64_t rows, int64_t cols, int es) {
 
 struct ProductShape {
     int64_t tiles_m, tiles_n, splits, steps_per_split;
-    int shape;
+    int shape, waves;
 };
 
 constexpr int64_t kMaxTiles = int64_t(1) << 22;
 
-// A tile's time: base + step us for each of its steps, `slots` tiles at once
-// (fits to 16 to 8192 tokens, 512 to 4096 columns and 640 to 16384 features).
+// A tile's rows and columns of the output, and its time: base + step us for each
+// of its steps, `slots` tiles at once (fits to 16 to 8192 tokens, 512 to 4096
+// columns and 640 to 16384 features).
 struct TileCost {
     int shape;
-    int64_t tile, slots;
+    int64_t rows, cols, slots;
     double base, step;
 };
 
-// Tiles and splits of a product; for kInput k is that of each of the two pairs.
-// Splits share a tile's steps among several workgroups, each of which writes
-// its sums in 32 bits, which are read again by a second kernel: 4 us and the
-// bytes at 4 TB/s.  The forward pass has none (the activation needs whole sums).
+// Tiles and splits of a product, by estimated time; for kInput k is that of each
+// of the two pairs.  Splits share a tile's steps among several workgroups, each
+// of which writes its sums in 32 bits, which a second kernel reads again: 4 us
+// and the bytes at 4 TB/s.
 //
-// Few tokens, forward (16-bit types; D = 4096, F = 8192, us): 1 token 25 with
-// kFew16, 60 in tiles of 128; 32 tokens 32 with kTile64, 37 with kFew32; 64: 34,
-// 41; 128: 37 with kTile128x32, 68 in tiles of 128.  Rows that do not start at
-// multiples of 16 bytes (D = 4095, F = 8193): 64 tokens 80 in tiles of 128, 157
-// with kFew64.  In 32 bits kTile64's two waves are not enough for its products (64
-// tokens 149, kFew64 80).
-// Beyond, with tiles of 128, the same with loads further ahead, and 256: 192
-// tokens 70, 48, 103; 512: 85, 103, 107; 1024: 159, 181, 122.
+// Measured (forward, bf16, D = 4096, F = 8192, us): 1 token 25 with kFew16, 60 in
+// tiles of 128; 32 tokens 32 with kTile64, 37 with kFew32; 64: 34, 41; 128: 37
+// with kTile128x32, 68 in tiles of 128; in tiles of 128, the same with loads
+// further ahead, and 256: 192 tokens 70, 48, 103; 512: 85, 103, 107; 1024: 159,
+// 181, 122.  Rows that do not start at multiples of 16 bytes (D = 4095, F = 8193):
+// 64 tokens 80 in tiles of 128, 157 with kFew64; 2048 tokens 460, in tiles of 256
+// 411.  In 32 bits kTile64's two waves are not enough for its products (64 tokens
+// 149, kFew64 80).
 ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, int dtype,
                            bool direct) {
-    static constexpr TileCost k16[] = {{kTile128, 128, 512, 5, 1.1},
-                                       {kTile128Deep, 128, 256, 4, 0.85},
-                                       {kTile256, 256, 256, 8, 1.7}};
-    static constexpr TileCost k32[] = {{kTile128, 128, 512, 5, 3.9}, {kTile128Deep, 128, 256, 4, 2.0}};
+    const bool f32 = dtype == PTORED_F32;
     const int es = esize_of(dtype);
     const int64_t depth = kStepBytes / es;
     const int64_t steps = std::max<int64_t>(1, (k + depth - 1) / depth) * (kind == kInput ? 2 : 1);
@@ -106,34 +104,35 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
     s.splits = 1;
     s.steps_per_split = steps;
     if (m == 0 || n == 0) return s;
-    const bool skinny = direct && m > 16 && m <= 128 && (dtype != PTORED_F32 || m > 64);
-    if (kind == kForward && skinny) {
-        s.shape = m <= 64 ? kTile64 : kTile128x32;
-        s.tiles_m = 1;
-        s.tiles_n = (n + 31) / 32;
-        return s;
-    }
-    if (kind == kForward && (m <= 16 || (dtype == PTORED_F32 && m <= 64)) && k * es >= 16) {
+    // what a split writes and the join reads
+    const double join = (double)(kind == kForward ? 2 : outs) * (double)m * (double)n * 8 / 4e6;
+    double best = -1;
+    if (kind == kForward && (m <= 16 || (f32 && m <= 64)) && k * es >= 16) {
         s.shape = m <= 16 ? kFew16 : m <= 32 ? kFew32 : kFew64;
         s.tiles_m = 1;
-        s.tiles_n = s.shape == kFew64 ? (n + 31) / 32 : (n + 15) / 16;
+        const int64_t features = s.shape == kFew64 ? 32 : 16;
+        s.tiles_n = (n + features - 1) / features;
+        // A workgroup takes 37 bytes of the weights a ns, the memory 5500 for all.
+        // (8192 columns x 2048 features, 1 token: 19 us in 128 workgroups.)
+        const int64_t units = k * es / 256;  // that waves share
+        const double bytes = 2.0 * (double)features * (double)k * es;
+        for (int64_t splits = 1; splits <= 16 && (splits == 1 || units >= 8 * splits); splits *= 2) {
+            const double us = std::max(bytes / (double)splits / 37e3, bytes * (double)s.tiles_n / 5.5e6) +
+                              (splits > 1 ? 4.0 + join * (double)splits : 0.0);
+            if (best >= 0 && us >= best) continue;
+            best = us;
+            s.splits = splits;
+        }
         // waves to share the columns: 2048 fill the chip
-        const int64_t most = s.shape == kFew16 ? 16 : 8;
-        s.splits = 8;
-        while (s.splits < most && s.splits * s.tiles_n < 2048) s.splits *= 2;
+        const int most = s.shape == kFew16 ? 16 : 8;
+        s.waves = 8;
+        while (s.waves < most && s.waves * s.tiles_n * s.splits < 2048) s.waves *= 2;
         return s;
     }
-    static constexpr TileCost kHeld16[] = {{kTile128, 128, 512, 5, 1.35}, {kTile256, 256, 256, 8, 2.1}};
-    const TileCost* costs = dtype == PTORED_F32 ? k32 : direct ? k16 : kHeld16;
-    const int count = dtype == PTORED_F32 ? (direct ? 2 : 1) : direct ? 3 : 2;
-    const double join = (double)outs * (double)m * (double)n * 8 / 4e6;
-    double best = -1;
-    for (int i = 0; i < count; ++i) {
-        const TileCost& c = costs[i];
-        const int64_t wide = kind == kForward ? c.tile / 2 : c.tile;
-        const int64_t tm = (m + c.tile - 1) / c.tile, tn = (n + wide - 1) / wide, tiles = tm * tn * outs;
+    auto look = [&](const TileCost& c) {
+        const int64_t tm = (m + c.rows - 1) / c.rows, tn = (n + c.cols - 1) / c.cols, tiles = tm * tn * outs;
         // more splits than make 2 rounds never pay
-        const int64_t most = kind == kForward ? 1 : std::min((2 * c.slots + tiles - 1) / tiles, (steps + 3) / 4);
+        const int64_t most = std::min((2 * c.slots + tiles - 1) / tiles, (steps + 3) / 4);
         for (int64_t splits = 1; splits <= std::max<int64_t>(most, 1); ++splits) {
             const int64_t per = (steps + splits - 1) / splits;
             if (splits > 1 && (steps + per - 1) / per != splits) continue;  // a split would be empty
@@ -148,11 +147,25 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
             s.splits = splits;
             s.steps_per_split = per;
         }
+    };
+    const int64_t half = kind == kForward ? 2 : 1;  // a tile's columns are those of two weights
+    if (!direct) {
+        look({kTile128, 128, 128 / half, 512, 5, f32 ? 3.9 : 1.35});
+        if (!f32) look({kTile256, 256, 256 / half, 256, 8, 2.1});
+    } else {
+        look({kTile128, 128, 128 / half, 512, 5, f32 ? 3.9 : 1.1});
+        look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.85});
+        if (!f32) look({kTile256, 256, 256 / half, 256, 8, 1.7});
+        if (kind == kForward) {
+            if (!f32) look({kTile64, 64, 32, 256, 5, 0.48});
+            look({kTile128x32, 128, 32, 256, 5, f32 ? 1.2 : 0.56});
+        }
     }
+    if (kind == kInput) look({kTile32x128, 32, 128, 512, 5, f32 ? 1.1 : 0.9});
     return s;
 }
 int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs) {
-    return s.splits > 1 ? s.splits * outs * m * pitch_of(n) * 4 : 0;
+    return s.splits > 1 ? s.splits * outs * m * pitch_of(n) * 4 : 0;  // kForward: 2 outs
 }
 bool launchable(const ProductShape& s, int outs) {
     return s.tiles_m <= kMaxTiles && s.tiles_n <= kMaxTiles &&
@@ -164,6 +177,7 @@ void set_shape(ProductArgs& a, const ProductShape& s, bool direct) {
     a.splits = (int32_t)s.splits;
     a.steps_per_split = s.steps_per_split;
     a.shape = s.shape;
+    a.waves = s.waves;
     a.direct = direct;
 }
 void set_a(ProductArgs& a, int i, const ptored_rows& r, int es) {
@@ -488,7 +502,7 @@ extern "C" int ptored_layer_norm_backward(const ptored_layer_norm_params* params
 
 extern "C" int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, ptored_rows w_gate,
                                 ptored_rows w_up, ptored_rows y, ptored_rows gate, ptored_rows up,
-                                hipStream_t stream) {
+                                void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (!ffn_valid(params) || x.data == nullptr || w_gate.data == nullptr || w_up.data == nullptr ||
         y.data == nullptr)
         return PTORED_ERR_INVALID_ARG;
@@ -509,6 +523,9 @@ extern "C" int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, 
                         direct_of(w_up, p.wide, p.cols, es);
     const ProductShape s = product_shape(kForward, p.rows, p.wide, p.cols, 1, p.dtype, direct);
     if (!launchable(s, 1)) return PTORED_ERR_UNSUPPORTED;
+    const int64_t need = product_workspace(s, p.rows, p.wide, 2);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PTORED_ERR_INVALID_ARG;
+    if (need > 0) b.vec(workspace, need, 16, true);
     if (!b.aligned()) return PTORED_ERR_INVALID_ARG;
     if (!b.disjoint()) return PTORED_ERR_OVERLAP;
     if (p.rows == 0 || p.wide == 0) return PTORED_OK;
@@ -525,8 +542,22 @@ extern "C" int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, 
     a.up = mat(up, es);
     a.outs = 1;
     a.activation = p.activation;
+    a.ws = static_cast<float*>(workspace);
+    a.ws_ld = pitch_of(p.wide);
     set_shape(a, s, direct);
     return status_of(PTORED_BY_TYPE(product_forward, p.dtype, a, stream));
+}
+
+extern "C" int ptored_gated_ffn_workspace(int64_t rows, int64_t cols, int64_t wide, int dtype,
+                                          int64_t* bytes) {
+    if (bytes == nullptr || !shape_ok(rows, cols) || !shape_ok(rows, wide) || !shape_ok(wide, cols))
+        return PTORED_ERR_INVALID_ARG;
+    if (!float_type(dtype)) return PTORED_ERR_UNSUPPORTED;
+    *bytes = 0;  // of any alignment
+    for (const bool direct : {false, true})
+        *bytes = std::max(*bytes, product_workspace(product_shape(kForward, rows, wide, cols, 1, dtype, direct),
+                                                    rows, wide, 2));
+    return PTORED_OK;
 }
 
 extern "C" int ptored_gated_ffn_backward_workspace(int64_t rows, int64_t cols, int64_t wide,
@@ -651,6 +682,7 @@ extern "C" int ptored_grad_norm_workspace(const ptored_grad* grads, int64_t coun
     int64_t total = 0;
     for (int64_t i = 0; i < count; ++i) {
         if (!shape_ok(grads[i].rows, grads[i].cols)) return PTORED_ERR_INVALID_ARG;
+        if (!float_type(grads[i].dtype)) return PTORED_ERR_UNSUPPORTED;
         total += grads[i].rows * grads[i].cols;
         if (total > ptored::block::kMaxElems) return PTORED_ERR_INVALID_ARG;
     }

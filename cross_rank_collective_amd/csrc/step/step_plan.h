@@ -56,10 +56,12 @@ struct ProductArgs {
     Mat out[2];                // kForward: y; kInput: dx; kWeight: dWg, dWu
     Mat gate, up;              // kForward: what is kept
     float* ws;                 // [split][out][m][ws_ld] partial sums when splits > 1
+                               // (kForward: g and u as two outs)
     int64_t ws_ld;             // n, rounded up to whole vectors of 4
     int64_t steps_per_split;
     int32_t tiles_m, tiles_n, splits;
     int32_t outs;        // kWeight: products, 1 or 2
+    int32_t waves;       // kFew16 to kFew64: of a workgroup
     int32_t out_f32, accumulate, activation;
     int32_t shape;       // a tile of kShapes
     int32_t direct;      // every row and column range is whole aligned chunks
@@ -72,9 +74,10 @@ enum : int {
     kTile256 = 2,      // 256 x 256, 8 waves; 16-bit types, aligned
     kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; aligned
     kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned
-    kFew16 = 5,        // kForward of up to 16 tokens; `splits` counts a workgroup's waves
-    kFew32 = 6,        // 32 tokens; F32
-    kFew64 = 7         // 64 tokens; F32
+    kTile32x128 = 5,   // kInput: 32 tokens x 128 columns, 4 waves
+    kFew16 = 6,        // kForward of up to 16 tokens
+    kFew32 = 7,        // 32 tokens; F32
+    kFew64 = 8         // 64 tokens; F32
 };
 constexpr int kStepBytes = 128;  // of each row along k that a step takes
 

@@ -64,7 +64,8 @@ def _load() -> ctypes.CDLL:
                                                    ptored_rows, ptored_rows, _vp, _vp, ptored_rows,
                                                    _vp, _vp, _vp, _i64, _vp]
         lib.ptored_layer_norm_backward_workspace.argtypes = [_i64, _i64, P(_i64)]
-        lib.ptored_gated_ffn.argtypes = [P(ptored_ffn_params), *[ptored_rows] * 6, _vp]
+        lib.ptored_gated_ffn.argtypes = [P(ptored_ffn_params), *[ptored_rows] * 6, _vp, _i64, _vp]
+        lib.ptored_gated_ffn_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, P(_i64)]
         lib.ptored_gated_ffn_backward.argtypes = [P(ptored_ffn_params), P(ptored_ffn_grad_io), _vp]
         lib.ptored_gated_ffn_backward_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, P(_i64)]
         lib.ptored_grad_norm.argtypes = [P(ptored_grad), _i64, _vp, _vp, _i64, _vp]
@@ -73,7 +74,7 @@ def _load() -> ctypes.CDLL:
         lib.ptored_grad_norm_workspace.argtypes = [P(ptored_grad), _i64, P(_i64)]
         for name in ("ptored_layer_norm", "ptored_layer_norm_backward",
                      "ptored_layer_norm_backward_workspace", "ptored_gated_ffn",
-                     "ptored_gated_ffn_backward", "ptored_gated_ffn_backward_workspace",
+                     "ptored_gated_ffn_workspace", "ptored_gated_ffn_backward", "ptored_gated_ffn_backward_workspace",
                      "ptored_grad_norm", "ptored_grad_scale", "ptored_grad_clip",
                      "ptored_grad_norm_workspace"):
             getattr(lib, name).restype = ctypes.c_int
@@ -103,8 +104,16 @@ def ptored_layer_norm_backward_workspace(rows: int, cols: int):
     return st, out.value
 
 
-def ptored_gated_ffn(params: ptored_ffn_params, x, w_gate, w_up, y, gate, up, stream: int) -> int:
-    return _load().ptored_gated_ffn(params, x, w_gate, w_up, y, gate, up, stream)
+def ptored_gated_ffn(params: ptored_ffn_params, x, w_gate, w_up, y, gate, up, workspace,
+                     workspace_bytes: int, stream: int) -> int:
+    return _load().ptored_gated_ffn(params, x, w_gate, w_up, y, gate, up, workspace,
+                                    workspace_bytes, stream)
+
+
+def ptored_gated_ffn_workspace(rows: int, cols: int, wide: int, dtype: int):
+    out = _i64()
+    st = _load().ptored_gated_ffn_workspace(rows, cols, wide, dtype, out)
+    return st, out.value
 
 
 def ptored_gated_ffn_backward(params: ptored_ffn_params, io: ptored_ffn_grad_io, stream: int) -> int:
@@ -242,7 +251,15 @@ def _activation_code(name) -> int:
     return code
 
 
-def gated_ffn(x, w_gate, w_up, y, *, activation: str = "silu", gate=None, up=None,
+def gated_ffn_workspace(rows: int, cols: int, wide: int, dtype) -> int:
+    """Bytes of workspace of ``gated_ffn`` for x [rows, cols] and weights
+    [wide, cols]."""
+    st, n = ptored_gated_ffn_workspace(rows, cols, wide, B._dtype_code(dtype))
+    B._raise_on(st)
+    return n
+
+
+def gated_ffn(x, w_gate, w_up, y, *, activation: str = "silu", gate=None, up=None, workspace=None,
               stream=None) -> None:
     """y = f(x w_gate^T) (x w_up^T): the column-parallel half of a gated
     feed-forward block.
@@ -253,7 +270,7 @@ def gated_ffn(x, w_gate, w_up, y, *, activation: str = "silu", gate=None, up=Non
     the backward pass.  Sums are in float32 and f takes them unrounded.
     """
     code = _activation_code(activation)
-    if K._native_call("gated_ffn", stream, x, w_gate, w_up, y, code, gate, up):
+    if K._native_call("gated_ffn", stream, x, w_gate, w_up, y, code, gate, up, workspace):
         return
     g = K._Group(x, "x")
     if y.dim() != 2:
@@ -269,7 +286,10 @@ def gated_ffn(x, w_gate, w_up, y, *, activation: str = "silu", gate=None, up=Non
     if g.cols == 0:  # sums over no columns
         K._zero((y, gate, up), g.index, stream)
         return
-    g.run(stream, ptored_gated_ffn, params, *args)
+    st, nbytes = ptored_gated_ffn_workspace(g.rows, g.cols, wide, g.code)
+    B._raise_on(st)
+    keep, ptr, given = K._workspace(nbytes, workspace, g.index, stream)
+    g.run(stream, ptored_gated_ffn, params, *args, ptr, given)
     K._wrote(y, gate, up)
 
 

@@ -97,7 +97,11 @@ typedef struct ptored_ffn_params {
  */
 int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, ptored_rows w_gate,
                      ptored_rows w_up, ptored_rows y, ptored_rows gate, ptored_rows up,
-                     hipStream_t stream);
+                     void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace (16-byte aligned) that such a forward pass needs; 0 but where
+ * few tokens meet few features (no HIP call). */
+int ptored_gated_ffn_workspace(int64_t rows, int64_t cols, int64_t wide, int dtype, int64_t* bytes);
 
 /* Buffers of the backward pass. */
 typedef struct ptored_ffn_grad_io {

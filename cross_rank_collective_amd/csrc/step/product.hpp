@@ -48,18 +48,18 @@ __device__ __forceinline__ uint32_t lds_address(const char* p) {
     return (uint32_t)(uintptr_t)(lds_char*)p;
 }
 
-// 16 bytes a lane from `off` behind the resource's base to the LDS at `to` (the
-// same for all lanes) + 16 x lane.  The compiler does not see the write:
+// 16 bytes a lane from `off` + `more` behind the resource's base to the LDS at `to`
+// (the same for all lanes, as `more` is) + 16 x lane.  The compiler does not see the write:
 // barriers with a wait order it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is reserved, so every user sets it first
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t off, uint32_t to) {
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t off, uint32_t more, uint32_t to) {
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
         "s_nop 0\n\t"
-        "buffer_load_dwordx4 %0, %1, 0 offen lds"
+        "buffer_load_dwordx4 %0, %1, %3 offen lds"
         :
-        : "v"(off), "s"(rsrc), "s"(to)
+        : "v"(off), "s"(rsrc), "s"(to), "s"(more)
         : "m0");
 }
 #pragma clang diagnostic pop
@@ -95,7 +95,10 @@ struct Side {
     static constexpr int kBack = DIRECT ? 0 : 16;
     static_assert(!HALVES || (LAYOUT == kAlong && kLoads % 2 == 0), "halves are whole loads");
 
-    uint32_t off[kLoads];  // bytes from the operand's place, or kNowhere
+    // bytes from the operand's place, or kNowhere; kAcross: of the first chunk, the
+    // next ones `pitch` on
+    uint32_t off[LAYOUT == kAlong ? kLoads : 1];
+    uint32_t pitch;
     int depth;             // kAlong: k of this thread's chunks in a step; kAcross: its first row's
     int moved;             // kAcross: elements from where the chunks are loaded to where they belong
     bool edge;             // some lane of the wave has moved chunks
@@ -108,7 +111,8 @@ struct Side {
     };
 
     // The thread's chunks of the product's rows [first, first + EXT) of `total`.
-    __device__ __forceinline__ void init(int64_t first, int64_t total, int64_t ld) {
+    // `up_ld`: the pitch of the second matrix.
+    __device__ __forceinline__ void init(int64_t first, int64_t total, int64_t ld, int64_t up_ld) {
         const int pos = (int)threadIdx.x % kPerRow, row0 = (int)threadIdx.x / kPerRow;
         moved = 0;
         if constexpr (LAYOUT == kAlong) {
@@ -117,7 +121,8 @@ struct Side {
 #pragma unroll
             for (int q = 0; q < kLoads; ++q) {
                 const int row = row0 + (HALVES ? q % (kLoads / 2) : q) * kRows;
-                off[q] = first + row < total ? (uint32_t)(row * ld) + c * 16 + kBack : kNowhere;
+                off[q] = first + row < total ? (uint32_t)(row * (second(q) ? up_ld : ld)) + c * 16 + kBack
+                                             : kNowhere;
             }
         } else {
             const int c = ((pos >> 2 ^ (row0 & 3)) << 2) | (pos & 3);
@@ -129,10 +134,9 @@ struct Side {
                 moved = (int)(col - from);
                 col = from;
             }
-#pragma unroll
-            for (int q = 0; q < kLoads; ++q)
-                // (the base lies kBack before the tile's first column, for moved ones)
-                off[q] = in ? (uint32_t)((row0 + q * kRows) * ld + (col - first) * ES + kBack) : kNowhere;
+            // (the base lies kBack before the tile's first column, for moved ones)
+            off[0] = in ? (uint32_t)(row0 * ld + (col - first) * ES + kBack) : kNowhere;
+            pitch = (uint32_t)(kRows * ld);
         }
         edge = __ballot(moved != 0) != 0;
     }
@@ -141,9 +145,11 @@ struct Side {
     // takes only in a row's last one.
     template <bool LAST>
     __device__ __forceinline__ uint32_t place(int q, int left) const {
-        if (!LAST) return off[q];
-        return (LAYOUT == kAlong ? depth : depth + q * kRows) >= left ? kNowhere : off[q];
+        const uint32_t at = off[LAYOUT == kAlong ? q : 0];
+        if (!LAST) return at;
+        return (LAYOUT == kAlong ? depth : depth + q * kRows) >= left ? kNowhere : at;
     }
+    __device__ __forceinline__ uint32_t more(int q) const { return LAYOUT == kAlong ? 0u : q * pitch; }
     static __device__ __forceinline__ bool second(int q) { return HALVES && q >= kLoads / 2; }
 
     __device__ __forceinline__ void load_direct(const char* p, const char* p2, int left, uint32_t to) const {
@@ -152,7 +158,7 @@ struct Side {
         auto each = [&](auto last) {
 #pragma unroll
             for (int q = 0; q < kLoads; ++q)
-                load_to_lds(second(q) ? r2 : r, place<decltype(last)::value>(q, left),
+                load_to_lds(second(q) ? r2 : r, place<decltype(last)::value>(q, left), more(q),
                             to + q * (THREADS * 16) + wave * 1024);
         };
         if (left >= kDepth)
@@ -170,7 +176,8 @@ struct Side {
         if (__builtin_expect(left >= kDepth && extent >= V, 1)) {
 #pragma unroll
             for (int q = 0; q < kLoads; ++q)
-                h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(second(q) ? r2 : r, (int)off[q], 0, 0);
+                h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(second(q) ? r2 : r, (int)place<false>(q, left),
+                                                               (int)more(q), 0);
         } else if (extent >= V) {
             // of a chunk that the row's end cuts, what ends with the row
             if (LAYOUT == kAlong && depth < left) h.by = max(depth + V - left, 0);
@@ -179,7 +186,7 @@ struct Side {
             for (int q = 0; q < kLoads; ++q) {
                 const uint32_t at = place<true>(q, left);
                 h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(
-                    second(q) ? r2 : r, (int)(at == kNowhere ? at : at - h.by * ES), 0, 0);
+                    second(q) ? r2 : r, (int)(at == kNowhere ? at : at - h.by * ES), (int)more(q), 0);
             }
         } else {
             // the rows' only chunks, element by element
@@ -191,9 +198,10 @@ struct Side {
                 for (int i = 0; i < V - 1; ++i) {
                     const int at = (int)(i >= extent || from == kNowhere ? kNowhere : from + i * ES);
                     if constexpr (ES == 4)
-                        w[i] = __builtin_amdgcn_raw_buffer_load_b32(second(q) ? r2 : r, at, 0, 0);
+                        w[i] = __builtin_amdgcn_raw_buffer_load_b32(second(q) ? r2 : r, at, (int)more(q), 0);
                     else
-                        w[i / 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(second(q) ? r2 : r, at, 0, 0)
+                        w[i / 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(second(q) ? r2 : r, at,
+                                                                                   (int)more(q), 0)
                                     << (16 * (i % 2));
                 }
                 h.w[q] = (u32x4){w[0], w[1], w[2], w[3]};
@@ -273,46 +281,35 @@ __device__ __forceinline__ void landed() {
     asm volatile("" ::: "memory");
 }
 
-// Swaps x's upper 32 lanes with y's lower ones.
-__device__ __forceinline__ void swap_halves(float& x, float& y) {
-    const auto v = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(y), false, false);
-    x = as_f(v[0]);
-    y = as_f(v[1]);
-}
-
-// 8 elements to or from `n` (at most 8 count) of a row.
-template <int DT>
-__device__ __forceinline__ void store8(char* p, const float* v, int64_t n) {
+// C elements, 16 bytes of type DT, to or from a row of which `n` (at most C
+// count) are left.
+template <int DT, int C>
+__device__ __forceinline__ void store_chunk(char* p, const float* v, int64_t n) {
     using E = Elem<DT>;
-    if (n >= 8) {
+    static_assert(C == E::V, "a slot");
+    if (__builtin_expect(n >= C, 1)) {
         *reinterpret_cast<u32x4_any*>(p) = E::narrow(v);
-        if constexpr (E::V == 4) *reinterpret_cast<u32x4_any*>(p + 16) = E::narrow(v + 4);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < C - 1; ++i)
         if (i < n) E::store1(p + i * E::kBytes, v[i]);
 }
-template <int DT>
-__device__ __forceinline__ void add8(const char* p, float* v, int64_t n) {
+template <int DT, int C>
+__device__ __forceinline__ void add_chunk(const char* p, float* v, int64_t n) {
     using E = Elem<DT>;
-    if (n >= 8) {
-        float w[8];
+    if (__builtin_expect(n >= C, 1)) {
+        float w[C];
         E::widen(*reinterpret_cast<const u32x4_any*>(p), w);
-        if constexpr (E::V == 4) E::widen(*reinterpret_cast<const u32x4_any*>(p + 16), w + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += w[i];
+        for (int i = 0; i < C; ++i) v[i] += w[i];
         return;
     }
+    float w[C];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) v[i] += E::load1(p + i * E::kBytes);
-}
-
-// 8 partial sums, `n` of them inside a row of whole vectors of 4.
-__device__ __forceinline__ void store_sums(float* p, const float* v, int64_t n) {
-    *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
-    if (n > 4) *reinterpret_cast<f32x4*>(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+    for (int i = 0; i < C - 1; ++i) w[i] = i < n ? E::load1(p + i * E::kBytes) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < C - 1; ++i) v[i] += w[i];
 }
 
 // WM x WN waves of TM x TN blocks of 32 x 32; NS buffers of STEP bytes along k in
@@ -366,22 +363,26 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     int pair = 0, loaded = 0;  // the operands' pair; steps asked for
     int64_t left;
     const char *pa, *pb, *pb2;
+    // (selected, not indexed: an array indexed by a register goes to scratch memory)
+    int64_t a_ld = 0, b_ld = 0;
     auto begin = [&](int64_t step) {
         pair = KIND == kInput ? (int)(step / per_pair) : KIND == kWeight ? which : 0;
         const int64_t in = KIND == kInput ? step - pair * per_pair : step;
-        const int from = KIND == kWeight ? 0 : pair;
+        const bool up = KIND != kForward && pair != 0, up_b = KIND == kInput && pair != 0;
+        a_ld = up ? a.a_ld[1] : a.a_ld[0];
+        b_ld = up_b ? a.b_ld[1] : a.b_ld[0];
         left = a.k - in * kDepth;
-        pa = a.a[pair] + (LA == kAlong ? m0 * a.a_ld[pair] + in * STEP
-                                       : in * kDepth * a.a_ld[pair] + m0 * E::kBytes);
-        pb = a.b[from] + (LB == kAlong ? n0 * a.b_ld[from] + in * STEP
-                                       : in * kDepth * a.b_ld[from] + n0 * E::kBytes);
+        pa = (up ? a.a[1] : a.a[0]) + (LA == kAlong ? m0 * a_ld + in * STEP
+                                                    : in * kDepth * a_ld + m0 * E::kBytes);
+        pb = (up_b ? a.b[1] : a.b[0]) + (LB == kAlong ? n0 * b_ld + in * STEP
+                                                      : in * kDepth * b_ld + n0 * E::kBytes);
         pb2 = kPair ? a.b[1] + n0 * a.b_ld[1] + in * STEP : pb;
     };
     A sa;
     B sb;
     auto places = [&] {
-        sa.init(m0, a.m, a.a_ld[pair]);
-        sb.init(n0, a.n, a.b_ld[KIND == kWeight ? 0 : pair]);
+        sa.init(m0, a.m, a_ld, a_ld);
+        sb.init(n0, a.n, b_ld, kPair ? a.b_ld[1] : b_ld);
     };
     auto advance = [&] {
         ++loaded;
@@ -395,8 +396,8 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
             begin(first);
             return;
         }
-        pa += LA == kAlong ? STEP : kDepth * a.a_ld[pair];
-        pb += LB == kAlong ? STEP : kDepth * a.b_ld[KIND == kWeight ? 0 : pair];
+        pa += LA == kAlong ? STEP : kDepth * a_ld;
+        pb += LB == kAlong ? STEP : kDepth * b_ld;
         pb2 += STEP;
     };
     // extents of the rows that chunks lie in
@@ -527,66 +528,89 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     landed<0>();  // the LDS may be another workgroup's after this
 
     // Register r of a block is column 8 (r / 4) + 4 (lane / 32) + r % 4 of row lane
-    // % 32.  With halves swapped a lane has 8 consecutive ones for each of two
-    // half blocks.
-    auto half = [&](f32x16& v, int h, float* to) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            to[r] = v[8 * h + r];
-            to[4 + r] = v[8 * h + 4 + r];
-            swap_halves(to[r], to[4 + r]);
-        }
-    };
+    // % 32.  Each wave turns its blocks, 32 rows at a time, in LDS of its own, so
+    // that its lanes store whole pieces of rows: from the registers a store reaches
+    // 32 rows, 32 bytes of each.
+    constexpr int kBlocks = kPair ? TN / 2 : TN, kPitch = kBlocks * 32 + 4;
+    constexpr int kArea = 32 * kPitch;
+    static_assert(WM * WN * (kPair ? 2 : 1) * kArea * 4 <= NS * kBytes, "room for it");
+    float* const area = reinterpret_cast<float*>(lds) + wave * ((kPair ? 2 : 1) * kArea);
+    // the arguments read again: nothing that only this end needs stays in registers
+    // over the steps
+    const auto& z = args_again<ProductArgs>();
+    const int64_t tile_col = n0 + wn * (kBlocks * 32);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int64_t row = m0 + (wm * TM + i) * 32 + (lane & 31);
-        // every lane takes part in the swaps
-        if constexpr (kPair) {
+        const int64_t tile_row = m0 + (wm * TM + i) * 32;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int j = 0; j < TN / 2; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t col = n0 + (wn * (TN / 2) + j) * 32 + h * 16 + (lane >> 5) * 8;
-                    float g[8], u[8], y[8];
-                    half(acc[i][j], h, g);
-                    half(acc[i][TN / 2 + j], h, u);
-                    const int64_t n = row < a.m ? a.n - col : 0;
-                    if (n <= 0) continue;
-                    if (a.splits > 1) {
-                        store_sums(a.ws + ((int64_t)split * 2 * a.m + row) * a.ws_ld + col, g, n);
-                        store_sums(a.ws + (((int64_t)split * 2 + 1) * a.m + row) * a.ws_ld + col, u, n);
-                        continue;
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(area + j / kBlocks * kArea + (lane & 31) * kPitch +
+                                          j % kBlocks * 32 + q * 8 + (lane >> 5) * 4) =
+                    (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        // f(row, column, columns left, sums of C columns in each area) of what is inside
+        auto pieces = [&](auto chunk, auto f) {
+            constexpr int C = decltype(chunk)::value, kPerRow = kBlocks * 32 / C, kAtOnce = 64 / kPerRow;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+                const int r = r0 + lane / kPerRow, c = lane % kPerRow * C;
+                const int64_t row = tile_row + r, col = tile_col + c;
+                if (row >= z.m || col >= z.n) continue;
+                float v[C], w[C];
+#pragma unroll
+                for (int k = 0; k < C; k += 4) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(area + r * kPitch + c + k);
+                    const f32x4 y = kPair ? *reinterpret_cast<const f32x4*>(area + kArea + r * kPitch + c + k) : x;
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) {
+                        v[k + l] = x[l];
+                        w[k + l] = y[l];
                     }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = activation<DT>(a.activation, g[e]) * u[e];
-                    store8<DT>(a.out[0].p + row * a.out[0].ld + col * E::kBytes, y, n);
-                    if (a.gate.p) store8<DT>(a.gate.p + row * a.gate.ld + col * E::kBytes, g, n);
-                    if (a.up.p) store8<DT>(a.up.p + row * a.up.ld + col * E::kBytes, u, n);
                 }
+                f(row, col, z.n - col, v, w);
+            }
+        };
+        using Narrow = std::integral_constant<int, E::V>;
+        using Wide = std::integral_constant<int, 4>;
+        if (z.splits > 1) {
+            // ws_ld holds whole vectors of 4, which the join reads
+            pieces(Wide{}, [&](int64_t row, int64_t col, int64_t, float* v, float* w) {
+                const int64_t outs = kPair ? 2 : z.outs;
+                float* p = z.ws + (((int64_t)split * outs + which) * z.m + row) * z.ws_ld + col;
+                *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
+                if (kPair) *reinterpret_cast<f32x4*>(p + z.m * z.ws_ld) = (f32x4){w[0], w[1], w[2], w[3]};
+            });
+        } else if constexpr (kPair) {
+            pieces(Narrow{}, [&](int64_t row, int64_t col, int64_t n, float* g, float* u) {
+                constexpr int C = E::V;
+                float y[C];
+#pragma unroll
+                for (int e = 0; e < C; ++e) y[e] = activation<DT>(z.activation, g[e]) * u[e];
+                store_chunk<DT, C>(z.out[0].p + row * z.out[0].ld + col * E::kBytes, y, n);
+                if (z.gate.p) store_chunk<DT, C>(z.gate.p + row * z.gate.ld + col * E::kBytes, g, n);
+                if (z.up.p) store_chunk<DT, C>(z.up.p + row * z.up.ld + col * E::kBytes, u, n);
+            });
         } else {
-            const Mat out = a.out[which];
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t col = n0 + (wn * TN + j) * 32 + h * 16 + (lane >> 5) * 8;
-                    float v[8];
-                    half(acc[i][j], h, v);
-                    const int64_t n = row < a.m ? a.n - col : 0;
-                    if (n <= 0) continue;
-                    if (a.splits > 1) {
-                        store_sums(a.ws + (((int64_t)split * a.outs + which) * a.m + row) * a.ws_ld + col,
-                                   v, n);
-                    } else if (a.out_f32) {
-                        char* p = out.p + row * out.ld + col * 4;
-                        if (a.accumulate) add8<PTORED_F32>(p, v, n);
-                        store8<PTORED_F32>(p, v, n);
-                    } else {
-                        char* p = out.p + row * out.ld + col * E::kBytes;
-                        if (a.accumulate) add8<DT>(p, v, n);
-                        store8<DT>(p, v, n);
-                    }
-                }
+            const Mat out = which ? z.out[1] : z.out[0];
+            if (z.out_f32) {
+                pieces(Wide{}, [&](int64_t row, int64_t col, int64_t n, float* v, float*) {
+                    char* p = out.p + row * out.ld + col * 4;
+                    if (z.accumulate) add_chunk<PTORED_F32, 4>(p, v, n);
+                    store_chunk<PTORED_F32, 4>(p, v, n);
+                });
+            } else {
+                pieces(Narrow{}, [&](int64_t row, int64_t col, int64_t n, float* v, float*) {
+                    char* p = out.p + row * out.ld + col * E::kBytes;
+                    if (z.accumulate) add_chunk<DT, E::V>(p, v, n);
+                    store_chunk<DT, E::V>(p, v, n);
+                });
+            }
         }
     }
 }
@@ -619,7 +643,7 @@ __global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(c
         if (group == 0 && col < a.n) {
             const bool second = KIND != kForward && row >= a.m;
             const int64_t r = second ? row - a.m : row;
-            const Mat out = a.out[second];
+            const Mat out = second ? a.out[1] : a.out[0];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (col + i >= a.n) continue;

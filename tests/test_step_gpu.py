@@ -269,6 +269,33 @@ def test_gated_ffn_tiles(rows, cols, wide, dtype):
     close(dwu, *R.product(hu.t(), x.t(), True), "dw_up")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 40, 100, 300])
+def test_gated_ffn_pitches_of_their_own(rows, dtype):
+    """Every matrix in rows of another pitch, some at multiples of 16 bytes and
+    some not."""
+    cols, wide = 264, 200
+    x, wg, wu = ffn_inputs(rows, cols, wide, dtype)
+    want = R.gated_ffn(x, wg, wu, "silu")
+    for step in (8, 1):
+        y, g, u = (Room(rows, wide, dtype, step * (4 + i)) for i in range(3))
+        gx, gwg, gwu = (put(t, step * (1 + i)) for i, t in enumerate((x, wg, wu)))
+        crc.gated_ffn(gx, gwg, gwu, y.t, gate=g.t, up=u.t)
+        for k, v in {"y": y, "gate": g, "up": u}.items():
+            close(v.t, *want[k], k)
+        dy = put(rand(rows, wide, seed=9, dtype=dtype), step * 7)
+        dg, du, dx = Room(rows, wide, dtype, step * 8), Room(rows, wide, dtype, step * 9), Room(rows, cols, dtype, 3)
+        dwg, dwu = Room(wide, cols, dtype, 5), Room(wide, cols, dtype, 6)
+        crc.gated_ffn_backward(dy, g.t, u.t, dg.t, du.t, x=gx, w_gate=gwg, w_up=gwu, dx=dx.t,
+                               dw_gate=dwg.t, dw_up=dwu.t)
+        hg, hu, exact = dg.t.cpu(), du.t.cpu(), dtype != F32
+        close(dx.t, *R.product(torch.cat([hg, hu], 1), torch.cat([wg, wu], 0).t(), exact), "dx")
+        close(dwg.t, *R.product(hg.t(), x.t(), exact), "dw_gate")
+        close(dwu.t, *R.product(hu.t(), x.t(), exact), "dw_up")
+        for r in (y, g, u, dg, du, dx, dwg, dwu):
+            r.check("an output")
+
+
 # ---------------------------------------------------------------- clipping
 
 def grads_of(shapes, dtype, seed=0, scale=1.0):

@@ -208,6 +208,40 @@ struct Side {
             }
         }
     }
+    // F32 as the exact sum of three bfloat16, each a tile of its own: the value's
+    // upper half (truncated, so that it cannot overflow), that of the exact
+    // remainder, and what is left of it.
+    static constexpr int kPlane = EXT * STEP / 2;
+    __device__ __forceinline__ void store_split(const Held& h, char* to) const {
+        const int row0 = (int)threadIdx.x / kPerRow, pos = (int)threadIdx.x % kPerRow;
+        const bool any = LAYOUT == kAlong ? h.cut : edge;
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int row = row0 + q * kRows;
+            u32x4 w = h.w[q];
+            if (__builtin_expect(any, 0)) w = shift_down(w, (LAYOUT == kAlong ? h.by : moved) * ES);
+            int at;
+            if constexpr (LAYOUT == kAlong) {  // rows of STEP / 2 bytes
+                const int c = pos ^ swizzle<STEP>(row0);
+                at = row * (STEP / 2) + ((c >> 1 ^ swizzle<STEP / 2>(row)) << 4) + (c & 1) * 8;
+            } else {  // rows of EXT elements: 8 chunks a piece of 64 bytes
+                const int c = ((pos >> 2 ^ (row0 & 3)) << 2) | (pos & 3);
+                at = row * (EXT * 2) + ((c >> 3 ^ (row & 3)) << 6) + (c & 7) * 8;
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                uint32_t hi[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    hi[i] = w[i] & 0xFFFF0000u;
+                    if (k < 2) w[i] = as_u(as_f(w[i]) - as_f(hi[i]));
+                }
+                *reinterpret_cast<u32x2*>(to + k * kPlane + at) =
+                    (u32x2){__builtin_amdgcn_perm(hi[1], hi[0], 0x07060302u),
+                            __builtin_amdgcn_perm(hi[3], hi[2], 0x07060302u)};
+            }
+        }
+    }
     __device__ __forceinline__ void store_held(const Held& h, char* to) const {
         auto each = [&](auto any) {
 #pragma unroll
@@ -314,8 +348,16 @@ __device__ __forceinline__ void add_chunk(const char* p, float* v, int64_t n) {
 
 // WM x WN waves of TM x TN blocks of 32 x 32; NS buffers of STEP bytes along k in
 // the LDS.
-template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, bool DIRECT>
+// HOW: what comes to the LDS, and how.
+enum : int {
+    kDirect = 0,  // loaded straight into it
+    kHeld = 1,    // through registers
+    kSplit = 2    // through registers, F32 as three bfloat16
+};
+template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, int HOW>
 __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
+    constexpr bool DIRECT = HOW == kDirect, SPLIT = HOW == kSplit;
+    static_assert(!SPLIT || DT == PTORED_F32, "planes of F32");
     constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
     constexpr bool kPair = KIND == kForward;  // a wave's lower blocks are the gate's, its upper ones the up's
     static_assert(!kPair || TN % 2 == 0, "as many gate's blocks as up's");
@@ -324,7 +366,11 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     using A = Side<DT, LA, BM, STEP, kThreads, DIRECT, false>;
     using B = Side<DT, LB, BN, STEP, kThreads, DIRECT, kPair>;
     using E = Elem<DT>;
-    constexpr int kDepth = A::kDepth, kBytes = A::kBytes + B::kBytes;
+    // as multiplied: planes of bfloat16, each of half a step's bytes
+    constexpr int FT = SPLIT ? (int)PTORED_BF16 : DT, P = SPLIT ? 3 : 1, kStep = SPLIT ? STEP / 2 : STEP;
+    constexpr int kDepth = A::kDepth;
+    constexpr int kPlaneA = SPLIT ? A::kPlane : A::kBytes, kPlaneB = SPLIT ? B::kPlane : B::kBytes;
+    constexpr int kBytes = P * (kPlaneA + kPlaneB);
     constexpr int kLoads = DIRECT ? A::kLoads + B::kLoads : 0;  // of a step that barriers wait for
     static_assert((NS - 1) * kLoads <= 63, "as far as the hardware counts");
     constexpr int kCols = kPair ? BN / 2 : BN;  // of the output
@@ -425,8 +471,13 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     };
     auto stage_held = [&](char* buf, auto which_set) {
         constexpr int set = decltype(which_set)::value;
-        sa.store_held(ha[set], buf);
-        sb.store_held(hb[set], buf + A::kBytes);
+        if constexpr (SPLIT) {
+            sa.store_split(ha[set], buf);
+            sb.store_split(hb[set], buf + P * kPlaneA);
+        } else {
+            sa.store_held(ha[set], buf);
+            sb.store_held(hb[set], buf + A::kBytes);
+        }
         hold(which_set);
     };
     using Set0 = std::integral_constant<int, 0>;
@@ -438,30 +489,41 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16)(0.0f);
     struct Fragments {
-        u32x4 a[TM], b[TN];
+        u32x4 a[P][TM], b[P][TN];
     };
     auto read = [&](const char* buf, int sub, Fragments& f) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) f.a[i] = fragment<DT, LA, BM, STEP>(buf, sub, wm * TM + i);
+        for (int p = 0; p < P; ++p) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-            f.b[j] = fragment<DT, LB, BN, STEP>(buf + A::kBytes, sub, kPair ? j / (TN / 2) * (WN * TN / 2) + wn * (TN / 2) + j % (TN / 2)
-                                                                : wn * TN + j);
+            for (int i = 0; i < TM; ++i)
+                f.a[p][i] = fragment<FT, LA, BM, kStep>(buf + p * kPlaneA, sub, wm * TM + i);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                f.b[p][j] = fragment<FT, LB, BN, kStep>(
+                    buf + P * kPlaneA + p * kPlaneB, sub,
+                    kPair ? j / (TN / 2) * (WN * TN / 2) + wn * (TN / 2) + j % (TN / 2) : wn * TN + j);
+        }
     };
-    // transposed: a lane's sums belong to one row of the output
+    // Transposed: a lane's sums belong to one row of the output.  Of planes' products
+    // those below 2^-22 of the largest are left out, the smallest taken first.
     auto products = [&](const Fragments& f) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int s = P - 1; s >= 0; --s)
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = multiply<DT>(f.b[j], f.a[i], acc[i][j]);
+            for (int p = 0; p <= s; ++p)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[i][j] = multiply<FT>(f.b[p][j], f.a[s - p][i], acc[i][j]);
     };
 
     // The instructions of 32 bytes along k: the next fragments' reads between the first
     // products.  Left to itself the compiler puts each read right before its use.
-    constexpr int kReadsA = LA == kAlong ? 1 : (E::kBytes == 2 ? 2 : 4);
-    constexpr int kReadsB = LB == kAlong ? 1 : (E::kBytes == 2 ? 2 : 4);
-    constexpr int kProducts = TM * TN * (DT == PTORED_F32 ? 4 : 1);
-    constexpr int kBetween = (TM * kReadsA + TN * kReadsB + kProducts - 1) / kProducts;
+    constexpr int kReadsA = LA == kAlong ? 1 : FT == PTORED_F32 ? 4 : 2;
+    constexpr int kReadsB = LB == kAlong ? 1 : FT == PTORED_F32 ? 4 : 2;
+    constexpr int kProducts = TM * TN * (FT == PTORED_F32 ? 4 : P * (P + 1) / 2);
+    constexpr int kBetween = (P * (TM * kReadsA + TN * kReadsB) + kProducts - 1) / kProducts;
     auto order = [] {
 #pragma unroll
         for (int i = 0; i < kProducts; ++i) {
@@ -497,7 +559,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
         read(cur, 1, odd);
         products(even);
         order();
-        if constexpr (STEP == 128) {
+        if constexpr (kStep == 128) {
             read(cur, 2, even);
             products(odd);
             order();
@@ -683,29 +745,33 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
     } else {
         if (a.shape == kTile32x128) {
             if constexpr (KIND != kInput) return kFailed;
-            else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 4, true>)
-                              : reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 2, false>);
+            else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 4, kDirect>)
+                              : reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 2, kHeld>);
+        } else if (a.shape == kTileSplit) {
+            threads = 512;
+            if constexpr (DT != PTORED_F32) return kFailed;
+            else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 2, 2, 2, 128, 2, kSplit>);
         } else if (!a.direct) {
-            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, false>);
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kHeld>);
             if constexpr (DT != PTORED_F32) {
                 if (a.shape == kTile256) {
                     threads = 512;
-                    k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, false>);
+                    k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, kHeld>);
                 }
             }
         } else if (a.shape == kTile128) {
-            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, true>);
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kDirect>);
         } else if (a.shape == kTile128Deep) {
-            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 4, true>);
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 4, kDirect>);
         } else if (a.shape == kTile256) {
             threads = 512;
             if constexpr (DT == PTORED_F32) return kFailed;
-            else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, true>);
+            else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, kDirect>);
         } else if constexpr (KIND == kForward) {
             if (a.shape == kTile64) threads = 128;
             k = a.shape == kTile64
-                    ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, true>)
-                    : reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, true>);
+                    ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, kDirect>)
+                    : reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, kDirect>);
         } else {
             return kFailed;
         }

@@ -161,6 +161,7 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
             look({kTile128x32, 128, 32, 256, 5, f32 ? 1.2 : 0.56});
         }
     }
+    if (f32) look({kTileSplit, 256, 128 / half, 256, 8, 1.9});
     if (kind == kInput) look({kTile32x128, 32, 128, 512, 5, f32 ? 1.1 : 0.9});
     return s;
 }

@@ -93,6 +93,7 @@ struct Side {
     static_assert(kRows % (LAYOUT == kAlong ? 16 : 4) == 0, "a thread's rows share their swizzle");
     // Chunks that end with a row are loaded from up to a chunk before their place.
     static constexpr int kBack = DIRECT ? 0 : 16;
+    static_assert(LAYOUT == kAlong || EXT * 2 >= 256, "four pieces of 64 bytes to permute");
     static_assert(!HALVES || (LAYOUT == kAlong && kLoads % 2 == 0), "halves are whole loads");
 
     // bytes from the operand's place, or kNowhere; kAcross: of the first chunk, the
@@ -747,6 +748,10 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
             if constexpr (KIND != kInput) return kFailed;
             else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 4, kDirect>)
                               : reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 2, kHeld>);
+        } else if (a.shape == kTile64x128) {
+            if constexpr (KIND == kWeight) return kFailed;
+            else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 1, 2, 128, 3, kDirect>)
+                              : reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 1, 2, 128, 2, kHeld>);
         } else if (a.shape == kTileSplit) {
             threads = 512;
             if constexpr (DT != PTORED_F32) return kFailed;

@@ -73,12 +73,12 @@ struct ProductShape {
 constexpr int64_t kMaxTiles = int64_t(1) << 22;
 
 // A tile's rows and columns of the output, and its time: base + step us for each
-// of its steps, `slots` tiles at once (fits to 16 to 8192 tokens, 512 to 4096
-// columns and 640 to 16384 features).
+// of its steps, `slots` tiles at once, or base + alone where no compute unit has
+// two (fits to 16 to 8192 tokens, 512 to 4096 columns and 640 to 16384 features).
 struct TileCost {
     int shape;
     int64_t rows, cols, slots;
-    double base, step;
+    double base, alone, step;
 };
 
 // Tiles and splits of a product, by estimated time; for kInput k is that of each
@@ -137,7 +137,7 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
             const int64_t per = (steps + splits - 1) / splits;
             if (splits > 1 && (steps + per - 1) / per != splits) continue;  // a split would be empty
             const double rounds = (double)((tiles * splits + c.slots - 1) / c.slots);
-            const double us = rounds * (c.base + c.step * (double)per) +
+            const double us = rounds * (c.base + (tiles * splits <= 256 ? c.alone : c.step) * (double)per) +
                               (splits > 1 ? 4.0 + join * (double)splits : 0.0);
             if (best >= 0 && us >= best) continue;
             best = us;
@@ -149,20 +149,20 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         }
     };
     const int64_t half = kind == kForward ? 2 : 1;  // a tile's columns are those of two weights
-    if (!direct) {
-        look({kTile128, 128, 128 / half, 512, 5, f32 ? 3.9 : 1.35});
-        if (!f32) look({kTile256, 256, 256 / half, 256, 8, 2.1});
+    if (direct) {
+        look({kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.0, f32 ? 3.9 : 1.1});
+        look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.85, f32 ? 2.0 : 0.85});
+        if (kind != kWeight) look({kTile64x128, 64, 128 / half, 512, 5, f32 ? 1.0 : 0.6, f32 ? 2.0 : 0.9});
+        if (!f32) look({kTile256, 256, 256 / half, 256, 8, 1.7, 1.7});
+        if (kind == kForward && !f32) look({kTile64, 64, 32, 256, 5, 0.48, 0.48});
+        if (kind == kForward) look({kTile128x32, 128, 32, 256, 5, f32 ? 1.2 : 0.56, f32 ? 1.2 : 0.56});
     } else {
-        look({kTile128, 128, 128 / half, 512, 5, f32 ? 3.9 : 1.1});
-        look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.85});
-        if (!f32) look({kTile256, 256, 256 / half, 256, 8, 1.7});
-        if (kind == kForward) {
-            if (!f32) look({kTile64, 64, 32, 256, 5, 0.48});
-            look({kTile128x32, 128, 32, 256, 5, f32 ? 1.2 : 0.56});
-        }
+        look({kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.15, f32 ? 3.9 : 1.35});
+        if (kind != kWeight) look({kTile64x128, 64, 128 / half, 768, 5, f32 ? 1.0 : 0.95, f32 ? 3.0 : 1.75});
+        if (!f32) look({kTile256, 256, 256 / half, 256, 8, 2.1, 2.1});
     }
-    if (f32) look({kTileSplit, 256, 128 / half, 256, 8, 1.9});
-    if (kind == kInput) look({kTile32x128, 32, 128, 512, 5, f32 ? 1.1 : 0.9});
+    if (f32) look({kTileSplit, 256, 128 / half, 256, 8, 2.3, 2.3});
+    if (kind == kInput) look({kTile32x128, 32, 128, 512, 5, f32 ? 0.7 : 0.6, f32 ? 1.1 : 0.9});
     return s;
 }
 int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs) {

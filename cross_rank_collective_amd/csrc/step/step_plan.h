@@ -75,10 +75,11 @@ enum : int {
     kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; aligned
     kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned
     kTile32x128 = 5,   // kInput: 32 tokens x 128 columns, 4 waves
-    kTileSplit = 6,    // 256 x 128, 8 waves, F32 as three bfloat16
-    kFew16 = 7,        // kForward of up to 16 tokens
-    kFew32 = 8,        // 32 tokens; F32
-    kFew64 = 9         // 64 tokens; F32
+    kTile64x128 = 6,   // 64 x 128, 4 waves, two or (not aligned) three workgroups a compute unit
+    kTileSplit = 7,    // 256 x 128, 8 waves, F32 as three bfloat16
+    kFew16 = 8,        // kForward of up to 16 tokens
+    kFew32 = 9,        // 32 tokens; F32
+    kFew64 = 10        // 64 tokens; F32
 };
 constexpr int kStepBytes = 128;  // of each row along k that a step takes
 

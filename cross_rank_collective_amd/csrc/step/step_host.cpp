@@ -59,6 +59,13 @@ bool ffn_supported(const ptored_ffn_params& p) {
 bool pitch_supported(const ptored_rows& r, int64_t rows, int es) {
     return r.data == nullptr || rows <= 1 || r.ld <= PTORED_FFN_MAX_PITCH / es;
 }
+bool widths_supported(const ptored_ffn_params& p, int es) {
+    return p.cols <= PTORED_FFN_MAX_PITCH / es && p.wide <= PTORED_FFN_MAX_PITCH / es;
+}
+// An operand as the kernels address it: a single row has no pitch of its own.
+ptored_rows operand(const ptored_rows& r, int64_t rows, int64_t cols) {
+    return {r.data, rows > 1 ? r.ld : cols};
+}
 // Rows that start at multiples of 16 bytes and hold whole chunks of 16.
 bool direct_of(const ptored_rows& r, int64_t rows, int64_t cols, int es) {
     return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && cols * es % 16 == 0 &&
@@ -204,6 +211,8 @@ bool grad_supported(const ptored_grad& g, bool scaled) {
     if (!float_type(g.dtype)) return false;
     if (scaled && g.out_dtype != PTORED_F32 && g.out_dtype != g.dtype) return false;
     if (g.rows == 0 || g.cols == 0) return true;
+    // the table keeps a type beside the address
+    if (reinterpret_cast<uintptr_t>(g.data) >> 48 != 0) return false;
     if (g.rows == 1) return g.cols < kGradMost;
     return g.rows <= kInt && g.ld <= kGradPitch && (!scaled || g.out_ld <= kGradPitch);
 }
@@ -517,8 +526,8 @@ extern "C" int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, 
         !b.rows(gate.data, p.rows, p.wide, gate.ld, es, true, false) ||
         !b.rows(up.data, p.rows, p.wide, up.ld, es, true, false))
         return PTORED_ERR_INVALID_ARG;
-    if (!ffn_supported(p) || !pitch_supported(x, p.rows, es) || !pitch_supported(w_gate, p.wide, es) ||
-        !pitch_supported(w_up, p.wide, es))
+    if (!ffn_supported(p) || !widths_supported(p, es) || !pitch_supported(x, p.rows, es) ||
+        !pitch_supported(w_gate, p.wide, es) || !pitch_supported(w_up, p.wide, es))
         return PTORED_ERR_UNSUPPORTED;
     const bool direct = direct_of(x, p.rows, p.cols, es) && direct_of(w_gate, p.wide, p.cols, es) &&
                         direct_of(w_up, p.wide, p.cols, es);
@@ -532,9 +541,9 @@ extern "C" int ptored_gated_ffn(const ptored_ffn_params* params, ptored_rows x, 
     if (p.rows == 0 || p.wide == 0) return PTORED_OK;
 
     ProductArgs a{};
-    set_a(a, 0, x, es);
-    set_b(a, 0, w_gate, es);
-    set_b(a, 1, w_up, es);
+    set_a(a, 0, operand(x, p.rows, p.cols), es);
+    set_b(a, 0, operand(w_gate, p.wide, p.cols), es);
+    set_b(a, 1, operand(w_up, p.wide, p.cols), es);
     a.m = p.rows;
     a.n = p.wide;
     a.k = p.cols;
@@ -609,7 +618,7 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         return PTORED_ERR_INVALID_ARG;
     if (!ffn_supported(p) || (outs > 0 && io->dw_dtype != PTORED_F32 && io->dw_dtype != p.dtype))
         return PTORED_ERR_UNSUPPORTED;
-    if (!pitch_supported(io->dgate, p.rows, es) || !pitch_supported(io->dup, p.rows, es) ||
+    if (!widths_supported(p, es) || !pitch_supported(io->dgate, p.rows, es) || !pitch_supported(io->dup, p.rows, es) ||
         !pitch_supported(x, p.rows, es) || !pitch_supported(wg, p.wide, es) ||
         !pitch_supported(wu, p.wide, es))
         return PTORED_ERR_UNSUPPORTED;
@@ -637,10 +646,10 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
     }
     if (input && p.rows > 0 && p.cols > 0) {
         ProductArgs a{};
-        set_a(a, 0, io->dgate, es);
-        set_a(a, 1, io->dup, es);
-        set_b(a, 0, wg, es);
-        set_b(a, 1, wu, es);
+        set_a(a, 0, operand(io->dgate, p.rows, p.wide), es);
+        set_a(a, 1, operand(io->dup, p.rows, p.wide), es);
+        set_b(a, 0, operand(wg, p.wide, p.cols), es);
+        set_b(a, 1, operand(wu, p.wide, p.cols), es);
         a.m = p.rows;
         a.n = p.cols;
         a.k = p.wide;
@@ -659,10 +668,10 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         for (int i = 0; i < 2; ++i) {
             const ptored_rows& dw = i == 0 ? io->dw_gate : io->dw_up;
             if (dw.data == nullptr) continue;
-            set_a(a, n, i == 0 ? io->dgate : io->dup, es);
+            set_a(a, n, operand(i == 0 ? io->dgate : io->dup, p.rows, p.wide), es);
             a.out[n++] = mat(dw, ws);
         }
-        set_b(a, 0, x, es);
+        set_b(a, 0, operand(x, p.rows, p.cols), es);
         a.m = p.wide;
         a.n = p.cols;
         a.k = p.rows;

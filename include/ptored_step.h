@@ -73,7 +73,10 @@ int ptored_layer_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* by
  *
  *     g = x Wg^T,  u = x Wu^T,  y = f(g) u
  * with x T x D, both weights F x D, and g, u, y T x F.  Products of 16-bit
- * types are exact, sums in binary32; f takes g as summed.
+ * types are exact, sums in binary32; f takes g as summed.  Products of F32 may be
+ * taken as those of each operand's exact sum of three bfloat16, of which those
+ * below 2^-21 of the whole are left out, and what an operand holds below 2^-133 is;
+ * then an infinite operand gives NaN where binary32 gives an infinity.
  */
 typedef enum ptored_activation {
     PTORED_SILU = 0,     /* f(g) = g / (1 + exp(-g)) */
@@ -81,7 +84,8 @@ typedef enum ptored_activation {
     PTORED_GELU_TANH = 2 /* f(g) = g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
 } ptored_activation;
 
-/* Largest row of any of its matrices, in bytes from one row to the next. */
+/* Longest rows (D and F) and largest pitch of the matrices that its products read,
+ * in bytes; more is UNSUPPORTED. */
 #define PTORED_FFN_MAX_PITCH (1 << 22)
 
 typedef struct ptored_ffn_params {
@@ -135,7 +139,9 @@ int ptored_gated_ffn_backward_workspace(int64_t rows, int64_t cols, int64_t wide
 
 /* ---------------------------------------------------------------- gradient clipping */
 
-/* One gradient: rows x cols elements, contiguous where rows is 1. */
+/* One gradient: rows x cols elements, contiguous where rows is 1 (fewer than 2^40;
+ * of several rows fewer than 2^31, their pitches at most 2^27; more is
+ * UNSUPPORTED). */
 typedef struct ptored_grad {
     const void* data;
     void* out;      /* where the scaled gradient goes; may be data itself */

@@ -1,0 +1,42 @@
+"""What the host code of the step's operators hands to launches, under
+AddressSanitizer and UndefinedBehaviorSanitizer, on the CPU (no GPU, no HIP
+runtime): ``tests/sanitize/step_launches.cpp`` makes the calls with made-up
+addresses and looks at what ``tests/sanitize/step_stub.cpp`` recorded.
+"""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "cross_rank_collective_amd", "csrc")
+HERE = os.path.join(ROOT, "tests", "sanitize")
+ROCM_INCLUDE = "/opt/rocm/include"
+SAN = ["-g", "-O1", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
+       "-fno-sanitize-recover=all"]
+
+pytestmark = pytest.mark.skipif(
+    shutil.which("g++") is None or not os.path.isdir(os.path.join(ROCM_INCLUDE, "hip")),
+    reason="needs g++ and the HIP headers")
+
+
+@pytest.fixture(scope="module")
+def program(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("step_launches") / "run")
+    cmd = ["g++", "-std=c++17", "-Wall", "-Wextra", *SAN, "-D__HIP_PLATFORM_AMD__",
+           f"-I{ROCM_INCLUDE}", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}", f"-I{HERE}",
+           os.path.join(CSRC, "step", "step_host.cpp"), os.path.join(HERE, "step_stub.cpp"),
+           os.path.join(HERE, "step_launches.cpp"), "-o", exe]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    return exe
+
+
+@pytest.mark.parametrize("name", ["products", "layers", "gradients"])
+def test_launches(program, name):
+    env = {**os.environ, "ASAN_OPTIONS": "detect_leaks=0:halt_on_error=1",
+           "UBSAN_OPTIONS": "halt_on_error=1:print_stacktrace=1"}
+    res = subprocess.run([program, name], capture_output=True, text=True, timeout=120, env=env)
+    assert res.returncode == 0, res.stdout + res.stderr

@@ -54,7 +54,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
-constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer resource: reads as zeros
+constexpr uint32_t kNowhere = 0x80000010u;  // past every buffer resource, 16 bytes before it too: reads as zeros
 
 // Address of LDS memory as the hardware takes it.
 __device__ __forceinline__ uint32_t lds_address(const char* p) {
@@ -181,36 +181,36 @@ struct Side {
             each(std::true_type{});
     }
 
-    // The same to registers.  `extent`: elements of the rows that chunks lie in.
+    // The same to registers, without a branch: after one, every wait for a load
+    // would be one for all that are younger too (501 x 1003 x 2501 f16 27.5 us).
+    // SHORT: one operand's rows, of `extent` elements, do not hold a chunk; both come
+    // element by element.
+    template <bool SHORT>
     __device__ __forceinline__ void load_held(Held& h, const char* p, const char* p2, int left,
                                               int64_t extent) const {
         const rsrc_t r = row_rsrc(p - kBack, 0x7FFFFFFF), r2 = HALVES ? row_rsrc(p2 - kBack, 0x7FFFFFFF) : r;
-        h.by = 0;
-        h.cut = false;
-        if (__builtin_expect(left >= kDepth && extent >= V, 1)) {
-#pragma unroll
-            for (int q = 0; q < kLoads; ++q)
-                h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(second(q) ? r2 : r, (int)place<false>(q, left),
-                                                               (int)more(q), 0);
-        } else if (extent >= V) {
+        if constexpr (!SHORT) {
             // of a chunk that the row's end cuts, what ends with the row
-            if (LAYOUT == kAlong && depth < left) h.by = max(depth + V - left, 0);
-            h.cut = LAYOUT == kAlong;
+            h.by = LAYOUT == kAlong && depth < left ? max(depth + V - left, 0) : 0;
+            h.cut = LAYOUT == kAlong && left < kDepth;
 #pragma unroll
             for (int q = 0; q < kLoads; ++q) {
-                const uint32_t at = place<true>(q, left);
+                const uint32_t at = off[LAYOUT == kAlong ? q : 0] - h.by * ES;
                 h.w[q] = __builtin_amdgcn_raw_buffer_load_b128(
-                    second(q) ? r2 : r, (int)(at == kNowhere ? at : at - h.by * ES), (int)more(q), 0);
+                    second(q) ? r2 : r,
+                    (int)((LAYOUT == kAlong ? depth : depth + q * kRows) < left ? at : kNowhere), (int)more(q), 0);
             }
         } else {
-            // the rows' only chunks, element by element
+            h.by = 0;
+            h.cut = false;
+            const int64_t inside = LAYOUT == kAlong ? left - depth : extent;
 #pragma unroll
             for (int q = 0; q < kLoads; ++q) {
                 const uint32_t from = place<true>(q, left);
                 uint32_t w[4] = {};
 #pragma unroll
-                for (int i = 0; i < V - 1; ++i) {
-                    const int at = (int)(i >= extent || from == kNowhere ? kNowhere : from + i * ES);
+                for (int i = 0; i < V; ++i) {
+                    const int at = (int)(i < inside && from != kNowhere ? from + i * ES : kNowhere);
                     if constexpr (ES == 4)
                         w[i] = __builtin_amdgcn_raw_buffer_load_b32(second(q) ? r2 : r, at, (int)more(q), 0);
                     else
@@ -366,7 +366,8 @@ __device__ __forceinline__ void add_chunk(const char* p, float* v, int64_t n) {
 enum : int {
     kDirect = 0,  // loaded straight into it
     kHeld = 1,    // through registers
-    kSplit = 2    // through registers, F32 as three bfloat16
+    kSplit = 2,   // through registers, F32 as three bfloat16
+    kShort = 3    // through registers, element by element
 };
 template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, int HOW>
 __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
@@ -463,15 +464,15 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     // extents of the rows that chunks lie in
     const int64_t ea = LA == kAlong ? a.k : a.m, eb = LB == kAlong ? a.k : a.n;
     // Registers: the steps after those in the LDS, two where they fit.
-    constexpr int kSets = DIRECT ? 1 : TM * TN > 4 ? 1 : 2;
+    constexpr int kSets = DIRECT || HOW == kShort ? 1 : TM * TN > 4 ? 1 : 2;
     typename A::Held ha[kSets];
     typename B::Held hb[kSets];
     auto hold = [&](auto which_set) {
         constexpr int set = decltype(which_set)::value;
         // past the last step the rows are over: zeros from nowhere
         const int n = remain(left, loaded < steps);
-        sa.load_held(ha[set], pa, pa, n, ea);
-        sb.load_held(hb[set], pb, pb2, n, eb);
+        sa.template load_held<HOW == kShort>(ha[set], pa, pa, n, ea);
+        sb.template load_held<HOW == kShort>(hb[set], pb, pb2, n, eb);
         advance();
     };
     // The next step to a buffer, in two halves.  Past the last one zeros, from
@@ -769,6 +770,8 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
             threads = 512;
             if constexpr (DT != PTORED_F32) return kFailed;
             else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 2, 2, 2, 128, 2, kSplit>);
+        } else if (a.shape == kTileShort) {
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kShort>);
         } else if (!a.direct) {
             k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kHeld>);
             if constexpr (DT != PTORED_F32) {

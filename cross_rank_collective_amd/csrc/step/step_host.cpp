@@ -119,12 +119,17 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         s.tiles_m = 1;
         const int64_t features = s.shape == kFew64 ? 32 : 16;
         s.tiles_n = (n + features - 1) / features;
-        // A workgroup takes 37 bytes of the weights a ns, the memory 5500 for all.
-        // (8192 columns x 2048 features, 1 token: 19 us in 128 workgroups.)
+        // A compute unit takes 37 bytes of the weights a ns, the memory 5500 for all,
+        // the same for each unit that still has a workgroup: those that have one more
+        // than the others go on alone.  (1 token, f32, 5440 columns: 4096 features
+        // 35 us, 5056 56 in 316 workgroups, 6144 57, 8192 63; 8192 columns x 2048
+        // features, 128 workgroups: 19.)
         const int64_t units = k * es / 256;  // that waves share
-        const double bytes = 2.0 * (double)features * (double)k * es;
         for (int64_t splits = 1; splits <= 16 && (splits == 1 || units >= 8 * splits); splits *= 2) {
-            const double us = std::max(bytes / (double)splits / 37e3, bytes * (double)s.tiles_n / 5.5e6) +
+            const double bytes = 2.0 * (double)features * (double)k * es / (double)splits;
+            const int64_t groups = s.tiles_n * splits, more = groups % 256;
+            const double us = (double)(groups / 256) * bytes * 256 / 5.5e6 +
+                              (more > 0 ? bytes * std::max(1 / 37e3, (double)more / 5.5e6) : 0.0) +
                               (splits > 1 ? 4.0 + join * (double)splits : 0.0);
             if (best >= 0 && us >= best) continue;
             best = us;
@@ -156,6 +161,12 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         }
     };
     const int64_t half = kind == kForward ? 2 : 1;  // a tile's columns are those of two weights
+    // the elements that operands' rows hold
+    const int64_t least = kind == kForward ? k : std::min(n, kind == kInput ? k : m);
+    if (least * es < 16) {
+        look({kTileShort, 128, 128 / half, 512, 5, 2.0, 4.0});
+        return s;
+    }
     if (direct) {
         look({kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.0, f32 ? 3.9 : 1.1});
         look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.85, f32 ? 2.0 : 0.85});

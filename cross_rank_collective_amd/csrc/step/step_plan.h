@@ -77,9 +77,10 @@ enum : int {
     kTile32x128 = 5,   // kInput: 32 tokens x 128 columns, 4 waves
     kTile64x128 = 6,   // 64 x 128, 4 waves, two or (not aligned) three workgroups a compute unit
     kTileSplit = 7,    // 256 x 128, 8 waves, F32 as three bfloat16
-    kFew16 = 8,        // kForward of up to 16 tokens
-    kFew32 = 9,        // 32 tokens; F32
-    kFew64 = 10        // 64 tokens; F32
+    kTileShort = 8,    // 128 x 128, 4 waves, rows that do not hold 16 bytes
+    kFew16 = 9,        // kForward of up to 16 tokens
+    kFew32 = 10,       // 32 tokens; F32
+    kFew64 = 11        // 64 tokens; F32
 };
 constexpr int kStepBytes = 128;  // of each row along k that a step takes
 

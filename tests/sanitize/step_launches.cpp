@@ -43,6 +43,7 @@ Tile tile_of(int shape) {
         case kTile128x32: return {128, 64, true, true, false, true};
         case kTile32x128: return {32, 128, true, true, true, true};
         case kTile64x128: return {64, 128, true, true, true, true};
+        case kTileShort: return {128, 128, true, true, true, false};
         default: return {256, 128, true, false, true, true};  // kTileSplit
     }
 }
@@ -69,6 +70,8 @@ int look(const Product& p, int64_t workspace) {
     const Tile t = tile_of(a.shape);
     EXPECT(p.dtype == PTORED_F32 ? t.f32 : t.narrow, "shape %d of type %d", a.shape, p.dtype);
     EXPECT(a.direct ? t.direct : t.held, "shape %d, direct %d", a.shape, a.direct);
+    const int64_t least = p.kind == kForward ? a.k : std::min(a.n, p.kind == kInput ? a.k : a.m);
+    EXPECT((least * es < 16) == (a.shape == kTileShort), "rows of %lld elements", (long long)least);
     EXPECT(p.kind == kInput || a.shape != kTile32x128, "kind");
     EXPECT(p.kind == kForward || (a.shape != kTile64 && a.shape != kTile128x32), "kind");
     EXPECT(p.kind != kWeight || a.shape != kTile64x128, "kind");

@@ -369,8 +369,14 @@ enum : int {
     kSplit = 2,   // through registers, F32 as three bfloat16
     kShort = 3    // through registers, element by element
 };
-template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, int HOW>
-__global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
+template <int WM, int WN, int TM, int TN, int STEP, int HOW>
+constexpr int product_bytes() {  // a buffer in the LDS
+    return (WM * TM + WN * TN) * 32 * STEP * (HOW == kSplit ? 3 : 2) / 2;
+}
+// Workgroup `id` of a product.  again(): the arguments where they are not kept in
+// registers.
+template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, int HOW, typename F>
+__device__ __forceinline__ void product_body(const ProductArgs& a, int id, char* lds, F again) {
     constexpr bool DIRECT = HOW == kDirect, SPLIT = HOW == kSplit;
     static_assert(!SPLIT || DT == PTORED_F32, "planes of F32");
     constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
@@ -389,7 +395,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     constexpr int kLoads = DIRECT ? A::kLoads + B::kLoads : 0;  // of a step that barriers wait for
     static_assert((NS - 1) * kLoads <= 63, "as far as the hardware counts");
     constexpr int kCols = kPair ? BN / 2 : BN;  // of the output
-    __shared__ __attribute__((aligned(1024))) char lds[NS * kBytes];
+    static_assert(kBytes == product_bytes<WM, WN, TM, TN, STEP, HOW>(), "the LDS");
 
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -398,7 +404,6 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     // the order in which 4 rows of tiles advance together, so that its cache
     // serves most reads of both operands.
     const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.outs * a.splits;
-    int id = (int)blockIdx.x;
     {
         const int die = id % 8, each = total / 8, rest = total % 8;
         id = die * each + (die < rest ? die : rest) + id / 8;
@@ -614,7 +619,7 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     float* const area = reinterpret_cast<float*>(lds) + wave * ((kPair ? 2 : 1) * kArea);
     // the arguments read again: nothing that only this end needs stays in registers
     // over the steps
-    const auto& z = args_again<ProductArgs>();
+    const ProductArgs& z = again();
     const int64_t tile_col = n0 + wn * (kBlocks * 32);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -692,12 +697,34 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
     }
 }
 
+template <int DT, int KIND, int WM, int WN, int TM, int TN, int STEP, int NS, int HOW>
+__global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs a) {
+    __shared__ __attribute__((aligned(1024))) char lds[NS * product_bytes<WM, WN, TM, TN, STEP, HOW>()];
+    product_body<DT, KIND, WM, WN, TM, TN, STEP, NS, HOW>(
+        a, (int)blockIdx.x, lds, []() -> const ProductArgs& { return args_again<ProductArgs>(); });
+}
+
+// The input's gradient and the weights' in one launch, in tiles of 128: either
+// alone leaves compute units idle where the matrices are small (5467 tokens, 655
+// columns, 324 features, bf16: 23 and 22 us one after the other).
+template <int DT, int HOW>
+__global__ __launch_bounds__(256) void product_both_kernel(const ProductPair p) {
+    __shared__ __attribute__((aligned(1024))) char lds[2 * product_bytes<2, 2, 2, 2, 128, HOW>()];
+    const int id = (int)blockIdx.x;
+    if (id < p.first)
+        product_body<DT, kWeight, 2, 2, 2, 2, 128, 2, HOW>(
+            p.weight, id, lds, []() -> const ProductArgs& { return args_again<ProductPair>().weight; });
+    else
+        product_body<DT, kInput, 2, 2, 2, 2, 128, 2, HOW>(
+            p.input, id - p.first, lds, []() -> const ProductArgs& { return args_again<ProductPair>().input; });
+}
+
 // out (+)= the splits' sums, or the forward pass's outputs from them.  A workgroup
 // takes 64 times 4 columns of a row, 4 threads each for every fourth split,
 // joined in the LDS in a fixed order.
 constexpr int kJoinLanes = 64, kJoinGroups = 4;
 template <int DT, int KIND>
-__global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(const ProductArgs a) {
+__device__ __forceinline__ void product_join(const ProductArgs& a) {
     using E = Elem<DT>;
     constexpr int kSums = KIND == kForward ? 2 : 1;  // g and u
     __shared__ f32x4 part[kSums][kJoinGroups][kJoinLanes];
@@ -746,6 +773,53 @@ __global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(c
         }
         __syncthreads();
     }
+}
+
+template <int DT, int KIND>
+__global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_join_kernel(const ProductArgs a) {
+    product_join<DT, KIND>(a);
+}
+// Those of either product that has splits.
+template <int DT>
+__global__ __launch_bounds__(kJoinLanes* kJoinGroups) void product_both_join_kernel(const ProductPair p) {
+    if (blockIdx.z == 0)
+        product_join<DT, kWeight>(p.weight);
+    else
+        product_join<DT, kInput>(p.input);
+}
+
+// The joining kernel's workgroups.
+inline dim3 product_joins(const ProductArgs& a, int kind) {
+    const int64_t rows = a.m * (kind == kForward ? 1 : a.outs);
+    return dim3((uint32_t)((a.n + 4 * kJoinLanes - 1) / (4 * kJoinLanes)),
+                (uint32_t)(rows < 32768 ? rows : 32768));
+}
+
+template <int DT>
+int product_both_launch(const ProductPair& p, hipStream_t stream) {
+    void* args[] = {const_cast<ProductPair*>(&p)};
+    const ProductArgs &w = p.weight, &x = p.input;
+    const void* k = w.direct && x.direct ? reinterpret_cast<const void*>(product_both_kernel<DT, kDirect>)
+                                         : reinterpret_cast<const void*>(product_both_kernel<DT, kHeld>);
+    const uint32_t grid = (uint32_t)p.first + (uint32_t)x.tiles_m * (uint32_t)x.tiles_n * (uint32_t)x.splits;
+    if (hipLaunchKernel(k, dim3(grid), dim3(256), args, 0, stream) != hipSuccess) return kFailed;
+    if (w.splits > 1 && x.splits > 1) {
+        const dim3 a = product_joins(w, kWeight), b = product_joins(x, kInput);
+        const dim3 both(a.x > b.x ? a.x : b.x, a.y > b.y ? a.y : b.y, 2);
+        return hipLaunchKernel(reinterpret_cast<const void*>(product_both_join_kernel<DT>), both,
+                               dim3(kJoinLanes * kJoinGroups), args, 0, stream) == hipSuccess
+                   ? kOk
+                   : kFailed;
+    }
+    const bool input = x.splits > 1;
+    if (!input && w.splits == 1) return kOk;
+    void* one[] = {const_cast<ProductArgs*>(input ? &x : &w)};
+    k = input ? reinterpret_cast<const void*>(product_join_kernel<DT, kInput>)
+              : reinterpret_cast<const void*>(product_join_kernel<DT, kWeight>);
+    return hipLaunchKernel(k, input ? product_joins(x, kInput) : product_joins(w, kWeight),
+                           dim3(kJoinLanes * kJoinGroups), one, 0, stream) == hipSuccess
+               ? kOk
+               : kFailed;
 }
 
 template <int DT, int KIND>
@@ -801,10 +875,7 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
             return kFailed;
     }
     if (a.splits == 1) return kOk;
-    const int64_t rows = a.m * (KIND == kForward ? 1 : a.outs);
-    const dim3 joins((uint32_t)((a.n + 4 * kJoinLanes - 1) / (4 * kJoinLanes)),
-                     (uint32_t)(rows < 32768 ? rows : 32768));
-    return hipLaunchKernel(reinterpret_cast<const void*>(product_join_kernel<DT, KIND>), joins,
+    return hipLaunchKernel(reinterpret_cast<const void*>(product_join_kernel<DT, KIND>), product_joins(a, KIND),
                            dim3(kJoinLanes * kJoinGroups), args, 0, stream) == hipSuccess
                ? kOk
                : kFailed;

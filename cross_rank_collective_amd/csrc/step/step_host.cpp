@@ -75,9 +75,15 @@ bool direct_of(const ptored_rows& r, int64_t rows, int64_t cols, int es) {
 struct ProductShape {
     int64_t tiles_m, tiles_n, splits, steps_per_split;
     int shape, waves;
+    double us;  // estimated
 };
 
 constexpr int64_t kMaxTiles = int64_t(1) << 22;
+
+// Whether an operand's rows are shorter than 16 bytes.
+bool short_rows(int kind, int64_t m, int64_t n, int64_t k, int es) {
+    return (kind == kForward ? k : std::min(n, kind == kInput ? k : m)) * es < 16;
+}
 
 // A tile's rows and columns of the output, and its time: base + step us for each
 // of its steps, `slots` tiles at once, or base + alone where no compute unit has
@@ -87,6 +93,11 @@ struct TileCost {
     int64_t rows, cols, slots;
     double base, alone, step;
 };
+
+TileCost tile128(int64_t half, bool f32, bool direct) {
+    if (direct) return {kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.0, f32 ? 3.9 : 1.1};
+    return {kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.15, f32 ? 3.9 : 1.35};
+}
 
 // Tiles and splits of a product, by estimated time; for kInput k is that of each
 // of the two pairs.  Splits share a tile's steps among several workgroups, each
@@ -132,7 +143,7 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
                               (more > 0 ? bytes * std::max(1 / 37e3, (double)more / 5.5e6) : 0.0) +
                               (splits > 1 ? 4.0 + join * (double)splits : 0.0);
             if (best >= 0 && us >= best) continue;
-            best = us;
+            best = s.us = us;
             s.splits = splits;
         }
         // waves to share the columns: 2048 fill the chip
@@ -152,7 +163,7 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
             const double us = rounds * (c.base + (tiles * splits <= 256 ? c.alone : c.step) * (double)per) +
                               (splits > 1 ? 4.0 + join * (double)splits : 0.0);
             if (best >= 0 && us >= best) continue;
-            best = us;
+            best = s.us = us;
             s.shape = c.shape;
             s.tiles_m = tm;
             s.tiles_n = tn;
@@ -161,21 +172,19 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         }
     };
     const int64_t half = kind == kForward ? 2 : 1;  // a tile's columns are those of two weights
-    // the elements that operands' rows hold
-    const int64_t least = kind == kForward ? k : std::min(n, kind == kInput ? k : m);
-    if (least * es < 16) {
+    if (short_rows(kind, m, n, k, es)) {
         look({kTileShort, 128, 128 / half, 512, 5, 2.0, 4.0});
         return s;
     }
     if (direct) {
-        look({kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.0, f32 ? 3.9 : 1.1});
+        look(tile128(half, f32, true));
         look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.85, f32 ? 2.0 : 0.85});
         if (kind != kWeight) look({kTile64x128, 64, 128 / half, 512, 5, f32 ? 1.0 : 0.6, f32 ? 2.0 : 0.9});
         if (!f32) look({kTile256, 256, 256 / half, 256, 8, 1.7, 1.7});
         if (kind == kForward && !f32) look({kTile64, 64, 32, 256, 5, 0.48, 0.48});
         if (kind == kForward) look({kTile128x32, 128, 32, 256, 5, f32 ? 1.2 : 0.56, f32 ? 1.2 : 0.56});
     } else {
-        look({kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.15, f32 ? 3.9 : 1.35});
+        look(tile128(half, f32, false));
         if (kind != kWeight) look({kTile64x128, 64, 128 / half, 768, 5, f32 ? 1.0 : 0.95, f32 ? 3.0 : 1.75});
         if (!f32) look({kTile256, 256, 256 / half, 256, 8, 2.1, 2.1});
     }
@@ -185,6 +194,61 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
 }
 int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs) {
     return s.splits > 1 ? s.splits * outs * m * pitch_of(n) * 4 : 0;  // kForward: 2 outs
+}
+// Both gradients in one launch of tiles of 128: splits that give all workgroups
+// about the same number of steps.  Taken where its time is below 0.9 of that of two
+// launches, whose estimates are up to a fifth above what larger tiles take.  One
+// launch and two, us (with the slopes): 2048 tokens x 1024 x 1024 bf16 36, 53; 512
+// x 1001 x 1003 30, 44; 6 x 299 x 1855 18, 24; 1024 x 512 x 512 f32 39, 53; 1024 x
+// 1536 x 4096 bf16 (0.92 of the estimate) 94, 84.
+struct BothShape {
+    ProductShape input, weight;
+    double us;  // negative: not offered
+};
+BothShape both_shape(int64_t rows, int64_t cols, int64_t wide, int outs, int dtype, bool direct) {
+    const bool f32 = dtype == PTORED_F32;
+    const int es = esize_of(dtype);
+    BothShape best{};
+    best.us = -1;
+    if (rows == 0 || cols == 0 || wide == 0 || outs == 0 || short_rows(kInput, rows, cols, wide, es) ||
+        short_rows(kWeight, wide, cols, rows, es))
+        return best;
+    const int64_t depth = kStepBytes / es;
+    const TileCost c = tile128(1, f32, direct);
+    auto tiles = [](int64_t n) { return (n + 127) / 128; };
+    const int64_t steps_in = (wide + depth - 1) / depth * 2, steps_w = (rows + depth - 1) / depth;
+    const int64_t tiles_in = tiles(rows) * tiles(cols), tiles_w = tiles(wide) * tiles(cols) * outs;
+    if (tiles_in + tiles_w > 4 * c.slots) return best;
+    const int64_t most = std::max(steps_in, steps_w);
+    for (int64_t target = 4;; target += std::max<int64_t>(1, target / 4)) {
+        auto shape = [&](int64_t m, int64_t n, int64_t steps) {
+            ProductShape s{};
+            s.shape = kTile128;
+            s.tiles_m = tiles(m);
+            s.tiles_n = tiles(n);
+            s.splits = (steps + target - 1) / target;
+            s.steps_per_split = (steps + s.splits - 1) / s.splits;
+            s.splits = (steps + s.steps_per_split - 1) / s.steps_per_split;
+            return s;
+        };
+        const ProductShape in = shape(rows, cols, steps_in), w = shape(wide, cols, steps_w);
+        const int64_t groups = tiles_in * in.splits + tiles_w * w.splits;
+        const double longest = (double)std::max(in.steps_per_split, w.steps_per_split);
+        const double share = (double)(tiles_in * steps_in + tiles_w * steps_w) / (double)c.slots;
+        double us = groups <= 256 ? c.base + c.alone * longest
+                                  : c.base * (double)((groups + c.slots - 1) / c.slots) +
+                                        c.step * std::max(longest, share);
+        const double sums = (in.splits > 1 ? (double)(in.splits * rows) : 0.0) +
+                            (w.splits > 1 ? (double)(w.splits * outs * wide) : 0.0);
+        if (sums > 0) us += 4.0 + sums * (double)cols * 8 / 4e6;
+        if (best.us < 0 || us < best.us) best = {in, w, us};
+        if (target >= most) break;
+    }
+    return best;
+}
+// (the input's partial sums begin where the weights' end)
+int64_t both_workspace(const BothShape& b, int64_t rows, int64_t cols, int64_t wide, int outs) {
+    return product_workspace(b.weight, wide, cols, outs) + product_workspace(b.input, rows, cols, 1);
 }
 bool launchable(const ProductShape& s, int outs) {
     return s.tiles_m <= kMaxTiles && s.tiles_n <= kMaxTiles &&
@@ -586,13 +650,16 @@ extern "C" int ptored_gated_ffn_backward_workspace(int64_t rows, int64_t cols, i
     if (bytes == nullptr || !shape_ok(rows, cols) || !shape_ok(rows, wide) || !shape_ok(wide, cols))
         return PTORED_ERR_INVALID_ARG;
     if (!float_type(dtype)) return PTORED_ERR_UNSUPPORTED;
-    int64_t most = 0;  // of any alignment and any choice of gradients; products take turns
+    int64_t most = 0;  // of any alignment and any choice of gradients; products take turns, or both are one launch
     for (const bool direct : {false, true}) {
         most = std::max(most, product_workspace(product_shape(kInput, rows, cols, wide, 1, dtype, direct),
                                                 rows, cols, 1));
-        for (const int outs : {1, 2})
+        for (const int outs : {1, 2}) {
             most = std::max(most, product_workspace(product_shape(kWeight, wide, cols, rows, outs, dtype,
                                                                   direct), wide, cols, outs));
+            const BothShape both = both_shape(rows, cols, wide, outs, dtype, direct);
+            if (both.us >= 0) most = std::max(most, both_workspace(both, rows, cols, wide, outs));
+        }
     }
     *bytes = most;
     return PTORED_OK;
@@ -641,8 +708,13 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         product_shape(kWeight, p.wide, p.cols, p.rows, std::max(outs, 1), p.dtype, direct_w);
     if ((input && !launchable(si, 1)) || (outs > 0 && !launchable(sw, outs)))
         return PTORED_ERR_UNSUPPORTED;
-    const int64_t need = std::max(input ? product_workspace(si, p.rows, p.cols, 1) : 0,
-                                  outs > 0 ? product_workspace(sw, p.wide, p.cols, outs) : 0);
+    const bool direct_both = direct_in && direct_w;
+    const BothShape sb = input && outs > 0 ? both_shape(p.rows, p.cols, p.wide, outs, p.dtype, direct_both)
+                                           : BothShape{{}, {}, -1};
+    const bool both = sb.us >= 0 && sb.us < 0.9 * (si.us + sw.us);
+    const int64_t need = both ? both_workspace(sb, p.rows, p.cols, p.wide, outs)
+                              : std::max(input ? product_workspace(si, p.rows, p.cols, 1) : 0,
+                                         outs > 0 ? product_workspace(sw, p.wide, p.cols, outs) : 0);
     if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
         return PTORED_ERR_INVALID_ARG;
     if (need > 0) b.vec(io->workspace, need, 16, true);
@@ -655,8 +727,9 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         const int rc = PTORED_BY_TYPE(product_slope, p.dtype, a, stream);
         if (rc != ptored::block::kOk) return status_of(rc);
     }
+    ProductPair pair{};
     if (input && p.rows > 0 && p.cols > 0) {
-        ProductArgs a{};
+        ProductArgs& a = pair.input;
         set_a(a, 0, operand(io->dgate, p.rows, p.wide), es);
         set_a(a, 1, operand(io->dup, p.rows, p.wide), es);
         set_b(a, 0, operand(wg, p.wide, p.cols), es);
@@ -669,12 +742,15 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         a.out_f32 = p.dtype == PTORED_F32;
         a.ws = static_cast<float*>(io->workspace);
         a.ws_ld = pitch_of(p.cols);
-        set_shape(a, si, direct_in);
-        const int rc = PTORED_BY_TYPE(product_input, p.dtype, a, stream);
+        if (both) a.ws += product_workspace(sb.weight, p.wide, p.cols, outs) / 4;
+        set_shape(a, both ? sb.input : si, both ? direct_both : direct_in);
+    }
+    if (input && !both && p.rows > 0 && p.cols > 0) {
+        const int rc = PTORED_BY_TYPE(product_input, p.dtype, pair.input, stream);
         if (rc != ptored::block::kOk) return status_of(rc);
     }
     if (outs > 0 && p.wide > 0 && p.cols > 0 && !(p.rows == 0 && io->accumulate)) {
-        ProductArgs a{};
+        ProductArgs& a = pair.weight;
         int n = 0;
         for (int i = 0; i < 2; ++i) {
             const ptored_rows& dw = i == 0 ? io->dw_gate : io->dw_up;
@@ -691,8 +767,10 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         a.accumulate = io->accumulate != 0;
         a.ws = static_cast<float*>(io->workspace);
         a.ws_ld = pitch_of(p.cols);
-        set_shape(a, sw, direct_w);
-        const int rc = PTORED_BY_TYPE(product_weight, p.dtype, a, stream);
+        set_shape(a, both ? sb.weight : sw, both ? direct_both : direct_w);
+        pair.first = a.tiles_m * a.tiles_n * a.outs * a.splits;
+        const int rc = both ? PTORED_BY_TYPE(product_both, p.dtype, pair, stream)
+                            : PTORED_BY_TYPE(product_weight, p.dtype, a, stream);
         if (rc != ptored::block::kOk) return status_of(rc);
     }
     return PTORED_OK;

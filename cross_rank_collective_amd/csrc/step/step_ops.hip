@@ -30,6 +30,9 @@ int PTORED_NAMED(product_input_)(const ProductArgs& a, hipStream_t s) {
 int PTORED_NAMED(product_weight_)(const ProductArgs& a, hipStream_t s) {
     return product_launch<PTORED_INST_DT, kWeight>(a, s);
 }
+int PTORED_NAMED(product_both_)(const ProductPair& p, hipStream_t s) {
+    return product_both_launch<PTORED_INST_DT>(p, s);
+}
 int PTORED_NAMED(product_slope_)(const SlopeArgs& a, hipStream_t s) {
     return slope_launch<PTORED_INST_DT>(a, s);
 }

@@ -67,6 +67,13 @@ struct ProductArgs {
     int32_t direct;      // every row and column range is whole aligned chunks
 };
 
+// Both gradients of a call in one launch, in tiles kTile128: the weights'
+// workgroups first.  A split product's partial sums are behind the other's.
+struct ProductPair {
+    ProductArgs weight, input;
+    int32_t first;  // workgroups of the weights'
+};
+
 // Tiles of the products.
 enum : int {
     kTile128 = 0,      // 128 x 128, 4 waves, two workgroups a compute unit
@@ -154,6 +161,7 @@ int grad_scale(const GradList&, hipStream_t);
     int product_forward_##T(const ProductArgs&, hipStream_t);\
     int product_input_##T(const ProductArgs&, hipStream_t);  \
     int product_weight_##T(const ProductArgs&, hipStream_t); \
+    int product_both_##T(const ProductPair&, hipStream_t);   \
     int product_slope_##T(const SlopeArgs&, hipStream_t);
 PTORED_STEP_LAUNCHES(f32)
 PTORED_STEP_LAUNCHES(bf16)

@@ -56,7 +56,9 @@ int look(const Product& p, int64_t workspace) {
     const int64_t outs = p.kind == kForward ? 2 : a.outs;
     EXPECT(a.splits >= 1, "splits");
     if (a.splits > 1)
-        EXPECT(a.ws_ld % 4 == 0 && a.ws_ld >= a.n && a.splits * outs * a.m * a.ws_ld * 4 <= workspace,
+        EXPECT(a.ws_ld % 4 == 0 && a.ws_ld >= a.n &&
+                   reinterpret_cast<char*>(a.ws) + a.splits * outs * a.m * a.ws_ld * 4 <=
+                       static_cast<char*>(fake(12)) + workspace,
                "%d splits of %lld x %lld", a.splits, (long long)a.m, (long long)a.n);
     if (a.shape >= kFew16) {
         const int64_t tokens = a.shape == kFew16 ? 16 : a.shape == kFew32 ? 32 : 64;
@@ -103,6 +105,7 @@ int products() {
         if (kind == 1) n = n / 8 * 8;
         return std::max<int64_t>(1, n);
     };
+    int both = 0;
     for (int i = 0; i < 20000; ++i) {
         const int dtype = (int)(rng() % 3);
         const int64_t T = size(70000), D = size(20000), F = size(20000), pad = (int64_t)(rng() % 3) * 4;
@@ -140,7 +143,16 @@ int products() {
         EXPECT(g_seen.products.size() == (size_t)((which & 1) + (which > 1)) && g_seen.others == 1, "launches");
         for (const Product& q : g_seen.products)
             if (look(q, need)) return 1;
+        if (g_seen.firsts.empty()) continue;
+        ++both;
+        const ProductArgs &w = g_seen.products[0].a, &d = g_seen.products[1].a;
+        EXPECT(g_seen.products.size() == 2 && w.shape == kTile128 && d.shape == kTile128 && w.direct == d.direct,
+               "both");
+        EXPECT(g_seen.firsts[0] == w.tiles_m * w.tiles_n * w.outs * w.splits, "the weights' workgroups");
+        if (w.splits > 1 && d.splits > 1)
+            EXPECT(d.ws >= w.ws + w.splits * w.outs * w.m * w.ws_ld, "partial sums of both");
     }
+    EXPECT(both > 1000, "%d launches of both gradients", both);
     return 0;
 }
 

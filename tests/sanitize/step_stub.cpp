@@ -23,6 +23,12 @@ Launches g_seen;
     PTORED_PRODUCT(kForward, forward, T, dt)                                             \
     PTORED_PRODUCT(kInput, input, T, dt)                                                 \
     PTORED_PRODUCT(kWeight, weight, T, dt)                                               \
+    int product_both_##T(const ProductPair& p, hipStream_t) {                            \
+        g_seen.products.push_back({kWeight, dt, p.weight});                              \
+        g_seen.products.push_back({kInput, dt, p.input});                                \
+        g_seen.firsts.push_back(p.first);                                                \
+        return kOk;                                                                      \
+    }                                                                                    \
     int product_slope_##T(const SlopeArgs&, hipStream_t) { return ++g_seen.others, kOk; }
 PTORED_STUBS(f32, PTORED_F32)
 PTORED_STUBS(bf16, PTORED_BF16)

@@ -14,6 +14,7 @@ struct Product {
 };
 struct Launches {
     std::vector<Product> products;
+    std::vector<int> firsts;  // of launches of both gradients: workgroups of the weights'
     std::vector<LayerGradArgs> layers;
     std::vector<GradPack> packs;
     std::vector<GradList> sums, joins, scales;

@@ -41,7 +41,15 @@ __device__ __forceinline__ f32x4 multiply16(u32x4 a, u32x4 b, f32x4 acc) {
 }
 
 // Tokens in TB blocks of 16.  The columns fill at least one lane's 16 bytes.
-template <int DT, int W, int FB, int TB, int U>
+//
+// ODD: some row of a 16-bit type begins between two words.  16 bytes that begin
+// there take two and a half times as long to load, so a lane loads the four words
+// from the one on that its 16 bytes begin in, and takes the fifth from the next
+// lane; only a unit's last lanes load it (13 tokens x 2545 x 4425 bf16, us: 38 with
+// misaligned loads, 25 with five words a lane, 18 so; in rows of 2546 elements 15).
+// Of the first and the last of a row's words half may be a neighbour's: it is
+// shifted out.
+template <int DT, int W, int FB, int TB, int U, bool ODD>
 __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
     using E = Elem<DT>;
     constexpr int ES = E::kBytes, V = E::V, kStep = 64 / ES, kUnit = U * kStep;
@@ -71,6 +79,37 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
     }
     struct Unit {
         u32x4 g[U][FB], u[U][FB], x[U][TB];
+        uint32_t g4[FB], u4[FB], x4[TB];  // ODD: the words behind, for the rows' last lanes
+    };
+    // bytes from the beginning of the word that a matrix's first element lies in; a
+    // lane's first word and how many bytes of it are others'
+    const auto before = [](const char* p) { return ODD ? (int)(reinterpret_cast<uint64_t>(p) & 2) : 0; };
+    const int bg = before(pg), bu = before(pu), bx = before(px);
+    int wg[FB], wu[FB], wx[TB], sg[FB], su[FB], sx[TB];
+    auto words = [&](int off, int b, int& word, int& shift) {
+        shift = off == kNone ? 0 : (off + b) & 2;
+        word = off == kNone ? kNone : off + b - shift;
+    };
+#pragma unroll
+    for (int i = 0; i < FB; ++i) {
+        words(og[i], bg, wg[i], sg[i]);
+        words(ou[i], bu, wu[i], su[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) words(ox[i], bx, wx[i], sx[i]);
+    auto to_words = [](int bytes, int b) { return ODD ? (bytes + b + 3) & ~3 : bytes; };
+    // Step s of a unit's chunks, `by` bytes on: the fifth word is the first of the lane
+    // 16 on, or of the row's first lane in the next step.
+    const int behind = ((lane + 16) & 63) * 4;
+    auto shifted = [&](auto& v, const auto& end, int s, int i, int by) -> u32x4 {
+        if constexpr (!ODD) return v[s][i];
+        const u32x4 w = v[s][i];
+        uint32_t first = w[0];
+        if (s + 1 < U) first = lane < 16 ? v[s + 1 < U ? s + 1 : s][i][0] : first;
+        uint32_t last = (uint32_t)__builtin_amdgcn_ds_bpermute(behind, (int)first);
+        if (s + 1 == U) last = lane < 48 ? last : end[i];
+        return (u32x4){__builtin_amdgcn_alignbyte(w[1], w[0], by), __builtin_amdgcn_alignbyte(w[2], w[1], by),
+                       __builtin_amdgcn_alignbyte(w[3], w[2], by), __builtin_amdgcn_alignbyte(last, w[3], by)};
     };
     Unit one, two;
     // units without an end in them; this split's among them
@@ -85,18 +124,32 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
     auto load = [&](Unit& to, int unit) {
         const bool in = unit < whole;
         const int from = (first + (unit + turn < whole ? unit + turn : unit + turn - whole)) * (U * 64);
-        const rsrc_t rg = row_rsrc(pg, in ? ng : 0), ru = row_rsrc(pu, in ? nu : 0);
-        const rsrc_t rx = row_rsrc(px, in ? nx : 0);
+        const rsrc_t rg = row_rsrc(pg - bg, in ? to_words(ng, bg) : 0);
+        const rsrc_t ru = row_rsrc(pu - bu, in ? to_words(nu, bu) : 0);
+        const rsrc_t rx = row_rsrc(px - bx, in ? to_words(nx, bx) : 0);
 #pragma unroll
         for (int s = 0; s < U; ++s) {
 #pragma unroll
             for (int i = 0; i < FB; ++i) {
-                to.g[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rg, og[i], from + s * 64, kPolicyKeep);
-                to.u[s][i] = __builtin_amdgcn_raw_buffer_load_b128(ru, ou[i], from + s * 64, kPolicyKeep);
+                to.g[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rg, wg[i], from + s * 64, kPolicyKeep);
+                to.u[s][i] = __builtin_amdgcn_raw_buffer_load_b128(ru, wu[i], from + s * 64, kPolicyKeep);
             }
 #pragma unroll
             for (int i = 0; i < TB; ++i)
-                to.x[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, ox[i], from + s * 64, kPolicyKeep);
+                to.x[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, wx[i], from + s * 64, kPolicyKeep);
+        }
+        if constexpr (ODD) {
+            const int end = from + U * 64 - 48;
+            auto word = [&](rsrc_t r, int off) {
+                return __builtin_amdgcn_raw_buffer_load_b32(r, lane < 48 ? kNone : off, end, kPolicyKeep);
+            };
+#pragma unroll
+            for (int i = 0; i < FB; ++i) {
+                to.g4[i] = word(rg, wg[i]);
+                to.u4[i] = word(ru, wu[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < TB; ++i) to.x4[i] = word(rx, wx[i]);
         }
     };
     f32x4 ag[FB][TB], au[FB][TB];
@@ -106,14 +159,17 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
         for (int j = 0; j < TB; ++j) ag[i][j] = au[i][j] = (f32x4)(0.0f);
     auto multiply = [&](const Unit& v) {
 #pragma unroll
-        for (int s = 0; s < U; ++s)
+        for (int s = 0; s < U; ++s) {
 #pragma unroll
-            for (int i = 0; i < FB; ++i)
+            for (int j = 0; j < TB; ++j) {
+                const u32x4 x = shifted(v.x, v.x4, s, j, sx[j]);
 #pragma unroll
-                for (int j = 0; j < TB; ++j) {
-                    ag[i][j] = multiply16<DT>(v.g[s][i], v.x[s][j], ag[i][j]);
-                    au[i][j] = multiply16<DT>(v.u[s][i], v.x[s][j], au[i][j]);
+                for (int i = 0; i < FB; ++i) {
+                    ag[i][j] = multiply16<DT>(shifted(v.g, v.g4, s, i, sg[i]), x, ag[i][j]);
+                    au[i][j] = multiply16<DT>(shifted(v.u, v.u4, s, i, su[i]), x, au[i][j]);
                 }
+            }
+        }
     };
     // What the units leave, at most U steps, is taken first, a step by each of the
     // first waves.  A chunk that the rows' end cuts is loaded so that it ends with
@@ -196,12 +252,21 @@ __global__ __launch_bounds__(W * 64) void few_kernel(const ProductArgs a) {
 }
 
 template <int DT, int FB, int TB, int U>
-static const void* few_pick(int waves, int& threads) {
-    threads = waves * 64;
+static const void* few_pick(const ProductArgs& a, int& threads) {
+    threads = 512;
     if constexpr (FB == 1 && TB == 1) {
-        if (waves == 16) return reinterpret_cast<const void*>(few_kernel<DT, 16, FB, TB, U>);
+        if constexpr (DT != PTORED_F32) {
+            uint64_t at = reinterpret_cast<uint64_t>(a.a[0]) | (a.m > 1 ? (uint64_t)a.a_ld[0] : 0);
+            for (int i = 0; i < 2; ++i) at |= reinterpret_cast<uint64_t>(a.b[i]) | (uint64_t)a.b_ld[i];
+            // (16 waves leave no registers for the fifth words)
+            if (at & 2) return reinterpret_cast<const void*>(few_kernel<DT, 8, FB, TB, U, true>);
+        }
+        if (a.waves == 16) {
+            threads = 1024;
+            return reinterpret_cast<const void*>(few_kernel<DT, 16, FB, TB, U, false>);
+        }
     }
-    return reinterpret_cast<const void*>(few_kernel<DT, 8, FB, TB, U>);
+    return reinterpret_cast<const void*>(few_kernel<DT, 8, FB, TB, U, false>);
 }
 
 template <int DT>
@@ -209,12 +274,11 @@ int few_launch(const ProductArgs& a, hipStream_t stream) {
     int threads = 0;
     const void* k;
     if (a.shape == kFew16)
-        k = few_pick<DT, 1, 1, 4>(a.waves, threads);
+        k = few_pick<DT, 1, 1, 4>(a, threads);
     else if constexpr (DT != PTORED_F32)
         return kFailed;
     else
-        k = a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a.waves, threads)
-                              : few_pick<DT, 2, 4, 2>(a.waves, threads);
+        k = a.shape == kFew32 ? few_pick<DT, 1, 2, 4>(a, threads) : few_pick<DT, 2, 4, 2>(a, threads);
     void* args[] = {const_cast<ProductArgs*>(&a)};
     return hipLaunchKernel(k, dim3((uint32_t)a.tiles_n, (uint32_t)a.splits), dim3((uint32_t)threads), args, 0,
                            stream) == hipSuccess

@@ -296,6 +296,28 @@ def test_gated_ffn_pitches_of_their_own(rows, dtype):
             r.check("an output")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,wide", [(1, 1024, 40), (3, 257, 17), (13, 2545, 65), (16, 128, 16), (7, 384, 300),
+                                            (1, 9, 3), (16, 4100, 33)])
+def test_gated_ffn_few_rows_between_words(rows, cols, wide, dtype):
+    """Rows of few tokens and of weights that begin between two words, with NaN in
+    the elements that share words with them."""
+    x, wg, wu = ffn_inputs(rows, cols, wide, dtype)
+    want = R.gated_ffn(x, wg, wu, "silu")
+    for pads, leads in (((1, 1, 1), (0, 0, 0)), ((1, 2, 1), (1, 1, 1)), ((2, 1, 3), (0, 1, 1)), ((8, 8, 8), (1, 0, 1))):
+        held = []
+        for t, pad, lead in zip((x, wg, wu), pads, leads):
+            ld = t.shape[1] + pad
+            room = torch.full((lead + t.shape[0] * ld + 8,), math.nan, dtype=dtype, device="cuda")
+            held.append(room[lead:lead + t.shape[0] * ld].view(t.shape[0], ld)[:, :t.shape[1]])
+            held[-1].copy_(t)
+        y, g, u = (Room(rows, wide, dtype, 1) for _ in range(3))
+        crc.gated_ffn(*held, y.t, gate=g.t, up=u.t)
+        for k, v in {"y": y, "gate": g, "up": u}.items():
+            close(v.t, *want[k], k)
+            v.check(k)
+
+
 # ---------------------------------------------------------------- clipping
 
 def grads_of(shapes, dtype, seed=0, scale=1.0):

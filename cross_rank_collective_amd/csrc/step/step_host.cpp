@@ -134,13 +134,19 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         // the same for each unit that still has a workgroup: those that have one more
         // than the others go on alone.  (1 token, f32, 5440 columns: 4096 features
         // 35 us, 5056 56 in 316 workgroups, 6144 57, 8192 63; 8192 columns x 2048
-        // features, 128 workgroups: 19.)
+        // features, 128 workgroups: 19.)  More than 16 tokens in F32 are bound by the
+        // products, 20 and 15.5 bytes a ns, and few features by tiles with splits
+        // (47 tokens, us, kFew64 and tiles: 1792 columns x 256 26, 13; 1024 x 2048 24,
+        // 16; 4096 x 8192 76, 86; 32 tokens, kFew32: 1792 x 256 18, 13; 1536 x 4096
+        // 17, 23).
+        const double rate = s.shape == kFew16 ? 37e3 : s.shape == kFew32 ? 20e3 : 15.5e3;
+        const double base = s.shape == kFew16 ? 0.0 : 6.0;
         const int64_t units = k * es / 256;  // that waves share
         for (int64_t splits = 1; splits <= 16 && (splits == 1 || units >= 8 * splits); splits *= 2) {
             const double bytes = 2.0 * (double)features * (double)k * es / (double)splits;
             const int64_t groups = s.tiles_n * splits, more = groups % 256;
-            const double us = (double)(groups / 256) * bytes * 256 / 5.5e6 +
-                              (more > 0 ? bytes * std::max(1 / 37e3, (double)more / 5.5e6) : 0.0) +
+            const double us = base + (double)(groups / 256) * bytes * std::max(1 / rate, 256 / 5.5e6) +
+                              (more > 0 ? bytes * std::max(1 / rate, (double)more / 5.5e6) : 0.0) +
                               (splits > 1 ? 4.0 + join * (double)splits : 0.0);
             if (best >= 0 && us >= best) continue;
             best = s.us = us;
@@ -150,7 +156,7 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         const int most = s.shape == kFew16 ? 16 : 8;
         s.waves = 8;
         while (s.waves < most && s.waves * s.tiles_n * s.splits < 2048) s.waves *= 2;
-        return s;
+        if (m <= 16) return s;
     }
     auto look = [&](const TileCost& c) {
         const int64_t tm = (m + c.rows - 1) / c.rows, tn = (n + c.cols - 1) / c.cols, tiles = tm * tn * outs;

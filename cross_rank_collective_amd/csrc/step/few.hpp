@@ -10,6 +10,12 @@
 // bytes, the next unit's loads in flight while one is multiplied, and add their
 // sums in the LDS at the end, in a fixed order.  Where few features leave compute
 // units idle, several workgroups share the columns and a second kernel joins them.
+//
+// Measured: 1 token, 4096 columns, 2 x 8192 features, bf16 25 us, 5.4 TB/s (21.7 at
+// the rate of a large copy).  All workgroups at the same column ask the same
+// memory channels: each begins at one of its own (252 MB of weights 57 us, rotated
+// and with the caches' usual policy 44).  8 waves where 16 are not needed to fill
+// the chip (4096 x 8192 29.6, 24.7).
 #pragma once
 
 #include "gated.hpp"

@@ -3,7 +3,9 @@
 //
 //     dg = dy u f'(g),  du = dy f(g)
 //
-// Bound by memory: three matrices in, two out.
+// Bound by memory: three matrices in, two out (8192 x 8192 bf16 115-122 us, 5.5-5.8
+// TB/s).  dg and du are outputs that the products read, rounded to the type: what
+// a training step keeps of them, and what its products in that type would read.
 #pragma once
 
 #include <algorithm>

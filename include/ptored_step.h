@@ -132,8 +132,8 @@ typedef struct ptored_ffn_grad_io {
 int ptored_gated_ffn_backward(const ptored_ffn_params* params, const ptored_ffn_grad_io* io,
                               hipStream_t stream);
 
-/* Bytes of workspace that such a backward pass needs with all gradients; often
- * 0 (no HIP call). */
+/* Bytes of workspace that such a backward pass needs with any of the gradients;
+ * often 0 (no HIP call). */
 int ptored_gated_ffn_backward_workspace(int64_t rows, int64_t cols, int64_t wide, int dtype,
                                         int64_t* bytes);
 

@@ -612,8 +612,12 @@ __device__ __forceinline__ void product_body(const ProductArgs& a, int id, char*
     // Register r of a block is column 8 (r / 4) + 4 (lane / 32) + r % 4 of row lane
     // % 32.  Each wave turns its blocks, 32 rows at a time, in LDS of its own, so
     // that its lanes store whole pieces of rows: from the registers a store reaches
-    // 32 rows, 32 bytes of each.
-    constexpr int kBlocks = kPair ? TN / 2 : TN, kPitch = kBlocks * 32 + 4;
+    // 32 rows, 32 bytes of each.  A row's pieces of 16 bytes change places with
+    // the row, so that a piece's rows lie in different banks.
+    constexpr int kBlocks = kPair ? TN / 2 : TN, kPitch = kBlocks * 32;
+    auto placed = [](int row, int col) {
+        return row * kPitch + ((col >> 2 ^ (kBlocks == 1 ? row >> 1 & 7 : row & 15)) << 2);
+    };
     constexpr int kArea = 32 * kPitch;
     static_assert(WM * WN * (kPair ? 2 : 1) * kArea * 4 <= NS * kBytes, "room for it");
     float* const area = reinterpret_cast<float*>(lds) + wave * ((kPair ? 2 : 1) * kArea);
@@ -630,8 +634,8 @@ __device__ __forceinline__ void product_body(const ProductArgs& a, int id, char*
         for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<f32x4*>(area + j / kBlocks * kArea + (lane & 31) * kPitch +
-                                          j % kBlocks * 32 + q * 8 + (lane >> 5) * 4) =
+                *reinterpret_cast<f32x4*>(area + j / kBlocks * kArea +
+                                          placed(lane & 31, j % kBlocks * 32 + q * 8 + (lane >> 5) * 4)) =
                     (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                             acc[i][j][4 * q + 3]};
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -647,8 +651,8 @@ __device__ __forceinline__ void product_body(const ProductArgs& a, int id, char*
                 float v[C], w[C];
 #pragma unroll
                 for (int k = 0; k < C; k += 4) {
-                    const f32x4 x = *reinterpret_cast<const f32x4*>(area + r * kPitch + c + k);
-                    const f32x4 y = kPair ? *reinterpret_cast<const f32x4*>(area + kArea + r * kPitch + c + k) : x;
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(area + placed(r, c + k));
+                    const f32x4 y = kPair ? *reinterpret_cast<const f32x4*>(area + kArea + placed(r, c + k)) : x;
 #pragma unroll
                     for (int l = 0; l < 4; ++l) {
                         v[k + l] = x[l];
@@ -706,16 +710,17 @@ __global__ __launch_bounds__(WM* WN * 64) void product_kernel(const ProductArgs 
 
 // The input's gradient and the weights' in one launch, in tiles of 128: either
 // alone leaves compute units idle where the matrices are small (5467 tokens, 655
-// columns, 324 features, bf16: 23 and 22 us one after the other).
+// columns, 324 features, bf16: 23 and 22 us one after the other).  8 waves, two
+// workgroups a compute unit (2048 x 1001 x 1003 54 us in 4 waves, 47).
 template <int DT, int HOW>
-__global__ __launch_bounds__(256) void product_both_kernel(const ProductPair p) {
+__global__ __launch_bounds__(512) void product_both_kernel(const ProductPair p) {
     __shared__ __attribute__((aligned(1024))) char lds[2 * product_bytes<2, 2, 2, 2, 128, HOW>()];
     const int id = (int)blockIdx.x;
     if (id < p.first)
-        product_body<DT, kWeight, 2, 2, 2, 2, 128, 2, HOW>(
+        product_body<DT, kWeight, 4, 2, 1, 2, 128, 2, HOW>(
             p.weight, id, lds, []() -> const ProductArgs& { return args_again<ProductPair>().weight; });
     else
-        product_body<DT, kInput, 2, 2, 2, 2, 128, 2, HOW>(
+        product_body<DT, kInput, 4, 2, 1, 2, 128, 2, HOW>(
             p.input, id - p.first, lds, []() -> const ProductArgs& { return args_again<ProductPair>().input; });
 }
 
@@ -802,7 +807,7 @@ int product_both_launch(const ProductPair& p, hipStream_t stream) {
     const void* k = w.direct && x.direct ? reinterpret_cast<const void*>(product_both_kernel<DT, kDirect>)
                                          : reinterpret_cast<const void*>(product_both_kernel<DT, kHeld>);
     const uint32_t grid = (uint32_t)p.first + (uint32_t)x.tiles_m * (uint32_t)x.tiles_n * (uint32_t)x.splits;
-    if (hipLaunchKernel(k, dim3(grid), dim3(256), args, 0, stream) != hipSuccess) return kFailed;
+    if (hipLaunchKernel(k, dim3(grid), dim3(512), args, 0, stream) != hipSuccess) return kFailed;
     if (w.splits > 1 && x.splits > 1) {
         const dim3 a = product_joins(w, kWeight), b = product_joins(x, kInput);
         const dim3 both(a.x > b.x ? a.x : b.x, a.y > b.y ? a.y : b.y, 2);
@@ -847,7 +852,12 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
         } else if (a.shape == kTileShort) {
             k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kShort>);
         } else if (!a.direct) {
-            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kHeld>);
+            // 8 waves hide more of the way through registers; the weights' reads across
+            // rows, of both operands, then cost more (501 x 1003 x 2501 f16 24.0, 20.1 us;
+            // 512 x 4095 x 8193 input's gradient 132, 125, the weights' 129, 133)
+            constexpr bool kMany = KIND != kWeight;
+            threads = kMany ? 512 : 256;
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, kMany ? 4 : 2, 2, kMany ? 1 : 2, 2, 128, 2, kHeld>);
             if constexpr (DT != PTORED_F32) {
                 if (a.shape == kTile256) {
                     threads = 512;
@@ -857,7 +867,10 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
         } else if (a.shape == kTile128) {
             k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 2, kDirect>);
         } else if (a.shape == kTile128Deep) {
-            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 2, 2, 128, 4, kDirect>);
+            // one workgroup a compute unit: two waves for each of its matrix cores (512
+            // x 1536 x 4096 bf16 21.8, 20.0 us)
+            threads = 512;
+            k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 2, 1, 2, 128, 4, kDirect>);
         } else if (a.shape == kTile256) {
             threads = 512;
             if constexpr (DT == PTORED_F32) return kFailed;

@@ -94,9 +94,10 @@ struct TileCost {
     double base, alone, step;
 };
 
-TileCost tile128(int64_t half, bool f32, bool direct) {
+// many: 8 waves.
+TileCost tile128(int64_t half, bool f32, bool direct, bool many) {
     if (direct) return {kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.0, f32 ? 3.9 : 1.1};
-    return {kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : 1.15, f32 ? 3.9 : 1.35};
+    return {kTile128, 128, 128 / half, 512, 5, f32 ? 2.0 : many ? 1.0 : 1.15, f32 ? 3.9 : 1.35};
 }
 
 // Tiles and splits of a product, by estimated time; for kInput k is that of each
@@ -183,14 +184,14 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         return s;
     }
     if (direct) {
-        look(tile128(half, f32, true));
-        look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.85, f32 ? 2.0 : 0.85});
+        look(tile128(half, f32, true, false));
+        look({kTile128Deep, 128, 128 / half, 256, 4, f32 ? 2.0 : 0.75, f32 ? 2.0 : 0.75});
         if (kind != kWeight) look({kTile64x128, 64, 128 / half, 512, 5, f32 ? 1.0 : 0.6, f32 ? 2.0 : 0.9});
         if (!f32) look({kTile256, 256, 256 / half, 256, 8, 1.7, 1.7});
         if (kind == kForward && !f32) look({kTile64, 64, 32, 256, 5, 0.48, 0.48});
         if (kind == kForward) look({kTile128x32, 128, 32, 256, 5, f32 ? 1.2 : 0.56, f32 ? 1.2 : 0.56});
     } else {
-        look(tile128(half, f32, false));
+        look(tile128(half, f32, false, kind != kWeight));
         if (kind != kWeight) look({kTile64x128, 64, 128 / half, 768, 5, f32 ? 1.0 : 0.95, f32 ? 3.0 : 1.75});
         if (!f32) look({kTile256, 256, 256 / half, 256, 8, 2.1, 2.1});
     }
@@ -220,7 +221,7 @@ BothShape both_shape(int64_t rows, int64_t cols, int64_t wide, int outs, int dty
         short_rows(kWeight, wide, cols, rows, es))
         return best;
     const int64_t depth = kStepBytes / es;
-    const TileCost c = tile128(1, f32, direct);
+    const TileCost c = tile128(1, f32, direct, false);
     auto tiles = [](int64_t n) { return (n + 127) / 128; };
     const int64_t steps_in = (wide + depth - 1) / depth * 2, steps_w = (rows + depth - 1) / depth;
     const int64_t tiles_in = tiles(rows) * tiles(cols), tiles_w = tiles(wide) * tiles(cols) * outs;

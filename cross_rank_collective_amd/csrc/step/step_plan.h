@@ -76,8 +76,8 @@ struct ProductPair {
 
 // Tiles of the products.
 enum : int {
-    kTile128 = 0,      // 128 x 128, 4 waves, two workgroups a compute unit
-    kTile128Deep = 1,  // the same with loads three steps ahead, one a compute unit; aligned
+    kTile128 = 0,      // 128 x 128, 4 waves (8 where not aligned), two workgroups a compute unit
+    kTile128Deep = 1,  // 8 waves, loads three steps ahead, one a compute unit; aligned
     kTile256 = 2,      // 256 x 256, 8 waves; 16-bit types, aligned
     kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; aligned
     kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned

@@ -106,12 +106,12 @@ TileCost tile128(int64_t half, bool f32, bool direct, bool many) {
 // and the bytes at 4 TB/s.
 //
 // Measured (forward, bf16, D = 4096, F = 8192, us): 1 token 25 with kFew16, 60 in
-// tiles of 128; 32 tokens 32 with kTile64, 37 with kFew32; 64: 34, 41; 128: 37
-// with kTile128x32, 68 in tiles of 128; in tiles of 128, the same with loads
-// further ahead, and 256: 192 tokens 70, 48, 103; 512: 85, 103, 107; 1024: 159,
-// 181, 122.  Rows that do not start at multiples of 16 bytes (D = 4095, F = 8193):
-// 64 tokens 80 in tiles of 128, 157 with kFew64; 2048 tokens 460, in tiles of 256
-// 411.  In 32 bits kTile64's two waves are not enough for its products (64 tokens
+// tiles of 128; 32 tokens 32 with kTile64, 37 as kFew32 in that type; 64: 34, 41;
+// 128: 37 with kTile128x32, 68 in tiles of 128; in tiles of 128, the same with loads
+// further ahead, and 256: 192 tokens 70, 45, 103; 512: 85, 101, 107; 1024: 159,
+// 178, 122.  Rows that do not start at multiples of 16 bytes (D = 4095, F = 8193):
+// 64 tokens 80 in tiles of 128, 157 as kFew64; 2048 tokens 460, in tiles of 256
+// 400.  In 32 bits kTile64's two waves are not enough for its products (64 tokens
 // 149, kFew64 80).
 ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, int dtype,
                            bool direct) {
@@ -205,8 +205,8 @@ int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs)
 // Both gradients in one launch of tiles of 128: splits that give all workgroups
 // about the same number of steps.  Taken where its time is below 0.9 of that of two
 // launches, whose estimates are up to a fifth above what larger tiles take.  One
-// launch and two, us (with the slopes): 2048 tokens x 1024 x 1024 bf16 36, 53; 512
-// x 1001 x 1003 30, 44; 6 x 299 x 1855 18, 24; 1024 x 512 x 512 f32 39, 53; 1024 x
+// launch and two, us (with the slopes): 2048 tokens x 1024 x 1024 bf16 35, 53; 512
+// x 1001 x 1003 28, 44; 6 x 299 x 1855 17, 24; 1024 x 512 x 512 f32 39, 53; 1024 x
 // 1536 x 4096 bf16 (0.92 of the estimate) 94, 84.
 struct BothShape {
     ProductShape input, weight;

@@ -249,6 +249,33 @@ def test_gated_ffn_backward(rows, cols, wide, pad, lead, dtype):
         r.check("a gradient")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,wide", [(5, 264, 24), (5, 250, 24), (200, 264, 24), (200, 1003, 24), (64, 264, 200),
+                                            (64, 250, 200), (200, 1000, 200), (200, 1003, 511), (700, 264, 200)])
+def test_gated_ffn_both_gradients(rows, cols, wide, dtype):
+    """All gradients of one call, sums of either kind split among workgroups or not,
+    added to what is there; both weights' and one alone."""
+    x, wg, wu = ffn_inputs(rows, cols, wide, dtype)
+    g, u, dy = (rand(rows, wide, seed=s, dtype=dtype) for s in (21, 22, 23))
+    add = [rand(wide, cols, seed=24 + i) for i in range(2)]
+    exact = dtype != F32
+    on = [t.cuda() for t in (dy, g, u, x, wg, wu)]
+    for which in ((0, 1), (0,), (1,)):
+        dg, du, dx = Room(rows, wide, dtype), Room(rows, wide, dtype, 8), Room(rows, cols, dtype, 8)
+        dw = [Room(wide, cols, F32, 4, 0, add[i]) if i in which else None for i in range(2)]
+        crc.gated_ffn_backward(on[0], on[1], on[2], dg.t, du.t, x=on[3], w_gate=on[4], w_up=on[5], dx=dx.t,
+                               dw_gate=dw[0].t if dw[0] else None, dw_up=dw[1].t if dw[1] else None,
+                               accumulate=True)
+        hg, hu = dg.t.cpu(), du.t.cpu()
+        pairs = torch.cat([hg, hu], 1), torch.cat([wg, wu], 0).t()
+        close(dx.t, *R.product(*pairs, exact), "dx")
+        for i in which:
+            value, bound = R.product((hg, hu)[i].t(), x.t(), exact)
+            close(dw[i].t, value + add[i].double(), bound + R.U * (value.abs() + add[i].double().abs()), f"dw {i}")
+        for r in (dg, du, dx, *(dw[i] for i in which)):
+            r.check("a gradient")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("rows,cols,wide", [(1000, 520, 2056), (2048, 2048, 512), (520, 1032, 4096)])
 def test_gated_ffn_tiles(rows, cols, wide, dtype):

@@ -34,7 +34,9 @@ namespace step {
 
 using namespace block;
 
-__device__ __forceinline__ bool is_inf(float v) { return (as_u(v) & 0x7FFFFFFFu) == 0x7F800000u; }
+// An infinity or a NaN: what a sum is whose parts passed binary32's range, a NaN
+// where they passed it both ways.
+__device__ __forceinline__ bool past_range(float v) { return (as_u(v) & 0x7F800000u) == 0x7F800000u; }
 
 // S slots of a row per thread.
 template <int DT, int S, int EDGE>
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a)
         block_sum<1>(red[turn], sum);
         turn ^= 1;
         float m = sum[0] * b.inv_cols;
-        if (__builtin_expect(is_inf(as_f((uint32_t)__builtin_amdgcn_readfirstlane((int)as_u(sum[0])))), 0)) {
+        if (__builtin_expect(past_range(as_f((uint32_t)__builtin_amdgcn_readfirstlane((int)as_u(sum[0])))), 0)) {
             // the sum passes binary32's range where the mean may not
             sum[0] = 0.0f;
 #pragma unroll
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a)
         block_sum<2>(red[turn], sum);
         turn ^= 1;
         float c = sum[0] * b.inv_cols, var = sum[1] * b.inv_cols;
-        if (__builtin_expect(is_inf(as_f((uint32_t)__builtin_amdgcn_readfirstlane((int)as_u(sum[1])))), 0)) {
+        if (__builtin_expect(past_range(as_f((uint32_t)__builtin_amdgcn_readfirstlane((int)as_u(sum[1])))), 0)) {
             sum[0] = sum[1] = 0.0f;
 #pragma unroll
             for (int s = 0; s < S; ++s)

@@ -37,6 +37,7 @@ using namespace block;
 // An infinity or a NaN: what a sum is whose parts passed binary32's range, a NaN
 // where they passed it both ways.
 __device__ __forceinline__ bool past_range(float v) { return (as_u(v) & 0x7F800000u) == 0x7F800000u; }
+constexpr float kMost = 0x1.fffffep127f;  // binary32's
 
 // S slots of a row per thread.
 template <int DT, int S, int EDGE>
@@ -140,8 +141,15 @@ __global__ __launch_bounds__(1024) void layer_norm_kernel(const LayerNormArgs a)
                 }
             block_sum<2>(red[turn], sum);
             turn ^= 1;
-            c = sum[0];
+            // Where a difference itself passes the range there is no c: m stands as it
+            // is, and as the variance's r is 0, the range's end does for the difference.
+            c = past_range(sum[0]) ? 0.0f : sum[0];
             var = sum[1];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    v[s][i] = __builtin_fabsf(v[s][i]) > kMost ? __builtin_copysignf(kMost, v[s][i]) : v[s][i];
         }
         var -= c * c;
         var = var < 0.0f ? 0.0f : var;  // a NaN stays

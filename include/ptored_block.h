@@ -32,8 +32,10 @@
  * HIP call in the order INVALID_ARG (counts, null pointers, shapes),
  * UNSUPPORTED (types, i32 among them, or more than PTORED_BLOCK_MAX_COLS
  * columns), INVALID_ARG (the workspace, alignment), OVERLAP.  Buffers overlap
- * where their spans do, from the first byte to the last with the gaps between
- * rows: two column ranges of one matrix do.  Zero rows or columns are no error.
+ * where they share a byte: two column ranges of one matrix do not, nor does a
+ * buffer in the gaps between a matrix's rows.  Of two matrices in rows of
+ * different pitches, both with gaps, it is their spans that count, from the
+ * first byte to the last.  Zero rows or columns are no error.
  * Results do not vary from run to run.
  */
 #ifndef PTORED_BLOCK_H

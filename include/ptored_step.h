@@ -5,9 +5,10 @@
  * the column-parallel half of a gated feed-forward block, and the clipping of
  * gradients by their global norm.
  *
- * Notation, matrices (ptored_rows), status codes, element types, streams and
- * the order of argument checks are those of ptored_block.h; matrices start at
- * any element, and `ld` is any pitch of at least the columns.  Everything is
+ * Notation, matrices (ptored_rows), status codes, element types, streams, the
+ * order of argument checks and what counts as an overlap are those of
+ * ptored_block.h; matrices start at any element, and `ld` is any pitch of at
+ * least the columns: gate and up may be the halves of one buffer.  Everything is
  * computed in binary32 or more from the first load to the stores, and each
  * output is rounded once, but for what a call says.  Results do not vary from
  * run to run.

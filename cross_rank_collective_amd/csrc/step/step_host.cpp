@@ -298,9 +298,12 @@ bool grad_supported(const ptored_grad& g, bool scaled) {
     if (g.rows == 1) return g.cols < kGradMost;
     return g.rows <= kInt && g.ld <= kGradPitch && (!scaled || g.out_ld <= kGradPitch);
 }
-int64_t span_of(const ptored_grad& g, int64_t ld, int es) {
-    return (g.rows == 1 ? g.cols : (g.rows - 1) * ld + g.cols) * es;
+// Where the elements of a gradient that has some lie.
+Extent lies(const ptored_grad& g, const void* p, int64_t ld, int dtype) {
+    return extent_of(p, g.rows, g.cols, g.rows == 1 ? g.cols : ld, esize_of(dtype));
 }
+Extent data_of(const ptored_grad& g) { return lies(g, g.data, g.ld, g.dtype); }
+Extent out_of(const ptored_grad& g) { return lies(g, g.out, g.out_ld, g.out_dtype); }
 
 int64_t chunks_of(const ptored_grad& g) {
     return g.rows == 0 || g.cols == 0 ? 0 : grad_chunks(g.rows, g.cols, g.dtype);
@@ -323,7 +326,7 @@ int64_t grad_table_bytes(const ptored_grad* grads, int64_t count) {
 int64_t groups_of(int64_t chunks) { return std::min<int64_t>(chunks, kGradGroups); }
 
 struct Span {
-    uintptr_t begin, end;
+    Extent at;
     bool out;
 };
 // Whether an output among the gradients (or `more`, 2 spans) overlaps another
@@ -335,28 +338,29 @@ int grads_overlap(const ptored_grad* grads, int64_t count, const Span* more) {
     for (int64_t i = 0; i < count; ++i) {
         const ptored_grad& g = grads[i];
         if (g.rows == 0 || g.cols == 0) continue;
-        const uintptr_t p = reinterpret_cast<uintptr_t>(g.data), q = reinterpret_cast<uintptr_t>(g.out);
-        const int64_t bytes = span_of(g, g.ld, esize_of(g.dtype));
-        const bool same = p == q && g.dtype == g.out_dtype && (g.rows == 1 || g.ld == g.out_ld);
-        s[n++] = {p, p + (uintptr_t)bytes, same};
-        if (!same) s[n++] = {q, q + (uintptr_t)span_of(g, g.out_ld, esize_of(g.out_dtype)), true};
+        const bool same = g.data == g.out && g.dtype == g.out_dtype && (g.rows == 1 || g.ld == g.out_ld);
+        s[n++] = {data_of(g), same};
+        if (!same) s[n++] = {out_of(g), true};
     }
     for (int i = 0; i < 2; ++i)
-        if (more[i].end > more[i].begin) s[n++] = more[i];
-    std::sort(s.get(), s.get() + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+        if (more[i].at.bytes > 0) s[n++] = more[i];
+    std::sort(s.get(), s.get() + n, [](const Span& a, const Span& b) { return a.at.p < b.at.p; });
     uintptr_t any = 0, outs = 0;  // how far buffers, and outputs among them, reach so far
-    for (size_t i = 0; i < n; ++i) {
-        if (s[i].begin < (s[i].out ? any : outs)) return 1;
-        any = std::max(any, s[i].end);
-        if (s[i].out) outs = std::max(outs, s[i].end);
+    bool apart = true;
+    for (size_t i = 0; i < n && apart; ++i) {
+        apart = s[i].at.p >= (s[i].out ? any : outs);
+        const uintptr_t end = s[i].at.p + (uintptr_t)s[i].at.bytes;
+        any = std::max(any, end);
+        if (s[i].out) outs = std::max(outs, end);
     }
+    // spans that meet, as column ranges of one matrix do: one by one
+    for (size_t i = 0; i < n && !apart; ++i)
+        for (size_t j = i + 1; j < n && s[j].at.p < s[i].at.p + (uintptr_t)s[i].at.bytes; ++j)
+            if ((s[i].out || s[j].out) && meet(s[i].at, s[j].at)) return 1;
     return 0;
 }
 
-Span span(const void* p, int64_t bytes, bool out) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return {b, b + (uintptr_t)bytes, out};
-}
+Span span(const void* p, int64_t bytes, bool out) { return {{reinterpret_cast<uintptr_t>(p), bytes, 0, bytes}, out}; }
 
 // The checks of all three calls.  `sums`: the norm is taken.
 int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sums, const float* norm,
@@ -391,13 +395,11 @@ int grads_checked(const ptored_grad* grads, int64_t count, bool scaled, bool sum
         return over < 0 ? PTORED_ERR_HIP : over > 0 ? PTORED_ERR_OVERLAP : PTORED_OK;
     }
     // only the norm and the workspace are written
-    if (more[0].begin < more[1].end && more[1].begin < more[0].end) return PTORED_ERR_OVERLAP;
+    if (meet(more[0].at, more[1].at)) return PTORED_ERR_OVERLAP;
     for (int64_t i = 0; i < count; ++i) {
-        const ptored_grad& g = grads[i];
-        if (g.rows == 0 || g.cols == 0) continue;
-        const Span s = span(g.data, span_of(g, g.ld, esize_of(g.dtype)), false);
+        if (grads[i].rows == 0 || grads[i].cols == 0) continue;
         for (const Span& m : more)
-            if (s.begin < m.end && m.begin < s.end) return PTORED_ERR_OVERLAP;
+            if (meet(data_of(grads[i]), m.at)) return PTORED_ERR_OVERLAP;
     }
     return PTORED_OK;
 }

@@ -167,7 +167,8 @@ int ptored_grad_norm(const ptored_grad* grads, int64_t count, float* norm, void*
  * `norm` is a DEVICE pointer, read when the kernels run: it may be what an
  * all-reduce of several ranks' norms left.  c is rounded to binary32 and every
  * product once to out_dtype.  max_norm >= 0 (infinity: c = 1).  An out is its
- * data exactly (type and pitch too) or overlaps no gradient's data or out.
+ * data exactly (type and pitch too) or overlaps no gradient's data or out;
+ * column slices of one buffer do not overlap.
  */
 int ptored_grad_scale(const ptored_grad* grads, int64_t count, const float* norm, float max_norm,
                       void* workspace, int64_t workspace_bytes, hipStream_t stream);

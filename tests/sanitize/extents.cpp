@@ -2,6 +2,7 @@
 // by byte: built with AddressSanitizer and UndefinedBehaviorSanitizer by
 // tests/test_extents_cpu.py with tests/sanitize/step_stub.cpp instead of the
 // kernels; needs no GPU.
+#include <algorithm>
 #include <cstdint>
 #include <cstdio>
 #include <random>
@@ -121,6 +122,63 @@ int halves() {
     return 0;
 }
 
+// Column slices of one gradient, each scaled in place or into slices of another; one
+// a column too wide, and the call is refused.
+int slices() {
+    std::mt19937_64 rng(4);
+    for (int i = 0; i < 4000; ++i) {
+        const int count = 1 + (int)(rng() % (i % 10 ? 6 : 200));
+        const int64_t rows = 2 + (int64_t)(rng() % 5);
+        std::vector<int64_t> width((size_t)count), first((size_t)count);
+        int64_t cols = 0;
+        for (size_t k = 0; k < width.size(); ++k) {
+            cols += (int64_t)(rng() % 3);
+            first[k] = cols;
+            cols += width[k] = 1 + (int64_t)(rng() % 40);
+        }
+        const int64_t ld = cols + (int64_t)(rng() % 3);
+        const bool into = rng() % 2;
+        const int dtype = (int)(rng() % 3), es = dtype == PTORED_F32 ? 4 : 2;
+        const int out_dtype = into && rng() % 2 ? PTORED_F32 : dtype, oes = out_dtype == PTORED_F32 ? 4 : 2;
+        char *data = reinterpret_cast<char*>((uintptr_t)1 << 40), *out = reinterpret_cast<char*>((uintptr_t)2 << 40);
+        std::vector<ptored_grad> g((size_t)count + 1);
+        for (size_t k = 0; k < width.size(); ++k)
+            g[k] = {data + first[k] * es, into ? out + first[k] * oes : data + first[k] * es, rows, width[k], ld, ld,
+                    dtype, out_dtype};
+        g.back() = {nullptr, nullptr, 0, INT64_MAX / 2, INT64_MAX, INT64_MAX, dtype, dtype};  // of no rows: not read
+        std::shuffle(g.begin(), g.end(), rng);
+        int64_t need = 0;
+        EXPECT(ptored_grad_norm_workspace(g.data(), count + 1, &need) == PTORED_OK, "query");
+        void* const ws = reinterpret_cast<void*>((uintptr_t)3 << 40);
+        float* const norm = reinterpret_cast<float*>((uintptr_t)4 << 40);
+        EXPECT(ptored_grad_clip(g.data(), count + 1, 1.0f, norm, ws, need, nullptr) == PTORED_OK, "%d slices", count);
+        EXPECT(ptored_grad_norm(g.data(), count + 1, norm, ws, need, nullptr) == PTORED_OK, "%d slices", count);
+        // one reaches into the next, its last column behind the buffer's into the next row's first
+        size_t k = rng() % g.size();
+        if (g[k].rows == 0) k = (k + 1) % g.size();
+        int64_t to = ld;
+        for (const ptored_grad& e : g)
+            if (e.rows > 0 && e.data > g[k].data)
+                to = std::min(to, ((const char*)e.data - (const char*)g[k].data) / es);
+        const int64_t at = ((const char*)g[k].data - data) / es;
+        if (to == ld && (count == 1 || ld - at + first[0] >= ld)) continue;
+        g[k].cols = to == ld ? ld - at + first[0] + 1 : to + 1;
+        if (g[k].cols > ld) continue;
+        EXPECT(ptored_grad_clip(g.data(), count + 1, 1.0f, norm, ws, need + 4096, nullptr) == PTORED_ERR_OVERLAP,
+               "%d slices, one too wide", count);
+    }
+    // the norm beside a single column, and on it
+    float* const m = reinterpret_cast<float*>((uintptr_t)1 << 40);
+    const ptored_grad column{m, m, 9, 1, 4, 4, PTORED_F32, PTORED_F32};
+    void* const ws = reinterpret_cast<void*>((uintptr_t)3 << 40);
+    for (int k = 0; k < 8; ++k) {
+        const int want = k % 4 ? PTORED_OK : PTORED_ERR_OVERLAP;
+        EXPECT(ptored_grad_clip(&column, 1, 1.0f, m + k, ws, 64, nullptr) == want, "norm at %d", k);
+        EXPECT(ptored_grad_norm(&column, 1, m + k, ws, 64, nullptr) == want, "norm at %d", k);
+    }
+    return 0;
+}
+
 }  // namespace
 
-int main() { return pairs() || halves() ? 1 : (std::printf("ok\n"), 0); }
+int main() { return pairs() || halves() || slices() ? 1 : (std::printf("ok\n"), 0); }

@@ -123,3 +123,26 @@ def test_a_column_that_is_shared_is_refused():
         crc.layer_norm([], x, room[:, :20], room[:, 19:39])
     with pytest.raises(crc.PtoredError, match="(?i)overlap"):  # rows that run into the next ones
         crc.layer_norm([], room[:, 30:].as_strided((5, 20), (40, 1), 30), room[:5, :20], None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,many", [(5, 3, 2), (64, 131, 3), (300, 40, 90), (7, 1000, 4)])
+def test_clipping_of_column_slices(rows, cols, many, dtype):
+    """Slices of one fused gradient, clipped in place and into slices of another."""
+    fused = rand(rows, many * cols, seed=1, dtype=dtype).cuda()
+    # each in a buffer of its own, in rows that lie as the slices do
+    parts = [fused.clone()[:, i * cols:(i + 1) * cols] for i in range(many)]
+    norm, want = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    crc.grad_clip(parts, 1.0, want)
+    for out_type in {dtype, torch.float32}:
+        into = torch.full((rows, many * cols + 2), 7.0, dtype=out_type, device="cuda")
+        outs = [into[:, 1 + i * cols:1 + (i + 1) * cols] for i in range(many)]
+        crc.grad_clip(list(fused.split(cols, 1)), 1.0, norm, outs=outs)
+        assert torch.equal(norm, want)
+        for o, p in zip(outs, parts):
+            assert torch.equal(o.to(dtype), p)
+        assert bool((into[:, 0] == 7).all() and (into[:, -1] == 7).all())
+    crc.grad_clip(list(fused.split(cols, 1)), 1.0, norm)
+    assert torch.equal(norm, want) and torch.equal(fused, torch.cat(parts, 1))
+    with pytest.raises(crc.PtoredError, match="(?i)overlap"):
+        crc.grad_clip([fused[:, :cols + 1], fused[:, cols:]], 1.0, norm)

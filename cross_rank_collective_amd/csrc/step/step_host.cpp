@@ -705,16 +705,18 @@ extern "C" int ptored_gated_ffn_backward(const ptored_ffn_params* params,
         return PTORED_ERR_INVALID_ARG;
     if (!ffn_supported(p) || (outs > 0 && io->dw_dtype != PTORED_F32 && io->dw_dtype != p.dtype))
         return PTORED_ERR_UNSUPPORTED;
-    if (!widths_supported(p, es) || !pitch_supported(io->dgate, p.rows, es) || !pitch_supported(io->dup, p.rows, es) ||
-        !pitch_supported(x, p.rows, es) || !pitch_supported(wg, p.wide, es) ||
-        !pitch_supported(wu, p.wide, es))
+    // what a product reads; the slopes alone have no limits
+    if ((input || outs > 0) &&
+        (!widths_supported(p, es) || !pitch_supported(io->dgate, p.rows, es) || !pitch_supported(io->dup, p.rows, es) ||
+         !pitch_supported(x, p.rows, es) || !pitch_supported(wg, p.wide, es) || !pitch_supported(wu, p.wide, es)))
         return PTORED_ERR_UNSUPPORTED;
     const bool whole = direct_of(io->dgate, p.rows, p.wide, es) && direct_of(io->dup, p.rows, p.wide, es);
     const bool direct_in = whole && direct_of(wg, p.wide, p.cols, es) && direct_of(wu, p.wide, p.cols, es);
     const bool direct_w = whole && direct_of(x, p.rows, p.cols, es);
-    const ProductShape si = product_shape(kInput, p.rows, p.cols, p.wide, 1, p.dtype, direct_in);
+    const ProductShape si =
+        input ? product_shape(kInput, p.rows, p.cols, p.wide, 1, p.dtype, direct_in) : ProductShape{};
     const ProductShape sw =
-        product_shape(kWeight, p.wide, p.cols, p.rows, std::max(outs, 1), p.dtype, direct_w);
+        outs > 0 ? product_shape(kWeight, p.wide, p.cols, p.rows, outs, p.dtype, direct_w) : ProductShape{};
     if ((input && !launchable(si, 1)) || (outs > 0 && !launchable(sw, outs)))
         return PTORED_ERR_UNSUPPORTED;
     const bool direct_both = direct_in && direct_w;

@@ -86,7 +86,7 @@ typedef enum ptored_activation {
 } ptored_activation;
 
 /* Longest rows (D and F) and largest pitch of the matrices that its products read,
- * in bytes; more is UNSUPPORTED. */
+ * in bytes; more is UNSUPPORTED.  dg and du alone are not products. */
 #define PTORED_FFN_MAX_PITCH (1 << 22)
 
 typedef struct ptored_ffn_params {

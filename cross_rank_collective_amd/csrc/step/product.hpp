@@ -838,9 +838,15 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
         if (rc != kOk) return rc;
     } else {
         if (a.shape == kTile32x128) {
-            if constexpr (KIND != kInput) return kFailed;
-            else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 4, kDirect>)
-                              : reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 2, kHeld>);
+            if constexpr (KIND == kInput) {
+                k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 2, kHeld>);
+                if (a.direct) {
+                    if constexpr (DT != PTORED_F32) return kFailed;
+                    else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 1, 4, 1, 1, 128, 4, kDirect>);
+                }
+            } else {
+                return kFailed;
+            }
         } else if (a.shape == kTile64x128) {
             if constexpr (KIND == kWeight) return kFailed;
             else k = a.direct ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 2, 1, 2, 128, 3, kDirect>)
@@ -875,13 +881,13 @@ int product_launch(const ProductArgs& a, hipStream_t stream) {
             threads = 512;
             if constexpr (DT == PTORED_F32) return kFailed;
             else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 4, 4, 2, 128, 2, kDirect>);
-        } else if constexpr (KIND == kForward) {
-            if (a.shape == kTile64) threads = 128;
-            k = a.shape == kTile64
-                    ? reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, kDirect>)
-                    : reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, kDirect>);
+        } else if (a.shape == kTile64) {
+            threads = 128;
+            if constexpr (KIND != kForward || DT == PTORED_F32) return kFailed;
+            else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 2, 1, 1, 2, 128, 8, kDirect>);
         } else {
-            return kFailed;
+            if constexpr (KIND != kForward) return kFailed;
+            else k = reinterpret_cast<const void*>(product_kernel<DT, KIND, 4, 1, 1, 2, 128, 6, kDirect>);
         }
         const uint32_t grid = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n * (uint32_t)(a.outs * a.splits);
         if (hipLaunchKernel(k, dim3(grid), dim3((uint32_t)threads), args, 0, stream) != hipSuccess)

@@ -196,7 +196,8 @@ ProductShape product_shape(int kind, int64_t m, int64_t n, int64_t k, int outs, 
         if (!f32) look({kTile256, 256, 256 / half, 256, 8, 2.1, 2.1});
     }
     if (f32) look({kTileSplit, 256, 128 / half, 256, 8, 2.3, 2.3});
-    if (kind == kInput) look({kTile32x128, 32, 128, 512, 5, f32 ? 0.7 : 0.6, f32 ? 1.1 : 0.9});
+    // (16 bits, aligned: a step takes as long as one of 64 x 128)
+    if (kind == kInput && (f32 || !direct)) look({kTile32x128, 32, 128, 512, 5, f32 ? 0.7 : 0.6, f32 ? 1.1 : 0.9});
     return s;
 }
 int64_t product_workspace(const ProductShape& s, int64_t m, int64_t n, int outs) {

@@ -79,9 +79,9 @@ enum : int {
     kTile128 = 0,      // 128 x 128, 4 waves (8 where not aligned), two workgroups a compute unit
     kTile128Deep = 1,  // 8 waves, loads three steps ahead, one a compute unit; aligned
     kTile256 = 2,      // 256 x 256, 8 waves; 16-bit types, aligned
-    kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; aligned
+    kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; 16-bit types, aligned
     kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned
-    kTile32x128 = 5,   // kInput: 32 tokens x 128 columns, 4 waves
+    kTile32x128 = 5,   // kInput: 32 tokens x 128 columns, 4 waves; F32, and 16-bit types where not aligned
     kTile64x128 = 6,   // 64 x 128, 4 waves, two or (not aligned) three workgroups a compute unit
     kTileSplit = 7,    // 256 x 128, 8 waves, F32 as three bfloat16
     kTileShort = 8,    // 128 x 128, 4 waves, rows that do not hold 16 bytes

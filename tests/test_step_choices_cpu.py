@@ -1,5 +1,6 @@
 """The kernels of the feed-forward block that the host code takes, on the CPU:
-every compiled one is reached by some call (``tests/sanitize/step_choices.cpp``)."""
+every compiled one is reached by some call, and by one that the GPU tests make
+(``tests/sanitize/step_choices.cpp``)."""
 
 import os
 import re
@@ -7,6 +8,8 @@ import shutil
 import subprocess
 
 import pytest
+
+from tests.step_sizes import CASES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "cross_rank_collective_amd")
@@ -45,3 +48,13 @@ def test_every_kernel_that_is_built_is_reached(reached):
     built = set(re.findall(r"\b((?:few|product(?:_both)?(?:_join)?)_kernel<[^>]*>)\(", symbols))
     assert len(built) > 50
     assert built == set(reached)
+
+
+def test_gpu_tests_take_every_kernel(program, reached):
+    lines = [f"{dtype} {t} {d} {f} {pad} {call}\n" for bits, t, d, f, pad, call in CASES
+             for dtype in ((0,) if bits == 32 else (1, 2))]
+    res = subprocess.run([program, "cases"], input="".join(lines), capture_output=True, text=True, check=True)
+    taken = [set(line.split("; ")) for line in res.stdout.splitlines()]
+    assert len(taken) == len(lines) and all(all(k) for k in taken)
+    missing = {k: c for k, c in reached.items() if not any(k in t for t in taken)}
+    assert not missing, missing

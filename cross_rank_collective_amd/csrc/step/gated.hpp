@@ -23,8 +23,10 @@ using namespace block;
 // since (1 + tanh(t)) / 2 is that of 2t.
 //
 // For 16-bit types the logistic function is the hardware's 2^v and reciprocal:
-// off by some (4 + 2 |v|) 2^-24, where the type rounds by 2^-9 or 2^-12, and 3%
-// off the whole forward pass of 2048 tokens (235 -> 226 us).
+// off by some (4 + 2 |v|) 2^-24 (v's product with log2(e) is rounded), at most
+// 2^-16, where the type rounds by 2^-8 or 2^-11, and 3% off the whole forward pass
+// of 2048 tokens (235 -> 226 us).  In either form it is 0 where it would be below
+// 2^-128, and may be below 2^-126.
 template <int DT>
 __device__ __forceinline__ float logistic(float v) {
     if constexpr (DT == PTORED_F32)

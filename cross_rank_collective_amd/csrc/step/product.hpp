@@ -29,11 +29,12 @@
 // the matrix instructions for F32, 2.7 times fewer of their cycles.
 //
 // Large products are bound by the matrix cores, at the clock that the card's power
-// leaves them: 62% busy at 1.7 GHz, no bank conflicts.  bf16, us (and the vendor's
+// leaves them: 62% busy at 1.7 GHz, bank conflicts 1% of the forward pass's cycles,
+// where its blocks are turned, and none of the gradients'.  bf16, us (and the vendor's
 // library's product of the same sizes, without activations): forward, 4096 tokens,
-// 4096 columns, 2 x 12288 features 593-640, 1.29-1.39 PFLOP/s (631); 8192 tokens,
-// 4096 columns, 8192 features: input's gradient 880 (891), the weights' 880
-// (1012).  Measured and not taken: four waves of 128 x 128 (829 TFLOP/s where
+// 4096 columns, 2 x 12288 features 593-640, 1.29-1.39 PFLOP/s (631), 2 x 4096 217
+// (172); 8192 tokens, 4096 columns, 8192 features: input's gradient 880 (891), the
+// weights' 880 (1012).  Measured and not taken: four waves of 128 x 128 (829 TFLOP/s where
 // eight of 128 x 64 reach 1100), steps of 64 bytes in rings of 4 or 5, waves'
 // priorities (slower, both), a load between any two products (no gain).
 // F32, gradients of 1024 tokens, 1536 columns, 4096 features: 461 us with F32's

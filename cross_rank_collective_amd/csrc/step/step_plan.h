@@ -76,9 +76,10 @@ struct ProductPair {
 
 // Tiles of the products.
 enum : int {
-    kTile128 = 0,      // 128 x 128, 4 waves (8 where not aligned), two workgroups a compute unit
+    kTile128 = 0,      // 128 x 128, 4 waves, two workgroups a compute unit (8 waves where not
+                       // aligned, but for kWeight alone, and in launches of both gradients)
     kTile128Deep = 1,  // 8 waves, loads three steps ahead, one a compute unit; aligned
-    kTile256 = 2,      // 256 x 256, 8 waves; 16-bit types, aligned
+    kTile256 = 2,      // 256 x 256, 8 waves; 16-bit types
     kTile64 = 3,       // kForward: 64 tokens x 32 features, 2 waves; 16-bit types, aligned
     kTile128x32 = 4,   // kForward: 128 tokens x 32 features, 4 waves; aligned
     kTile32x128 = 5,   // kInput: 32 tokens x 128 columns, 4 waves; F32, and 16-bit types where not aligned

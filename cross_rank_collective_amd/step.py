@@ -266,8 +266,9 @@ def gated_ffn(x, w_gate, w_up, y, *, activation: str = "silu", gate=None, up=Non
 
     ``x`` is [T, D], ``w_gate`` and ``w_up`` [F, D] and ``y`` [T, F], of one
     floating type; f is "silu", "gelu" (by the error function) or "gelu_tanh".
-    ``gate`` and ``up`` ([T, F], of that type) are given the two projections, for
-    the backward pass.  Sums are in float32 and f takes them unrounded.
+    ``gate`` and ``up`` ([T, F], of that type; the halves of one [T, 2F] tensor, if
+    wanted) are given the two projections, for the backward pass.  Sums are in
+    float32 and f takes them unrounded.
     """
     code = _activation_code(activation)
     if K._native_call("gated_ffn", stream, x, w_gate, w_up, y, code, gate, up, workspace):

@@ -27,6 +27,7 @@ extern "C" {
  *     x' = x + y_0 + ... + y_{N-1}                the N ranks' partial outputs
  *     m  = mean_d(x'),  r = 1/sqrt(mean_d((x' - m)^2) + eps)
  *     z  = (x' - m) r w + b
+ * A row whose variance passes binary32's range has r = 0.
  */
 typedef struct ptored_layer_norm_params {
     int64_t rows, cols;   /* T, D; D <= PTORED_BLOCK_MAX_COLS */
